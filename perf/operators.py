@@ -226,7 +226,8 @@ def _run_own(s):
         if "workspace" not in s:
             n, v = s["logits"].shape
             s["workspace"] = torch.empty(
-                gdn.gdn_token_logprobs_workspace_size(n, v, s["case"]["k"], s["logits"].dtype),
+                gdn.gdn_token_logprobs_workspace_size(n, v, s["case"]["k"],
+                                                      dtype=s["logits"].dtype),
                 dtype=torch.uint8, device="cuda")
         gdn.gdn_token_logprobs(s["logits"], s["targets"], s["logprobs"], s["entropy"],
                                top_ids=s["top_ids"], top_logprobs=s["top_logprobs"],
