@@ -21,6 +21,7 @@ HEAD_DIM = 128
 
 GDN_OK = 0
 GDN_F32, GDN_BF16 = 0, 1
+GDN_KV_BF16, GDN_KV_E4M3 = 0, 1
 STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARGUMENT", 2: "GDN_ERR_UNSUPPORTED",
                 3: "GDN_ERR_WORKSPACE", 4: "GDN_ERR_CUDA", 5: "GDN_ERR_DEVICE_TIMEOUT",
                 6: "GDN_ERR_DEVICE_INDEX"}
@@ -30,7 +31,9 @@ EXPORTED = ("gdn_prefill_workspace_size", "gdn_chunk_prefill", "gdn_decode_step"
             "gdn_chunk_prefill_snapshots", "gdn_chunk_prefill_gated", "gdn_decode_step_gated",
             "gdn_prefill_varlen_workspace_size", "gdn_chunk_prefill_varlen", "gdn_decode_multi",
             "gdn_get_device_error", "gdn_status_string", "gdn_version",
-            "gdn_selftest_device_timeout", "gdn_chunk_prefill_ex")
+            "gdn_selftest_device_timeout", "gdn_chunk_prefill_ex",
+            "gdn_kv_cache_append", "gdn_kv_cache_read", "gdn_prefix_attention_workspace_size",
+            "gdn_prefix_attention", "gdn_token_logprobs_workspace_size", "gdn_token_logprobs")
 NOALLOC_SCRATCH_BYTES = 64 << 20   # GDN_NOALLOC_SCRATCH_BYTES in include/gdn.h
 
 
@@ -63,6 +66,13 @@ class GdnPrefillExt(ctypes.Structure):
                 ("snap_state", ctypes.c_void_p), ("snap_conv_state", ctypes.c_void_p),
                 ("num_snap_slots", ctypes.c_int32), ("snap_slots", ctypes.c_void_p),
                 ("prev_workspace", ctypes.c_void_p)]
+
+
+class GdnKvCache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("format", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p)]
 
 
 _vp = ctypes.c_void_p
@@ -111,6 +121,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.gdn_state_checkpoint.restype = ctypes.c_int
     L.gdn_state_checkpoint.argtypes = ([ctypes.c_int32, dp, ctypes.c_int] + [_vp] * 4 +
                                        [ctypes.c_int32, _vp, _vp, ctypes.c_int32, _vp])
+    i32, i64, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    cp = ctypes.POINTER(GdnKvCache)
+    L.gdn_kv_cache_append.restype = ctypes.c_int
+    L.gdn_kv_cache_append.argtypes = [cp, i32, ctypes.c_int, _vp, i64, _vp, i64, _vp, _vp]
+    L.gdn_kv_cache_read.restype = ctypes.c_int
+    L.gdn_kv_cache_read.argtypes = [cp, i32, _vp, ctypes.c_int, _vp, _vp, _vp]
+    L.gdn_prefix_attention_workspace_size.restype = sz
+    L.gdn_prefix_attention_workspace_size.argtypes = [i32] * 5
+    L.gdn_prefix_attention.restype = ctypes.c_int
+    L.gdn_prefix_attention.argtypes = ([cp] + [i32] * 3 + [_vp, i64, _vp, i32, _vp, i32, _vp,
+                                       ctypes.c_float, ctypes.c_int] + [_vp] * 3 + [sz, _vp])
+    L.gdn_token_logprobs_workspace_size.restype = sz
+    L.gdn_token_logprobs_workspace_size.argtypes = [i32, i32, ctypes.c_int, i32]
+    L.gdn_token_logprobs.restype = ctypes.c_int
+    L.gdn_token_logprobs.argtypes = ([i32, i32, ctypes.c_int, _vp, i64, _vp, ctypes.c_float, _vp,
+                                      _vp, i32] + [_vp] * 3 + [sz, _vp])
     L.gdn_get_device_error.restype = ctypes.c_int
     L.gdn_get_device_error.argtypes = [_vp]
     L.gdn_selftest_device_timeout.restype = ctypes.c_int
@@ -604,6 +630,186 @@ def gdn_state_checkpoint(op: str, state, conv_state, slot_state, slot_conv_state
                                 _ptr(slot_state), _ptr(slot_conv_state), nb, _ptr(rows),
                                 _ptr(slots), n, _stream(stream))
     _check(st, "gdn_state_checkpoint")
+
+
+# ---------------------------------------------------------------- full-attention layers
+
+def _kv_cache(k_cache, v_cache, k_exp, v_exp) -> GdnKvCache:
+    """The C struct of a paged cache [num_pages, H, page_size, D]: bf16, or float8_e4m3fn codes
+    with uint8 exponents [num_pages, H, page_size]."""
+    if k_cache.device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache: shape {tuple(k_cache.shape)}, expected 4 dimensions")
+    if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError(f"k_cache: dtype {k_cache.dtype}, expected bfloat16 or float8_e4m3fn")
+    dev, shape = k_cache.device, tuple(k_cache.shape)
+    _need(k_cache, "k_cache", shape, k_cache.dtype, dev)
+    _need(v_cache, "v_cache", shape, k_cache.dtype, dev)
+    fmt = GDN_KV_BF16
+    if k_cache.dtype == torch.float8_e4m3fn:
+        fmt = GDN_KV_E4M3
+        _need(k_exp, "k_exp", shape[:3], torch.uint8, dev)
+        _need(v_exp, "v_exp", shape[:3], torch.uint8, dev)
+    elif k_exp is not None or v_exp is not None:
+        raise ValueError("a bf16 cache has no exponents: k_exp and v_exp must be None")
+    pages, heads, page_size, d = shape
+    return GdnKvCache(pages, page_size, heads, d, fmt, _ptr(k_cache), _ptr(v_cache),
+                      _ptr(k_exp), _ptr(v_exp))
+
+
+def _token_stride(t: torch.Tensor, name: str, shape, dtype, device) -> int:
+    """The token stride (elements) of t [..., H, D], whose heads are dense and whose leading
+    dimensions lie one token after the other."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    H, D = shape[-2:]
+    if (D > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != D):
+        raise ValueError(f"{name}: the last two dimensions must be dense")
+    lead, stride = [(n, s) for n, s in zip(t.shape[:-2], t.stride()[:-2]) if n > 1], H * D
+    if lead:
+        stride = lead[-1][1]
+        for (_, s), (n, inner) in zip(lead[:-1], lead[1:]):
+            if s != n * inner:
+                raise ValueError(f"{name}: tokens must lie at one stride")
+    return stride
+
+
+def gdn_kv_cache_append(k, v, k_cache, v_cache, slots, *, k_exp=None, v_exp=None,
+                        stream=None) -> None:
+    """Write n tokens' keys and values k, v [n, H, D] (bf16 or fp32; slices of wider rows are
+    fine) to their ``slots`` [n] of the paged cache k_cache, v_cache [num_pages, H, page_size,
+    D]: bf16, or float8_e4m3fn with k_exp, v_exp (see gdn_kv_cache_append in include/gdn.h)."""
+    L = load_library()
+    c = _kv_cache(k_cache, v_cache, k_exp, v_exp)
+    n, dev = slots.shape[0], k_cache.device
+    shape = (n, c.num_kv_heads, c.head_dim)
+    _need(slots, "slots", (n,), torch.int32, dev)
+    dt = _dt(k)
+    ks = _token_stride(k, "k", shape, k.dtype, dev)
+    vs = _token_stride(v, "v", shape, k.dtype, dev)
+    st = L.gdn_kv_cache_append(ctypes.byref(c), n, dt, _ptr(k), ks, _ptr(v), vs, _ptr(slots),
+                               _stream(stream))
+    _check(st, "gdn_kv_cache_append")
+
+
+def gdn_kv_cache_read(k_cache, v_cache, slots, k_out, v_out, *, k_exp=None, v_exp=None,
+                      stream=None):
+    """Gather ``slots`` [n] of the cache into k_out, v_out [n, H, D] (bf16 or fp32); negative
+    slots read as zeros.  Returns (k_out, v_out)."""
+    L = load_library()
+    c = _kv_cache(k_cache, v_cache, k_exp, v_exp)
+    n, dev = slots.shape[0], k_cache.device
+    _need(slots, "slots", (n,), torch.int32, dev)
+    dt = _dt(k_out)
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        _need(t, name, (n, c.num_kv_heads, c.head_dim), k_out.dtype, dev)
+    st = L.gdn_kv_cache_read(ctypes.byref(c), n, _ptr(slots), dt, _ptr(k_out), _ptr(v_out),
+                             _stream(stream))
+    _check(st, "gdn_kv_cache_read")
+    return k_out, v_out
+
+
+def gdn_prefix_attention_workspace_size(batch: int, seqlen: int, num_heads: int,
+                                        num_kv_heads: int, head_dim: int) -> int:
+    return int(load_library().gdn_prefix_attention_workspace_size(batch, seqlen, num_heads,
+                                                                  num_kv_heads, head_dim))
+
+
+def gdn_prefix_attention(q, k_cache, v_cache, out, *, pages, kv_len, prefix_pages=None,
+                         prefix_len: int = 0, k_exp=None, v_exp=None,
+                         scale: Optional[float] = None, lse=None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of T new tokens of each of B sequences that share a prefix (see
+    gdn_prefix_attention in include/gdn.h).  q [B, T, Hq, D] bf16, the cache as in
+    gdn_kv_cache_append, prefix_pages [>= ceil(prefix_len / page_size)], pages [B, max_pages],
+    kv_len [B] (own tokens, the T new ones included), out [B, T, Hq, D] bf16 or fp32, lse
+    [B, T, Hq] fp32 or None; scale defaults to 1 / sqrt(D).  Returns ``out``."""
+    L = load_library()
+    c = _kv_cache(k_cache, v_cache, k_exp, v_exp)
+    if q.dim() != 4:
+        raise ValueError(f"q: shape {tuple(q.shape)}, expected 4 dimensions")
+    B, T, Hq, D = q.shape
+    dev = k_cache.device
+    qs = _token_stride(q, "q", (B, T, Hq, c.head_dim), torch.bfloat16, dev)
+    dt = _dt(out)
+    _need(out, "out", (B, T, Hq, D), out.dtype, dev)
+    if pages.dim() != 2:
+        raise ValueError(f"pages: shape {tuple(pages.shape)}, expected (B, max_pages)")
+    _need(pages, "pages", (B, pages.shape[1]), torch.int32, dev)
+    _need(kv_len, "kv_len", (B,), torch.int32, dev)
+    if prefix_len < 0:
+        raise ValueError("prefix_len must not be negative")
+    if prefix_len:
+        if prefix_pages is None:
+            raise ValueError("prefix_pages is required")
+        _need(prefix_pages, "prefix_pages", (prefix_pages.numel(),), torch.int32, dev)
+        if prefix_pages.numel() * c.page_size < prefix_len:
+            raise ValueError("prefix_pages holds fewer tokens than prefix_len")
+    if lse is not None:
+        _need(lse, "lse", (B, T, Hq), torch.float32, dev)
+    need = int(L.gdn_prefix_attention_workspace_size(B, T, Hq, c.num_kv_heads, D))
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = L.gdn_prefix_attention(ctypes.byref(c), B, T, Hq, _ptr(q), qs, _ptr(prefix_pages),
+                                int(prefix_len), _ptr(pages), pages.shape[1], _ptr(kv_len),
+                                float(D ** -0.5 if scale is None else scale), dt, _ptr(out),
+                                _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream))
+    _check(st, "gdn_prefix_attention")
+    return out
+
+
+def gdn_token_logprobs_workspace_size(rows: int, vocab: int, top_k: int = 0,
+                                      dtype=torch.bfloat16) -> int:
+    dt = GDN_BF16 if dtype == torch.bfloat16 else GDN_F32
+    return int(load_library().gdn_token_logprobs_workspace_size(rows, vocab, dt, top_k))
+
+
+def gdn_token_logprobs(logits, targets, logprobs, entropy=None, *, top_ids=None,
+                       top_logprobs=None, scale: float = 1.0,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Log probabilities of ``targets`` [N] (int32; negative: none, 0 is written) under logits
+    [N, V] (bf16 or fp32, rows may be slices of wider ones), the rows' ``entropy`` [N] and, with
+    top_ids int32 / top_logprobs fp32 [N, k], the k most likely tokens (see gdn_token_logprobs
+    in include/gdn.h).  ``targets`` and ``logprobs`` may both be None."""
+    L = load_library()
+    if logits.dim() != 2:
+        raise ValueError(f"logits: shape {tuple(logits.shape)}, expected (N, V)")
+    dev = logits.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    N, V = logits.shape
+    dt = _dt(logits)
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("logits: rows must be dense")
+    if (targets is None) != (logprobs is None):
+        raise ValueError("targets and logprobs go together")
+    if targets is not None:
+        _need(targets, "targets", (N,), torch.int32, dev)
+        _need(logprobs, "logprobs", (N,), torch.float32, dev)
+    if entropy is not None:
+        _need(entropy, "entropy", (N,), torch.float32, dev)
+    k = 0
+    if top_ids is not None or top_logprobs is not None:
+        if top_ids is None or top_logprobs is None:
+            raise ValueError("top_ids and top_logprobs go together")
+        k = top_ids.shape[1] if top_ids.dim() == 2 else -1
+        _need(top_ids, "top_ids", (N, k), torch.int32, dev)
+        _need(top_logprobs, "top_logprobs", (N, k), torch.float32, dev)
+    need = int(L.gdn_token_logprobs_workspace_size(N, V, dt, k))
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = L.gdn_token_logprobs(N, V, dt, _ptr(logits), logits.stride(0) if N > 1 else V,
+                              _ptr(targets), float(scale), _ptr(logprobs), _ptr(entropy), k,
+                              _ptr(top_ids), _ptr(top_logprobs), _ptr(workspace), ws_bytes,
+                              _stream(stream))
+    _check(st, "gdn_token_logprobs")
 
 
 def gdn_get_device_error(stream=None) -> int:

@@ -249,6 +249,54 @@ cudaError_t gdn_launch_gated_norm_f32(float* out, const float* z, const float* w
                                       int num_slots, cudaStream_t stream,
                                       const int32_t* cu = nullptr, int Hv = 0);
 
+// ----------------------------------------------------------------- full-attention layers
+
+// A paged key/value cache: k, v [num_pages][H][page][D] in bf16, or (f8) e4m3 codes with biased
+// scale exponents k_exp, v_exp [num_pages][H][page]; page = 1 << page_shift tokens.
+struct GdnKvCacheArgs {
+  int num_pages, page_shift, H, D, f8;
+  void* k; void* v;
+  uint8_t* k_exp; uint8_t* v_exp;
+};
+
+cudaError_t gdn_launch_kv_append(const GdnKvCacheArgs& c, int n, int in_bf16, const void* k,
+                                 long long k_stride, const void* v, long long v_stride,
+                                 const int32_t* slots, cudaStream_t stream);
+cudaError_t gdn_launch_kv_read(const GdnKvCacheArgs& c, int n, const int32_t* slots, int out_bf16,
+                               void* k_out, void* v_out, cudaStream_t stream);
+
+// Attention of B sequences of T new tokens (Hq query heads) to a shared prefix and their own
+// cached tokens.
+struct GdnAttnArgs {
+  GdnKvCacheArgs cache;
+  int B, T, Hq, prefix_len, max_pages, out_bf16;
+  float scale;
+  const void* q;              // [B T][Hq][D] bf16, tokens q_stride elements apart
+  long long q_stride;
+  const int32_t* prefix_pages;
+  const int32_t* pages;       // [B][max_pages]
+  const int32_t* kv_len;      // [B]
+  void* out;                  // [B T][Hq][D]
+  float* lse;                 // [B T][Hq] or NULL
+  void* workspace;
+};
+size_t gdn_prefix_attention_bytes(int B, int T, int Hq, int H, int D);
+cudaError_t gdn_launch_prefix_attention(const GdnAttnArgs& a, cudaStream_t stream);
+
+// Log probabilities of given tokens, entropy, top alternatives of N rows of V logits.
+struct GdnLogprobArgs {
+  int N, V, bf16, top_k;
+  float scale;
+  const void* logits;
+  long long row_stride;
+  const int32_t* targets;
+  float* logprobs; float* entropy;
+  int32_t* top_ids; float* top_logprobs;
+  void* workspace;
+};
+size_t gdn_token_logprobs_bytes(int N, int V, int bf16, int top_k);
+cudaError_t gdn_launch_token_logprobs(const GdnLogprobArgs& a, cudaStream_t stream);
+
 // Per-translation-unit device error words: read and clear (host side, synchronous copy).
 unsigned gdn_take_error_decode();
 unsigned gdn_take_error_conv();
@@ -257,3 +305,6 @@ unsigned gdn_take_error_prefill_simt();
 unsigned gdn_take_error_prefill_tc();
 unsigned gdn_take_error_varlen();
 unsigned gdn_take_error_decode_multi();
+unsigned gdn_take_error_kv_cache();
+unsigned gdn_take_error_prefix_attention();
+unsigned gdn_take_error_logprobs();

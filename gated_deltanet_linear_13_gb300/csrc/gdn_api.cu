@@ -528,6 +528,167 @@ gdn_status gdn_state_checkpoint(int32_t op, const gdn_dims* dims, gdn_dtype conv
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+// The cache struct, checked; out gets the kernels' form of it.
+static gdn_status check_kv_cache(const gdn_kv_cache* c, GdnKvCacheArgs* out) {
+  if (!c || c->num_pages < 0 || c->num_kv_heads < 1 || c->page_size < 1 || c->head_dim < 1)
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (c->format != GDN_KV_BF16 && c->format != GDN_KV_E4M3) return GDN_ERR_INVALID_ARGUMENT;
+  if (c->head_dim != 128 && c->head_dim != 256) return GDN_ERR_UNSUPPORTED;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return GDN_ERR_UNSUPPORTED;
+  // rows of one head's tokens are counted in 32 bits
+  if ((long long)c->num_pages * c->page_size * c->num_kv_heads > 0x7fffffffLL)
+    return GDN_ERR_UNSUPPORTED;
+  const bool f8 = c->format == GDN_KV_E4M3;
+  if (c->num_pages > 0 &&
+      (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v) || (f8 && (!c->k_exp || !c->v_exp))))
+    return GDN_ERR_INVALID_ARGUMENT;
+  out->num_pages = c->num_pages;
+  out->page_shift = __builtin_ctz((unsigned)c->page_size);
+  out->H = c->num_kv_heads;
+  out->D = c->head_dim;
+  out->f8 = f8;
+  out->k = c->k; out->v = c->v; out->k_exp = c->k_exp; out->v_exp = c->v_exp;
+  return GDN_OK;
+}
+
+static bool is_dtype(gdn_dtype t) { return t == GDN_F32 || t == GDN_BF16; }
+
+gdn_status gdn_kv_cache_append(const gdn_kv_cache* cache, int32_t n, gdn_dtype in_dtype,
+                               const void* k, int64_t k_token_stride, const void* v,
+                               int64_t v_token_stride, const int32_t* slots, void* stream) {
+  GdnKvCacheArgs c;
+  const gdn_status st = check_kv_cache(cache, &c);
+  if (st != GDN_OK) return st;
+  if (n < 0 || !is_dtype(in_dtype)) return GDN_ERR_INVALID_ARGUMENT;
+  if (n == 0) return GDN_OK;
+  if (!k || !v || !aligned16(k) || !aligned16(v) || !slots || !aligned4(slots))
+    return GDN_ERR_INVALID_ARGUMENT;
+  const int64_t row = (int64_t)c.H * c.D, per16 = 16 / (int64_t)elem_bytes(in_dtype);
+  if (k_token_stride < row || v_token_stride < row || k_token_stride % per16 ||
+      v_token_stride % per16)
+    return GDN_ERR_INVALID_ARGUMENT;
+  return gdn_launch_kv_append(c, n, in_dtype == GDN_BF16, k, k_token_stride, v, v_token_stride,
+                              slots, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? GDN_OK
+             : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_kv_cache_read(const gdn_kv_cache* cache, int32_t n, const int32_t* slots,
+                             gdn_dtype out_dtype, void* k_out, void* v_out, void* stream) {
+  GdnKvCacheArgs c;
+  const gdn_status st = check_kv_cache(cache, &c);
+  if (st != GDN_OK) return st;
+  if (n < 0 || !is_dtype(out_dtype)) return GDN_ERR_INVALID_ARGUMENT;
+  if (n == 0) return GDN_OK;
+  if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out) || !slots || !aligned4(slots))
+    return GDN_ERR_INVALID_ARGUMENT;
+  return gdn_launch_kv_read(c, n, slots, out_dtype == GDN_BF16, k_out, v_out,
+                            static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? GDN_OK
+             : GDN_ERR_CUDA;
+}
+
+static gdn_status check_attn_dims(int32_t batch, int32_t seqlen, int32_t num_heads,
+                                  int32_t num_kv_heads, int32_t head_dim) {
+  if (batch < 0 || seqlen < 0 || num_kv_heads < 1 || num_heads < 1 || num_heads % num_kv_heads)
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (head_dim != 128 && head_dim != 256) return GDN_ERR_UNSUPPORTED;
+  // query rows (and the work items of a call) are counted in 32 bits
+  if ((long long)batch * seqlen > (1 << 24) || num_heads > 1024 ||
+      (long long)batch * seqlen * num_heads > (1 << 28))
+    return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+size_t gdn_prefix_attention_workspace_size(int32_t batch, int32_t seqlen, int32_t num_heads,
+                                           int32_t num_kv_heads, int32_t head_dim) {
+  if (check_attn_dims(batch, seqlen, num_heads, num_kv_heads, head_dim) != GDN_OK) return 0;
+  if (batch == 0 || seqlen == 0) return 0;
+  return gdn_prefix_attention_bytes(batch, seqlen, num_heads, num_kv_heads, head_dim);
+}
+
+gdn_status gdn_prefix_attention(const gdn_kv_cache* cache, int32_t batch, int32_t seqlen,
+                                int32_t num_heads, const void* q, int64_t q_token_stride,
+                                const int32_t* prefix_pages, int32_t prefix_len,
+                                const int32_t* pages, int32_t max_pages, const int32_t* kv_len,
+                                float scale, gdn_dtype out_dtype, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  GdnAttnArgs a = {};
+  gdn_status st = check_kv_cache(cache, &a.cache);
+  if (st != GDN_OK) return st;
+  st = check_attn_dims(batch, seqlen, num_heads, a.cache.H, a.cache.D);
+  if (st != GDN_OK) return st;
+  if (prefix_len < 0 || max_pages < 0 || !isfinite(scale) || !is_dtype(out_dtype))
+    return GDN_ERR_INVALID_ARGUMENT;
+  if ((long long)max_pages * cache->page_size > 0x7fffff00LL || prefix_len > 0x7fffff00)
+    return GDN_ERR_UNSUPPORTED;
+  if (batch == 0 || seqlen == 0) return GDN_OK;
+  if (!q || !aligned16(q) || !out || !aligned16(out) || (lse && !aligned4(lse)))
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (q_token_stride < (int64_t)num_heads * a.cache.D || q_token_stride % 8)
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (prefix_len > 0 && (!prefix_pages || !aligned4(prefix_pages))) return GDN_ERR_INVALID_ARGUMENT;
+  if (max_pages > 0 && (!pages || !aligned4(pages))) return GDN_ERR_INVALID_ARGUMENT;
+  if (!kv_len || !aligned4(kv_len)) return GDN_ERR_INVALID_ARGUMENT;
+  if ((prefix_len > 0 || max_pages > 0) && cache->num_pages == 0) return GDN_ERR_INVALID_ARGUMENT;
+  const size_t need =
+      gdn_prefix_attention_bytes(batch, seqlen, num_heads, a.cache.H, a.cache.D);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+    return GDN_ERR_WORKSPACE;
+  a.B = batch; a.T = seqlen; a.Hq = num_heads; a.prefix_len = prefix_len;
+  a.max_pages = max_pages; a.out_bf16 = out_dtype == GDN_BF16; a.scale = scale;
+  a.q = q; a.q_stride = q_token_stride;
+  a.prefix_pages = prefix_pages; a.pages = pages; a.kv_len = kv_len;
+  a.out = out; a.lse = lse; a.workspace = workspace;
+  return gdn_launch_prefix_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? GDN_OK
+             : GDN_ERR_CUDA;
+}
+
+static gdn_status check_logprob_dims(int32_t rows, int32_t vocab, gdn_dtype dtype,
+                                     int32_t top_k) {
+  if (rows < 0 || vocab < 1 || !is_dtype(dtype) || top_k < 0 || top_k > vocab)
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (top_k > 32) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+size_t gdn_token_logprobs_workspace_size(int32_t rows, int32_t vocab, gdn_dtype dtype,
+                                         int32_t top_k) {
+  if (check_logprob_dims(rows, vocab, dtype, top_k) != GDN_OK || rows == 0) return 0;
+  return gdn_token_logprobs_bytes(rows, vocab, dtype == GDN_BF16, top_k);
+}
+
+gdn_status gdn_token_logprobs(int32_t rows, int32_t vocab, gdn_dtype dtype, const void* logits,
+                              int64_t row_stride, const int32_t* targets, float scale,
+                              float* logprobs, float* entropy, int32_t top_k, int32_t* top_ids,
+                              float* top_logprobs, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  const gdn_status st = check_logprob_dims(rows, vocab, dtype, top_k);
+  if (st != GDN_OK) return st;
+  if (!isfinite(scale) || !(scale > 0.0f) || row_stride < vocab) return GDN_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return GDN_OK;
+  const uintptr_t align = elem_bytes(dtype) - 1;
+  if (!logits || (reinterpret_cast<uintptr_t>(logits) & align)) return GDN_ERR_INVALID_ARGUMENT;
+  if ((logprobs != nullptr) != (targets != nullptr)) return GDN_ERR_INVALID_ARGUMENT;
+  if (top_k > 0 && (!top_ids || !top_logprobs)) return GDN_ERR_INVALID_ARGUMENT;
+  if (!aligned4(targets) || !aligned4(logprobs) || !aligned4(entropy) || !aligned4(top_ids) ||
+      !aligned4(top_logprobs))
+    return GDN_ERR_INVALID_ARGUMENT;
+  const size_t need = gdn_token_logprobs_bytes(rows, vocab, dtype == GDN_BF16, top_k);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need))
+    return GDN_ERR_WORKSPACE;
+  GdnLogprobArgs a = {};
+  a.N = rows; a.V = vocab; a.bf16 = dtype == GDN_BF16; a.top_k = top_k; a.scale = scale;
+  a.logits = logits; a.row_stride = row_stride; a.targets = targets; a.logprobs = logprobs;
+  a.entropy = entropy; a.top_ids = top_ids; a.top_logprobs = top_logprobs;
+  a.workspace = workspace;
+  return gdn_launch_token_logprobs(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? GDN_OK
+             : GDN_ERR_CUDA;
+}
+
 gdn_status gdn_selftest_device_timeout(uint32_t max_iters, void* stream) {
   if (max_iters == 0 || max_iters > (1u << 20)) return GDN_ERR_INVALID_ARGUMENT;
   return gdn_launch_selftest_wait(max_iters, static_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -539,7 +700,9 @@ gdn_status gdn_get_device_error(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return GDN_ERR_CUDA;
   unsigned bits = gdn_take_error_decode() | gdn_take_error_conv() | gdn_take_error_checkpoint() |
                   gdn_take_error_prefill_simt() | gdn_take_error_prefill_tc() |
-                  gdn_take_error_varlen() | gdn_take_error_decode_multi();
+                  gdn_take_error_varlen() | gdn_take_error_decode_multi() |
+                  gdn_take_error_kv_cache() | gdn_take_error_prefix_attention() |
+                  gdn_take_error_logprobs();
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   if (bits & gdn::kErrTimeout) return GDN_ERR_DEVICE_TIMEOUT;
   if (bits & gdn::kErrIndex) return GDN_ERR_DEVICE_INDEX;

@@ -400,6 +400,118 @@ gdn_status gdn_chunk_prefill_noalloc(const gdn_dims* dims, const gdn_opts* opts,
                                      float* state, void* conv_state,
                                      const int32_t* state_slots, void* out, void* stream);
 
+/* ------------------------------------------------------------------ full-attention layers
+ *
+ * A hybrid model interleaves the recurrent layers above with full-attention layers (PR #164b
+ * "Architecture": [3 DeltaNet + 1 GQA] blocks) and shares prompt prefixes between requests
+ * (PR #164 "Hybrid APC Runtime").  The calls below are what such a layer needs next to the
+ * recurrent state: its paged key/value cache, the attention of a batch that shares a prefix,
+ * and the scores of drafted tokens.
+ */
+
+/* What a key/value cache holds.  GDN_KV_E4M3: a vector x of head_dim elements (one token, one
+ * head) as e4m3 codes with one power-of-two scale 2^e: e is the least integer of [-60, 60] with
+ * max|x| 2^-e <= 448 over the finite elements of x (-60 for a zero vector), the code of x_i is
+ * x_i 2^-e rounded to nearest even and saturated at +-448 (infinities too); NaN stays NaN.  The
+ * value that it stands for, code * 2^e, is exact in bf16. */
+typedef enum { GDN_KV_BF16 = 0, GDN_KV_E4M3 = 1 } gdn_kv_format;
+
+/* A paged cache: pages of page_size tokens, slot s = page * page_size + position in the page. */
+typedef struct {
+  int32_t num_pages;     /* >= 0 */
+  int32_t page_size;     /* 16, 32, 64 or 128 tokens */
+  int32_t num_kv_heads;  /* H >= 1; num_pages * page_size * H < 2^31 */
+  int32_t head_dim;      /* D: 128 or 256 */
+  gdn_kv_format format;
+  void* k;               /* [num_pages, H, page_size, D] bf16 or e4m3 codes, 16-byte aligned */
+  void* v;
+  uint8_t* k_exp;        /* GDN_KV_E4M3: [num_pages, H, page_size], e + 127; else ignored */
+  uint8_t* v_exp;
+} gdn_kv_cache;
+
+/*
+ * gdn_kv_cache_append -- write n tokens' keys and values to their slots of the cache,
+ * quantising them as they are written when the cache is GDN_KV_E4M3.
+ *   k, v      token i at k + i * k_token_stride elements, [H, D] dense, in in_dtype (rounded
+ *             to bf16 for a bf16 cache); 16-byte aligned, strides a multiple of 16 bytes and at
+ *             least H * D (keys and values may be slices of one projection's rows).
+ *   slots     [n] device int32; a negative slot skips its token; one beyond the cache is
+ *             skipped and recorded as GDN_ERR_DEVICE_INDEX.  No two tokens name one slot.
+ */
+gdn_status gdn_kv_cache_append(const gdn_kv_cache* cache, int32_t n, gdn_dtype in_dtype,
+                               const void* k, int64_t k_token_stride, const void* v,
+                               int64_t v_token_stride, const int32_t* slots, void* stream);
+
+/*
+ * gdn_kv_cache_read -- gather n slots of the cache into k_out, v_out [n, H, D] in out_dtype
+ * (the stored values, exactly; 16-byte aligned).  A negative slot reads as zeros; so does one
+ * beyond the cache, which is recorded as GDN_ERR_DEVICE_INDEX.
+ */
+gdn_status gdn_kv_cache_read(const gdn_kv_cache* cache, int32_t n, const int32_t* slots,
+                             gdn_dtype out_dtype, void* k_out, void* v_out, void* stream);
+
+/*
+ * gdn_prefix_attention -- attention of T new tokens of each of B sequences that share a prefix:
+ * the products with the prefix's keys and values run once over the rows of the whole batch.
+ * Definition: for query t of sequence b, head h (key/value head h / (Hq / H)), over the visible
+ * keys j: the prefix_len shared tokens, then the sequence's own tokens 0 .. n - 1,
+ * n = kv_len[b] - T + 1 + t (own tokens include the T new ones, already in the cache):
+ *     p_j = exp(scale q.k_j - lse),  lse = log sum_j exp(scale q.k_j),  out = sum_j p_j v_j
+ * A row with no visible key (or whose scores are all -inf) has out = 0 and lse = -inf.
+ *   q             [B, T, Hq, D] bf16; tokens q_token_stride elements apart (a multiple of 8, at
+ *                 least Hq * D), heads dense; 16-byte aligned.
+ *   prefix_pages  [ceil(prefix_len / page_size)] device int32: the prefix's pages in order
+ *                 (ignored when prefix_len is 0).
+ *   pages         [B, max_pages] device int32: the sequences' own pages in order; entries past
+ *                 a sequence's last page are not read.
+ *   kv_len        [B] device int32: own tokens of each sequence.  A negative length leaves the
+ *                 sequence out (outputs zero, lse -inf, the prefix too); one beyond
+ *                 max_pages * page_size counts as that and is recorded as
+ *                 GDN_ERR_DEVICE_INDEX.
+ *   out           [B, T, Hq, D] in out_dtype, 16-byte aligned; lse [B, T, Hq] fp32 or NULL.
+ *   workspace     gdn_prefix_attention_workspace_size() bytes (0 for invalid sizes).
+ * A page entry outside the cache is recorded as GDN_ERR_DEVICE_INDEX (its tokens read as zero
+ * codes).  Cache entries at and past a sequence's length may hold anything, NaN included.
+ * The lengths stay on the device, so a captured graph can be replayed as they grow.
+ * Accuracy: exact products of bf16 (or e4m3) operands, fp32 scores and softmax statistics; the
+ * probabilities are rounded to bf16 (bf16 cache) or to nine significant bits (e4m3 cache) as
+ * operands of the second product.
+ */
+size_t gdn_prefix_attention_workspace_size(int32_t batch, int32_t seqlen, int32_t num_heads,
+                                           int32_t num_kv_heads, int32_t head_dim);
+gdn_status gdn_prefix_attention(const gdn_kv_cache* cache, int32_t batch, int32_t seqlen,
+                                int32_t num_heads, const void* q, int64_t q_token_stride,
+                                const int32_t* prefix_pages, int32_t prefix_len,
+                                const int32_t* pages, int32_t max_pages, const int32_t* kv_len,
+                                float scale, gdn_dtype out_dtype, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gdn_token_logprobs -- scores of given tokens under N rows of V logits, in one pass over them
+ * (the rows of a multi-token verification step, or of a prompt).  With x = scale * logits
+ * (scale: the inverse temperature, > 0):
+ *     lse = log sum_v exp(x_v)       logprobs[r] = x[targets[r]] - lse
+ *     entropy[r] = -sum_v p_v log p_v,  p = exp(x - lse)  (a -inf logit adds nothing)
+ *     top_ids, top_logprobs: the top_k largest logits in order, ties by the lowest index (NaN
+ *     above everything), and x - lse of each.
+ * A row whose logits are all -inf has logprob -inf, entropy 0 and top_logprobs -inf.
+ *   logits        row r at logits + r * row_stride elements (row_stride >= V), in dtype; any
+ *                 alignment of the element's own.
+ *   targets       [N] device int32, or NULL together with logprobs.  A negative target has
+ *                 logprob 0; one >= V has NaN and is recorded as GDN_ERR_DEVICE_INDEX.
+ *   logprobs, entropy  [N] fp32; entropy may be NULL.
+ *   top_k         0 .. 32, at most V; top_ids int32 and top_logprobs fp32 [N, top_k].
+ *   workspace     gdn_token_logprobs_workspace_size() bytes, 16-byte aligned (may be NULL when
+ *                 that is 0).
+ */
+size_t gdn_token_logprobs_workspace_size(int32_t rows, int32_t vocab, gdn_dtype dtype,
+                                         int32_t top_k);
+gdn_status gdn_token_logprobs(int32_t rows, int32_t vocab, gdn_dtype dtype, const void* logits,
+                              int64_t row_stride, const int32_t* targets, float scale,
+                              float* logprobs, float* entropy, int32_t top_k, int32_t* top_ids,
+                              float* top_logprobs, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 /*
  * Synchronises `stream`, then returns and clears the device error word: GDN_OK, or the
  * first condition recorded by a kernel since the last call (GDN_ERR_DEVICE_INDEX,
