@@ -1,10 +1,38 @@
-// Attention of a batch that shares a long prefix, over the paged key/value cache.  First form:
-// one warp a query row, keys one after the other with a running maximum and sum.
+// Attention of a batch that shares a long prefix, over the paged key/value cache.
+//
+// Work.  The rows (token, query head) that read the same keys form a unit: the rows of the whole
+// batch for one key/value head of the prefix, the rows of one sequence for one key/value head of
+// its own tokens, each cut into row tiles of 128.  A unit's keys are cut into tiles of 128.  All
+// (unit, key tile) pairs lie on one line, units one after the other; CTA c of the grid takes the
+// c-th equal part of it (a unit's start counts as kUnitCost tiles), so that every SM streams the
+// same number of keys whatever the lengths.  A unit's parts leave unnormalised outputs with each
+// row's reference m and sum l; the merge kernel joins a row's parts, prefix and own alike:
+//     out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.
+// The line is laid out on the device from the lengths, so a captured call can be replayed as they
+// grow.
+//
+// A part: S = Q K^T (M = 128 rows, N = 128 keys) and O += P V on tcgen05, S double-buffered in
+// tensor memory, P written over its S and read from there as the A operand; a running reference
+// m per row (raised, with O rescaled, only when the maximum passes it by more than kSlack, so
+// that a rescale is rare; any reference is exact, it cancels).  A producer warp streams K and V
+// tiles by TMA through a ring in shared memory, one copy a page.
+//
+// 8-bit cache: the codes are the operands as they lie in memory, nothing is converted on the way
+// to the tensor cores.  A bf16 element of Q, scaled by a power of two per row, is the sum of two
+// e4m3 numbers (4 + 4 significant bits; only elements below 2^-10 of the row's largest lose
+// bits), so S is two 8-bit products at twice the bf16 rate.  P takes three e5m2 terms (3 + 3 + 3
+// bits; e5m2 for its range: the smallest probabilities matter when a few keys outweigh
+// thousands).  The keys' scales multiply the scores; the values' scales 2^e_j go into the
+// exponent, P'_j = 2^(t_j + e_j - m) with m bounding t_j + e_j, and come out of the row sum
+// again, l = sum_j P'_j 2^(-e_j).
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "sm100_ptx.cuh"
 
 using namespace gdn;
+using namespace gdn::ptx;
 
 static __device__ unsigned int g_err_attn;
 
@@ -17,99 +45,854 @@ unsigned gdn_take_error_prefix_attention() {
 
 namespace {
 
+constexpr int kCtas = 152;                 // one CTA an SM
+constexpr int kRows = 128, kKeys = 128;
+constexpr int kUnitCost = 2;
+constexpr int KB = 1024;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Warps: 0 producer, 1 MMA issuer, 2 the 8-bit cache's scales, 4-11 softmax (two a TMEM lane
+// quarter, 64 of the tile's keys each).
+constexpr int kThreads = 384, kSoftmaxWarps = 8;
+
 template <int D, bool kF8>
-__device__ __forceinline__ void load_row(const void* base, const uint8_t* exps, long long row,
-                                         int lane, float (&x)[D / 32]) {
-  constexpr int E = D / 32;
-  if constexpr (kF8) {
-    const uint8_t* p = static_cast<const uint8_t*>(base) + row * D + lane * E;
-    const float f = exp2f((float)exps[row] - 127.0f);
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const __half h = __half(__nv_cvt_fp8_to_halfraw(p[i], __NV_E4M3));
-      x[i] = __half2float(h) * f;
-    }
-  } else {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + row * D + lane * E;
-#pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = __bfloat162float(p[i]);
-  }
+struct Shape {
+  static constexpr int kSlotBytes = kF8 ? kKeys * D : kKeys * 256;   // keys x at most 256 bytes
+  static constexpr int kSlotsPerTile = kF8 ? 1 : D / 128;           // of K, and of V
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kSlots = kF8 ? (D == 256 ? 4 : 8) : (D == 256 ? 5 : 6);
+  static constexpr int kElem = kF8 ? 128 : 64;                       // elements of a 128-byte row
+  // shared memory
+  static constexpr int kRing = kQBytes;
+  static constexpr int kMax = kRing + kSlots * kSlotBytes;           // [2][2][128] float
+  static constexpr int kQFac = kMax + 2048;                          // [128] float (8-bit)
+  static constexpr int kScales = kQFac + (kF8 ? 512 : 0);            // [2][3][128] float (8-bit)
+  static constexpr int kBars = kScales + (kF8 ? 3072 : 0);
+  static constexpr int kMisc = kBars + 8 * (2 * kSlots + 12 + 1);
+  static constexpr int kBytes = kMisc + 64;
+};
+static_assert(Shape<256, false>::kBytes <= 227 * KB && Shape<256, true>::kBytes <= 227 * KB &&
+                  Shape<128, false>::kBytes <= 227 * KB && Shape<128, true>::kBytes <= 227 * KB,
+              "shared memory");
+
+// tensor memory (columns)
+constexpr uint32_t TM_S = 0, TM_O = 256;
+
+struct Params {
+  GdnAttnArgs a;
+  int G, row_tiles_p, row_tiles_s, prefix_tiles;
+  int rows_p, rows_s;              // rows stored a part (<= 128)
+  float *o_p, *o_s;                // parts: [slot][rows][D]
+  float2 *ml_p, *ml_s;             // [slot][rows]: m (base 2), l
+  long long* line;                 // [B + 1]: where each sequence's units start; the line's end
+};
+
+__device__ __forceinline__ int own_len(const GdnAttnArgs& a, int b) {
+  const int n = a.kv_len[b], most = a.max_pages << a.cache.page_shift;
+  return n > most ? most : n;
+}
+// keys that some row of row tile rt of a sequence of n tokens sees (the last row's)
+__device__ __forceinline__ int tile_keys(const Params& p, int n, int rt) {
+  const int t = min(p.a.T - 1, ((rt + 1) * kRows - 1) / p.G);
+  return max(0, min(n, n - p.a.T + 1 + t));
+}
+__device__ __forceinline__ int key_tiles(int keys) { return (keys + kKeys - 1) / kKeys; }
+// a unit's length on the line
+__device__ __forceinline__ int unit_len(int tiles) { return tiles > 0 ? tiles + kUnitCost : 0; }
+__device__ __forceinline__ long long seq_len_on_line(const Params& p, int b) {
+  const int n = own_len(p.a, b);
+  long long w = 0;
+  if (n > 0)
+    for (int rt = 0; rt < p.row_tiles_s; ++rt) w += unit_len(key_tiles(tile_keys(p, n, rt)));
+  return w * p.a.cache.H;
 }
 
-template <int D, bool kF8, typename Tout>
-__global__ void __launch_bounds__(128) gdn_prefix_attention_simple(GdnAttnArgs a) {
-  constexpr int E = D / 32;
-  const GdnKvCacheArgs& c = a.cache;
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= (long long)a.B * a.T * a.Hq) return;
-  const int tok = (int)(row / a.Hq), hq = (int)(row % a.Hq), h = hq / (a.Hq / c.H);
-  const int b = tok / a.T, t = tok % a.T;
-  float q[E], o[E] = {}, m = -INFINITY, l = 0.0f;
-  const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q) + tok * a.q_stride +
-                            (long long)hq * D + lane * E;
-#pragma unroll
-  for (int i = 0; i < E; ++i) q[i] = __bfloat162float(qp[i]);
-  int len = a.kv_len[b];
-  const bool active = len >= 0;
-  const long long most = (long long)a.max_pages << c.page_shift;
-  if (len > most) {
-    if (lane == 0) atomicOr(&g_err_attn, kErrIndex);
-    len = (int)most;
+// One CTA's piece of a unit.
+struct Item {
+  bool prefix;
+  int h, b, rt, n;          // head, sequence, row tile, the sequence's own tokens
+  int keys, j0, j1;         // keys some row sees; key tiles [j0, j1)
+  long long unit;           // index among the prefix's / the sequences' units
+};
+
+// Walks the pieces of [pos, end) of the line; the same sequence in every warp.
+struct Walk {
+  long long pos, end, at;   // at: where the current unit starts
+  bool prefix;
+  int u, b, rt, h;
+
+  __device__ void start(const Params& p, long long lo, long long hi, int b0, long long at0) {
+    pos = lo; end = hi;
+    const long long wp = unit_len(p.prefix_tiles), units = (long long)p.a.cache.H * p.row_tiles_p;
+    prefix = p.prefix_tiles > 0 && lo < wp * units;
+    u = prefix ? (int)(lo / wp) : 0;
+    b = prefix ? 0 : b0; rt = 0; h = 0;
+    at = prefix ? u * wp : at0;
   }
-  const int own = max(0, min(len, len - a.T + 1 + t));
-  const int pm = (1 << c.page_shift) - 1;
-  const long long total = active ? (long long)a.prefix_len + own : 0;
-  for (long long j = 0; j < total; ++j) {
-    const bool pre = j < a.prefix_len;
-    const int i = (int)(pre ? j : j - a.prefix_len);
-    const int page = pre ? a.prefix_pages[i >> c.page_shift]
-                         : a.pages[(long long)b * a.max_pages + (i >> c.page_shift)];
-    float k[E] = {}, v[E] = {};
-    if (page < 0 || page >= c.num_pages) {
-      if (lane == 0) atomicOr(&g_err_attn, kErrIndex);
-    } else {
-      const long long r = (((long long)page * c.H + h) << c.page_shift) + (i & pm);
-      load_row<D, kF8>(c.k, c.k_exp, r, lane, k);
-      load_row<D, kF8>(c.v, c.v_exp, r, lane, v);
+  __device__ bool next(const Params& p, Item* it) {
+    const int H = p.a.cache.H;
+    while (at < end) {
+      int keys, n = 0;
+      if (prefix) {
+        keys = p.a.prefix_len;
+      } else {
+        if (b >= p.a.B) return false;
+        n = own_len(p.a, b);
+        keys = n > 0 ? tile_keys(p, n, rt) : 0;
+      }
+      const int tiles = key_tiles(keys), len = unit_len(tiles);
+      it->prefix = prefix;
+      it->keys = keys; it->n = n;
+      if (prefix) {
+        it->h = u / p.row_tiles_p; it->rt = u % p.row_tiles_p; it->b = 0; it->unit = u;
+      } else {
+        it->h = h; it->rt = rt; it->b = b;
+        it->unit = ((long long)b * p.row_tiles_s + rt) * H + h;
+      }
+      const long long first = at + kUnitCost;
+      const long long j0 = pos > first ? pos - first : 0;
+      const long long j1 = end > first ? end - first : 0;
+      it->j0 = (int)(j0 < tiles ? j0 : tiles);
+      it->j1 = (int)(j1 < tiles ? j1 : tiles);
+      at += len;
+      if (prefix) {
+        if (++u == H * p.row_tiles_p) { prefix = false; u = 0; }
+      } else if (n <= 0) {
+        ++b; rt = 0; h = 0;
+      } else if (++h == H) {
+        h = 0;
+        if (++rt == p.row_tiles_s) { rt = 0; ++b; }
+      }
+      if (it->j1 > it->j0) return true;
     }
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], k[e], s);
-    s = warp_sum(s) * a.scale;
-    const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.0f : mn;
-    const float f = expf(m - base), p = expf(s - base);
-    m = mn;
-    l = l * f + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * v[e];
+    return false;
   }
-  Tout* op = static_cast<Tout*>(a.out) + row * D + lane * E;
+};
+
+// Row r of an item: its token (of B T), head within the group, keys seen; false past the rows.
+__device__ __forceinline__ bool item_row(const Params& p, const Item& it, int r, int* token, int* g,
+                                         int* lim) {
+  const long long R = (long long)it.rt * kRows + r;
+  const int t = (int)(R / p.G);
+  *g = (int)(R - (long long)t * p.G);
+  if (it.prefix) {
+    *token = t;
+    *lim = p.a.prefix_len;
+    return t < p.a.B * p.a.T;
+  }
+  *token = it.b * p.a.T + t;
+  *lim = max(0, min(it.n, it.n - p.a.T + 1 + t));
+  return t < p.a.T;
+}
+
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (*abort) return false;
+  if (mbar_wait_or_abort(bar, parity, abort)) return true;
+  if (!*abort) atomicOr(&g_err_attn, kErrTimeout);
+  *abort = 1;
+  return false;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t half2_sub(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t half2_to_e5m2(uint32_t a) {
+  return __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&a), __NV_SATFINITE,
+                                    __NV_E5M2);
+}
+
+// Four numbers of [0, 57344] as sums of three e5m2 numbers (bytes of t0, t1, t2).  e5m2 is the
+// upper byte of fp16: the first two terms take the leading bits by truncation (the differences
+// are exact in fp16), the last is rounded.
+__device__ __forceinline__ void split_e5m2(const float (&x)[4], uint32_t* t0, uint32_t* t1,
+                                           uint32_t* t2) {
+  const uint32_t a = pack_half(x[0], x[1]), b = pack_half(x[2], x[3]);
+  const uint32_t ra = half2_sub(a, a & 0xff00ff00u), rb = half2_sub(b, b & 0xff00ff00u);
+  *t0 = __byte_perm(a, b, 0x7531);
+  *t1 = __byte_perm(ra, rb, 0x7531);
+  *t2 = half2_to_e5m2(half2_sub(ra, ra & 0xff00ff00u)) |
+        half2_to_e5m2(half2_sub(rb, rb & 0xff00ff00u)) << 16;
+}
+
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+  tmem_ld32(taddr, *reinterpret_cast<float(*)[32]>(&v[0]));
+  tmem_ld32(taddr + 32, *reinterpret_cast<float(*)[32]>(&v[32]));
+}
+
+template <int D, bool kF8>
+__global__ void __launch_bounds__(kThreads, 1)
+    gdn_prefix_attention_kernel(const Params p, const __grid_constant__ CUtensorMap map_k,
+                                const __grid_constant__ CUtensorMap map_v) {
+  using Z = Shape<D, kF8>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sb = smem_addr(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* sAbort = reinterpret_cast<volatile int*>(smem + Z::kMisc);
+  uint32_t* sTmem = reinterpret_cast<uint32_t*>(smem + Z::kMisc + 4);
+  int* sB0 = reinterpret_cast<int*>(smem + Z::kMisc + 8);
+  long long* sAt0 = reinterpret_cast<long long*>(smem + Z::kMisc + 16);
+  long long* sScan = reinterpret_cast<long long*>(smem + Z::kMax);   // 12 + 1 words, before use
+  const uint32_t bar_full = sb + Z::kBars, bar_empty = bar_full + 8 * Z::kSlots;
+  const uint32_t bar_s = bar_empty + 8 * Z::kSlots, bar_p = bar_s + 16, bar_pv = bar_p + 16;
+  const uint32_t bar_q = bar_pv + 16, bar_xf = bar_q + 8, bar_xe = bar_xf + 16;
+  const uint32_t bar_drain = bar_xe + 16;
+
+  if (tid == 0) {
+    for (int i = 0; i < Z::kSlots; ++i) {
+      mbar_init(bar_full + 8 * i, 1);
+      mbar_init(bar_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_s + 8 * i, 1);
+      mbar_init(bar_p + 8 * i, kSoftmaxWarps);
+      mbar_init(bar_pv + 8 * i, 1);
+      mbar_init(bar_xf + 8 * i, 32);
+      mbar_init(bar_xe + 8 * i, kSoftmaxWarps);
+    }
+    mbar_init(bar_q, kSoftmaxWarps);
+    mbar_init(bar_drain, 1);
+    fence_mbar_init();
+    *sAbort = 0;
+    *sB0 = p.a.B;
+    *sAt0 = 0;
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(sTmem), 512);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+  }
+
+  // ---- the line: its length, then the sequence in which this CTA's part starts
+  long long sum = 0;
+  for (int b = tid; b < p.a.B; b += kThreads) sum += seq_len_on_line(p, b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) sScan[warp] = sum;
+  __syncthreads();
+  const long long wp = (long long)unit_len(p.prefix_tiles) * p.a.cache.H * p.row_tiles_p;
+  long long W = wp;
+  for (int i = 0; i < kThreads / 32; ++i) W += sScan[i];
+  const int parts = (int)(W < kCtas ? W : kCtas), c = blockIdx.x;
+  const long long lo = parts > c ? W * c / parts : W, hi = parts > c ? W * (c + 1) / parts : W;
+  const bool find = lo < hi && lo >= wp;
+  if (find || c == 0) {
+    long long carry = wp;
+    for (int b0 = 0; b0 < p.a.B; b0 += kThreads) {
+      const int b = b0 + tid;
+      const long long w = b < p.a.B ? seq_len_on_line(p, b) : 0;
+      long long x = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      __syncthreads();                                // sScan is read no more
+      if (lane == 31) sScan[warp] = x;
+      __syncthreads();
+      long long before = carry;
+      for (int i = 0; i < kThreads / 32; ++i) {
+        if (i < warp) before += sScan[i];
+        carry += sScan[i];
+      }
+      const long long at = before + x - w;
+      if (find && at <= lo && lo < at + w) {
+        *sB0 = b;
+        *sAt0 = at;
+      }
+      if (c == 0 && b < p.a.B) {
+        p.line[b] = at;
+        const int n = p.a.kv_len[b];
+        if (n > (p.a.max_pages << p.a.cache.page_shift)) atomicOr(&g_err_attn, kErrIndex);
+      }
+      if (c != 0 && carry > lo) break;                // uniform
+    }
+    if (c == 0 && tid == 0) p.line[p.a.B] = W;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *sTmem;
+  Walk walk;
+  walk.start(p, lo, hi, *sB0, *sAt0);
+  Item it;
+
+  if (warp == 0) {
+    // =================================================== producer
+    const int shift = p.a.cache.page_shift, per = kKeys >> shift, page = 1 << shift;
+    const int head_rows = p.a.cache.H << shift;       // rows of a page, all heads
+    const int outside = p.a.cache.num_pages * head_rows;
+    uint32_t ring = 0;                                // slots filled so far
+    auto row_of = [&](int j) -> int {                 // of this lane's page of key tile j
+      const int i = j * per + lane;
+      if (lane >= per || (long long)i * page >= it.keys) return outside;
+      const int id = it.prefix ? p.a.prefix_pages[i]
+                               : p.a.pages[(long long)it.b * p.a.max_pages + i];
+      if ((unsigned)id >= (unsigned)p.a.cache.num_pages) {
+        atomicOr(&g_err_attn, kErrIndex);
+        return outside;
+      }
+      return id * head_rows + (it.h << shift);
+    };
+    auto fill = [&](const CUtensorMap* map, int row) {
+#pragma unroll
+      for (int s = 0; s < Z::kSlotsPerTile; ++s, ++ring) {
+        const uint32_t slot = ring % Z::kSlots, use = ring / Z::kSlots;
+        if (use > 0) wait(bar_empty + 8 * slot, (use - 1) & 1, sAbort);
+        if (__any_sync(0xffffffffu, *sAbort)) return;
+        if (lane == 0) mbar_arrive_expect_tx(bar_full + 8 * slot, Z::kSlotBytes);
+        __syncwarp();
+        if (lane < per) {
+#pragma unroll
+          for (int k = 0; k < Z::kSlotBytes / (16 * KB); ++k)
+            tma_load_3d(sb + Z::kRing + slot * Z::kSlotBytes + k * 16 * KB + (lane << (shift + 7)),
+                        map, (s * (Z::kSlotBytes / (16 * KB)) + k) * Z::kElem, row, 0,
+                        bar_full + 8 * slot);
+        }
+        __syncwarp();
+      }
+    };
+    while (walk.next(p, &it)) {
+      int row = row_of(it.j0);
+      fill(&map_k, row);
+      for (int j = it.j0 + 1; j < it.j1; ++j) {
+        const int after = row_of(j);
+        fill(&map_k, after);
+        fill(&map_v, row);
+        row = after;
+      }
+      fill(&map_v, row);
+    }
+    // after an abort: copies still in flight land before the CTA leaves
+    if (__any_sync(0xffffffffu, *sAbort))
+      for (uint32_t i = ring > Z::kSlots ? ring - Z::kSlots : 0; i < ring; ++i)
+        mbar_wait_bounded(bar_full + 8 * (i % Z::kSlots), (i / Z::kSlots) & 1);
+  } else if (warp == 1) {
+    // =================================================== MMA issuer
+    const bool leader = elect_one();
+    const int page = 1 << p.a.cache.page_shift;
+    uint32_t ring = 0, g = 0, items = 0;
+    auto scores = [&](uint32_t gt) {
+      const uint32_t d = tmem + TM_S + 128 * (gt & 1);
+#pragma unroll
+      for (int s = 0; s < Z::kSlotsPerTile; ++s, ++ring) {
+        const uint32_t slot = ring % Z::kSlots, kb = sb + Z::kRing + slot * Z::kSlotBytes;
+        if (!__all_sync(0xffffffffu, wait(bar_full + 8 * slot, (ring / Z::kSlots) & 1, sAbort)))
+          return;
+        tc_fence_after();
+        if (leader) {
+          if constexpr (kF8) {
+            constexpr uint32_t id = idesc_f8(128, kKeys, 0, 0, false, false);
+#pragma unroll
+            for (int k = 0; k < 2 * (D / 32); ++k) {
+              const int kk = k % (D / 32);
+              mma_f8(d, sdesc_sw128(sb + (k / (D / 32)) * kRows * D + (kk >> 2) * 16 * KB + (kk & 3) * 32, 16, 1024),
+                     sdesc_sw128(kb + (kk >> 2) * 16 * KB + (kk & 3) * 32, 16, 1024), id, k > 0);
+            }
+          } else {
+            constexpr uint32_t id = idesc_bf16(128, kKeys, false, false);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_bf16(d, sdesc_sw128(sb + (2 * s + (k >> 2)) * 16 * KB + (k & 3) * 32, 16, 1024),
+                       sdesc_sw128(kb + (k >> 2) * 16 * KB + (k & 3) * 32, 16, 1024), id,
+                       s > 0 || k > 0);
+          }
+          mma_commit(bar_empty + 8 * slot);
+          if (s == Z::kSlotsPerTile - 1) mma_commit(bar_s + 8 * (gt & 1));
+        }
+        __syncwarp();
+      }
+    };
+    auto values = [&](uint32_t gt, int j, bool first) {
+      const uint32_t a = tmem + TM_S + 128 * (gt & 1);
+      if (!__all_sync(0xffffffffu, wait(bar_p + 8 * (gt & 1), (gt >> 1) & 1, sAbort))) return;
+      const int live = it.keys - j * kKeys;           // rows of the tile that hold keys
+#pragma unroll
+      for (int s = 0; s < Z::kSlotsPerTile; ++s, ++ring) {
+        const uint32_t slot = ring % Z::kSlots, vb = sb + Z::kRing + slot * Z::kSlotBytes;
+        if (!__all_sync(0xffffffffu, wait(bar_full + 8 * slot, (ring / Z::kSlots) & 1, sAbort)))
+          return;
+        if (live < kKeys && (live & (page - 1))) {
+          // the rest of the last page holds anything: zero it (0 * NaN)
+          const int r1 = (live + page - 1) & ~(page - 1);
+          for (int i = live * 8 + lane; i < r1 * 8; i += 32)
+#pragma unroll
+            for (int k = 0; k < Z::kSlotBytes / (16 * KB); ++k)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(vb + k * 16 * KB + i * 16),
+                           "r"(0)
+                           : "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        tc_fence_after();
+        if (leader) {
+          if constexpr (kF8) {
+            constexpr uint32_t id = idesc_f8(128, D, 1, 0, false, true);
+#pragma unroll
+            for (int k = 0; k < 12; ++k)
+              mma_f8_ta(tmem + TM_O, a + 32 * (k >> 2) + 8 * (k & 3),
+                        sdesc_sw128(vb + (k & 3) * 4096, 16 * KB, 1024), id, !first || k > 0);
+          } else {
+            constexpr uint32_t id = idesc_bf16(128, 128, false, true);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)                // P's two terms
+              mma_bf16_ta(tmem + TM_O + 128 * s, a + 8 * k,
+                          sdesc_sw128(vb + (k & 7) * 2048, 16 * KB, 1024), id, !first || k > 0);
+          }
+          mma_commit(bar_empty + 8 * slot);
+          if (s == Z::kSlotsPerTile - 1) mma_commit(bar_pv + 8 * (gt & 1));
+        }
+        __syncwarp();
+      }
+    };
+    while (walk.next(p, &it)) {
+      wait(bar_q, items & 1, sAbort);
+      ++items;
+      scores(g);
+      for (int j = it.j0 + 1; j < it.j1; ++j) {
+        scores(g + 1);
+        values(g, j - 1, j - 1 == it.j0);
+        ++g;
+      }
+      values(g, it.j1 - 1, it.j1 - 1 == it.j0);
+      ++g;
+    }
+    if (__any_sync(0xffffffffu, *sAbort)) {
+      // after an abort: products in flight end before tensor memory is freed
+      if (leader) mma_commit(bar_drain);
+      __syncwarp();
+      mbar_wait_bounded(bar_drain, 0);
+    }
+  } else if (warp == 2) {
+    // =================================================== the 8-bit cache's scales
+    if constexpr (kF8) {
+      uint32_t g = 0;
+      const int shift = p.a.cache.page_shift, pm = (1 << shift) - 1;
+      while (walk.next(p, &it)) {
+        for (int j = it.j0; j < it.j1; ++j, ++g) {
+          const int key = j * kKeys + lane * 4;
+          uint32_t ke = 0x7f7f7f7fu, ve = 0x7f7f7f7fu;  // 2^0 for keys that nothing sees
+          if (key < it.keys) {
+            const int i = key >> shift;
+            const int id = it.prefix ? p.a.prefix_pages[i]
+                                     : p.a.pages[(long long)it.b * p.a.max_pages + i];
+            if ((unsigned)id < (unsigned)p.a.cache.num_pages) {
+              const long long r = (((long long)id * p.a.cache.H + it.h) << shift) + (key & pm);
+              ke = *reinterpret_cast<const uint32_t*>(p.a.cache.k_exp + r);
+              ve = *reinterpret_cast<const uint32_t*>(p.a.cache.v_exp + r);
+            }
+          }
+          float ks[4], ev[4], iv[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool live = key + e < it.keys;
+            // exponents outside the format's range can only come from entries never written
+            const int k = live ? min(max((int)(ke >> (8 * e) & 0xff), 67), 187) : 127;
+            const int v = live ? min(max((int)(ve >> (8 * e) & 0xff), 67), 187) : 127;
+            ks[e] = __uint_as_float((uint32_t)k << 23);
+            ev[e] = (float)(v - 127);
+            iv[e] = __uint_as_float((uint32_t)(254 - v) << 23);
+          }
+          const uint32_t st = g & 1;
+          if (g >= 2) wait(bar_xe + 8 * st, ((g >> 1) - 1) & 1, sAbort);
+          float4* dst = reinterpret_cast<float4*>(smem + Z::kScales + st * 1536) + lane;
+          dst[0] = make_float4(ks[0], ks[1], ks[2], ks[3]);
+          dst[32] = make_float4(ev[0], ev[1], ev[2], ev[3]);
+          dst[64] = make_float4(iv[0], iv[1], iv[2], iv[3]);
+          mbar_arrive(bar_xf + 8 * st);
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    // =================================================== softmax
+    const int sw = warp - 4, quarter = sw & 3, half = sw >> 2;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    float* sMax = reinterpret_cast<float*>(smem + Z::kMax);
+    float* sQFac = reinterpret_cast<float*>(smem + Z::kQFac);
+    // the scale's sign goes into Q, and so does a scale of zero
+    const float coef = p.a.scale == 0.0f ? 1.0f : fabsf(p.a.scale) * kLog2e;
+    const uint32_t flip = p.a.scale < 0.0f ? 0x80008000u : 0u;
+    const uint32_t keep = p.a.scale == 0.0f ? 0u : ~0u;
+    // bf16: P up to 2^kSlack.  8-bit: P up to 2^15 (of e5m2's 57344), its reference 12 below
+    constexpr float kSlack = kF8 ? 3.0f : 8.0f, kLift = kF8 ? 12.0f : 0.0f;
+    uint32_t g = 0;
+    while (walk.next(p, &it)) {
+      // ---- Q: the item's rows, gathered into the swizzled K-major layout
+      {
+        constexpr int L = D / 8, kPer = 32 / L;       // lanes a row, rows a pass
+#pragma unroll 4
+        for (int i = 0; i < 16; i += kPer) {
+          const int row = sw * 16 + i + lane / L, l = lane % L;
+          int token, gh, lim;
+          const bool ok = item_row(p, it, row, &token, &gh, &lim);
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (ok)
+            u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) +
+                                                token * p.a.q_stride +
+                                                (long long)(it.h * p.G + gh) * D + l * 8);
+          u.x = (u.x & keep) ^ flip; u.y = (u.y & keep) ^ flip;
+          u.z = (u.z & keep) ^ flip; u.w = (u.w & keep) ^ flip;
+          if constexpr (!kF8) {
+            *reinterpret_cast<uint4*>(smem + (l >> 3) * 16 * KB + row * 128 +
+                                      (((l & 7) ^ (row & 7)) << 4)) = u;
+          } else {
+            float x[8], top = 0.0f;
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[2 * e] = __uint_as_float(w[e] << 16);
+              x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1)
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // 2^-e with top 2^-e of [224, 448]; e kept where both powers are normal
+            int e = (int)(__float_as_uint(top) >> 23) - 127 - 8 +
+                    ((__float_as_uint(top) & 0x7fffffu) > 0x600000u ? 1 : 0);
+            e = min(max(e, -120), 120);
+            // (an infinite query makes its row NaN)
+            const float f = top < INFINITY ? __uint_as_float((uint32_t)(127 - e) << 23) : NAN;
+            uint32_t hi[2], lo2[2];
+#pragma unroll
+            for (int e2 = 0; e2 < 2; ++e2) {
+              uint32_t hw[2], lw[2];
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const float a0 = x[4 * e2 + 2 * q] * f, a1 = x[4 * e2 + 2 * q + 1] * f;
+                const __nv_fp8x2_storage_t h8 =
+                    __nv_cvt_float2_to_fp8x2(make_float2(a0, a1), __NV_SATFINITE, __NV_E4M3);
+                const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2(h8, __NV_E4M3));
+                hw[q] = h8;
+                lw[q] = __nv_cvt_float2_to_fp8x2(
+                    make_float2(a0 - __low2float(back), a1 - __high2float(back)), __NV_SATFINITE,
+                    __NV_E4M3);
+              }
+              hi[e2] = hw[0] | hw[1] << 16;
+              lo2[e2] = lw[0] | lw[1] << 16;
+            }
+            uint8_t* at = smem + (l >> 4) * 16 * KB + row * 128 +
+                          ((((l & 15) >> 1) ^ (row & 7)) << 4) + (l & 1) * 8;
+            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(at + kRows * D) = make_uint2(lo2[0], lo2[1]);
+            if (l == 0) sQFac[row] = __uint_as_float((uint32_t)(127 + e) << 23);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();                            // the previous item's reads of O
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_q);
+        if constexpr (kF8) named_bar_sync(5, 32 * kSoftmaxWarps);
+      }
+      int token, gh, lim;
+      const bool live = item_row(p, it, r, &token, &gh, &lim);
+      if (!live) lim = 0;
+      const bool any_live = __any_sync(0xffffffffu, live);
+      const float rc = kF8 ? coef * sQFac[r] : coef;
+      float m = -INFINITY, l = 0.0f;                  // reference, this half's sum
+      for (int j = it.j0; j < it.j1; ++j, ++g) {
+        const uint32_t buf = g & 1, ts = tmem + TM_S + 128 * buf + lane_base;
+        wait(bar_s + 8 * buf, (g >> 1) & 1, sAbort);
+        if constexpr (kF8) wait(bar_xf + 8 * buf, (g >> 1) & 1, sAbort);
+        if (any_live) {
+          tc_fence_after();
+          float s[64];
+          tmem_ld64(ts + 64 * half, s);
+          tmem_wait_ld();
+          const float4* ks = reinterpret_cast<const float4*>(smem + Z::kScales + buf * 1536) + 16 * half;
+          if constexpr (kF8) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float4 k4 = ks[i], v4 = ks[32 + i];
+              s[4 * i] = fmaf(s[4 * i] * k4.x, rc, v4.x);
+              s[4 * i + 1] = fmaf(s[4 * i + 1] * k4.y, rc, v4.y);
+              s[4 * i + 2] = fmaf(s[4 * i + 2] * k4.z, rc, v4.z);
+              s[4 * i + 3] = fmaf(s[4 * i + 3] * k4.w, rc, v4.w);
+            }
+          }
+          const int seen = lim - j * kKeys - 64 * half;  // this half's keys that the row sees
+          if (__any_sync(0xffffffffu, seen < 64)) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i >= seen) s[i] = -INFINITY;
+          }
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int i = 4; i < 64; i += 4) {
+            mx[0] = fmaxf(mx[0], s[i]);
+            mx[1] = fmaxf(mx[1], s[i + 1]);
+            mx[2] = fmaxf(mx[2], s[i + 2]);
+            mx[3] = fmaxf(mx[3], s[i + 3]);
+          }
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          float* sm = sMax + buf * 256;
+          sm[half * 128 + r] = top;
+          named_bar_sync(1 + quarter, 64);
+          top = fmaxf(top, sm[(1 - half) * 128 + r]);
+          if constexpr (!kF8) top *= rc;
+          // the reference: the first maximum; later only when it is passed by more than kSlack
+          const bool raise = top - kLift > m + kSlack;
+          if (j == it.j0) {
+            m = top - kLift;
+          } else if (__any_sync(0xffffffffu, raise)) {
+            const float mn = raise ? top - kLift : m;
+            const float f = raise ? ex2_approx(m - mn) : 1.0f;
+            m = mn;
+            l *= f;
+            wait(bar_pv + 8 * (buf ^ 1), ((g - 1) >> 1) & 1, sAbort);  // O of the tiles before
+            tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < D / 2; i += 32) {
+              float o[32];
+              const uint32_t to = tmem + TM_O + lane_base + half * (D / 2) + i;
+              tmem_ld32(to, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= f;
+              tmem_st32(to, o);
+            }
+            tmem_wait_st();
+          }
+          const float base = m == -INFINITY ? 0.0f : m;
+          float sum4[4] = {};
+          if constexpr (kF8) {
+            uint32_t t0[16], t1[16], t2[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float4 iv = ks[64 + i];
+              float e[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) e[q] = ex2_approx(s[4 * i + q] - base);
+              sum4[0] = fmaf(e[0], iv.x, sum4[0]);
+              sum4[1] = fmaf(e[1], iv.y, sum4[1]);
+              sum4[2] = fmaf(e[2], iv.z, sum4[2]);
+              sum4[3] = fmaf(e[3], iv.w, sum4[3]);
+              split_e5m2(e, &t0[i], &t1[i], &t2[i]);
+            }
+            tmem_st16(ts + 16 * half, t0);
+            tmem_st16(ts + 32 + 16 * half, t1);
+            tmem_st16(ts + 64 + 16 * half, t2);
+          } else {
+            float hi[32], lo[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float e0 = ex2_approx(fmaf(s[2 * i], rc, -base));
+              const float e1 = ex2_approx(fmaf(s[2 * i + 1], rc, -base));
+              sum4[(2 * i) & 3] += e0;
+              sum4[(2 * i + 1) & 3] += e1;
+              const uint32_t h = pack_bf16(e0, e1);
+              hi[i] = __uint_as_float(h);
+              lo[i] = __uint_as_float(pack_bf16(e0 - __uint_as_float(h << 16),
+                                                e1 - __uint_as_float(h & 0xffff0000u)));
+            }
+            tmem_st32(ts + 32 * half, hi);
+            tmem_st32(ts + 64 + 32 * half, lo);
+          }
+          l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar_p + 8 * buf);
+          if constexpr (kF8) mbar_arrive(bar_xe + 8 * buf);
+        }
+      }
+      // ---- the part: O, m, l of the item's rows
+      wait(bar_pv + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, sAbort);
+      if (any_live) {
+        tc_fence_after();
+        float* sl = sMax + (g & 1) * 256;             // the other buffer is the last tile's
+        sl[half * 128 + r] = l;
+        named_bar_sync(1 + quarter, 64);
+        l += sl[(1 - half) * 128 + r];
+        const int stored = it.prefix ? p.rows_p : p.rows_s;
+        const long long row = (it.unit + c) * stored + r;
+        float* op = (it.prefix ? p.o_p : p.o_s) + row * D + half * (D / 2);
+#pragma unroll 1
+        for (int i = 0; i < D / 2; i += 32) {
+          float o[32];
+          tmem_ld32(tmem + TM_O + lane_base + half * (D / 2) + i, o);
+          tmem_wait_ld();
+          if (live) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<float4*>(op + i)[e] =
+                  make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+        if (live && half == 0) (it.prefix ? p.ml_p : p.ml_s)[row] = make_float2(m, l);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------------------- the merge
+//
+// One row (token, head) a group of kLanes threads: the parts of its prefix unit and of its own
+// unit, found from the line's layout.
+template <int D, typename Tout>
+__global__ void __launch_bounds__(256) gdn_prefix_merge_kernel(const Params p) {
+  constexpr int kLanes = D / 8;
+  pdl_wait();
+  const long long rows = (long long)p.a.B * p.a.T * p.a.Hq;
+  const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / kLanes;
+  const int l8 = threadIdx.x % kLanes;
+  if (row >= rows) return;
+  const int token = (int)(row / p.a.Hq), hq = (int)(row % p.a.Hq);
+  const int h = hq / p.G, gh = hq % p.G, b = token / p.a.T, t = token % p.a.T, H = p.a.cache.H;
+  const long long W = p.line[p.a.B];
+  const int parts = (int)(W < kCtas ? W : kCtas);
+  float acc[8] = {}, m = -INFINITY, l = 0.0f;
+  auto join = [&](long long at, int tiles, long long unit, const float* o, const float2* ml,
+                  int stored, int r) {
+    // the CTAs that hold the first and the last of the unit's tiles
+    const long long x0 = at + kUnitCost, x1 = x0 + tiles - 1;
+    const int c0 = (int)(((x0 + 1) * parts - 1) / W), c1 = (int)(((x1 + 1) * parts - 1) / W);
+    for (int c = c0; c <= c1; ++c) {
+      const long long at_row = (unit + c) * stored + r;
+      const float2 v = ml[at_row];
+      const float4* src = reinterpret_cast<const float4*>(o + at_row * D + l8 * 8);
+      const float4 a = src[0], d = src[1];
+      if (v.x == -INFINITY) continue;                 // no key seen
+      const float mn = fmaxf(m, v.x);
+      const float f = m == -INFINITY ? 0.0f : ex2_approx(m - mn), w = ex2_approx(v.x - mn);
+      m = mn;
+      l = l * f + v.y * w;
+      const float x[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = acc[e] * f + x[e] * w;
+    }
+  };
+  const int n_raw = p.a.kv_len[b];
+  if (n_raw >= 0 && W > 0) {
+    if (p.prefix_tiles > 0) {
+      const long long R = (long long)token * p.G + gh;
+      const long long unit = (long long)h * p.row_tiles_p + R / kRows;
+      join(unit * unit_len(p.prefix_tiles), p.prefix_tiles, unit, p.o_p, p.ml_p, p.rows_p,
+           (int)(R % kRows));
+    }
+    const int n = own_len(p.a, b), R = t * p.G + gh, rt = R / kRows;
+    const int tiles = n > 0 ? key_tiles(tile_keys(p, n, rt)) : 0;
+    if (tiles > 0) {
+      long long at = p.line[b];
+      for (int i = 0; i < rt; ++i) at += (long long)H * unit_len(key_tiles(tile_keys(p, n, i)));
+      at += (long long)h * unit_len(tiles);
+      join(at, tiles, ((long long)b * p.row_tiles_s + rt) * H + h, p.o_s, p.ml_s, p.rows_s,
+           R % kRows);
+    }
+  }
+  // l is NaN where a score is, 0 where no key is seen
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  Tout* out = static_cast<Tout*>(p.a.out) + row * D + l8 * 8;
+  if constexpr (sizeof(Tout) == 2) {
+    uint32_t w[4];
 #pragma unroll
-  for (int e = 0; e < E; ++e) st_elem(op + e, o[e] * inv);
-  if (a.lse && lane == 0) a.lse[row] = l == 0.0f ? -INFINITY : m + logf(l);
+    for (int e = 0; e < 4; ++e) w[e] = pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    reinterpret_cast<float4*>(out)[0] =
+        make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+    reinterpret_cast<float4*>(out)[1] =
+        make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv);
+  }
+  if (p.a.lse && l8 == 0) p.a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// ------------------------------------------------------------------------------- host side
+
+struct Layout {
+  int row_tiles_p, row_tiles_s, rows_p, rows_s;
+  size_t line, ml_p, ml_s, o_p, o_s, total;
+};
+
+Layout layout_of(int B, int T, int Hq, int H, int D) {
+  auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
+  Layout y;
+  const int G = Hq / H;
+  const long long rp = (long long)B * T * G, rs = (long long)T * G;
+  y.row_tiles_p = (int)((rp + kRows - 1) / kRows);
+  y.row_tiles_s = (int)((rs + kRows - 1) / kRows);
+  y.rows_p = (int)(rp < kRows ? rp : kRows);
+  y.rows_s = (int)(rs < kRows ? rs : kRows);
+  const size_t np = ((size_t)H * y.row_tiles_p + kCtas) * y.rows_p;
+  const size_t ns = ((size_t)B * y.row_tiles_s * H + kCtas) * y.rows_s;
+  size_t off = 0;
+  y.line = off; off += up(8 * ((size_t)B + 1));
+  y.ml_p = off; off += up(8 * np);
+  y.ml_s = off; off += up(8 * ns);
+  y.o_p = off; off += up(4 * np * D);
+  y.o_s = off; off += up(4 * ns * D);
+  y.total = off;
+  return y;
 }
 
 template <int D, bool kF8>
-void launch(const GdnAttnArgs& a, cudaStream_t stream) {
-  const long long rows = (long long)a.B * a.T * a.Hq;
-  const unsigned grid = (unsigned)((rows + 3) / 4);
-  if (a.out_bf16) gdn_prefix_attention_simple<D, kF8, __nv_bfloat16><<<grid, 128, 0, stream>>>(a);
-  else gdn_prefix_attention_simple<D, kF8, float><<<grid, 128, 0, stream>>>(a);
+cudaError_t launch(const Params& p, cudaStream_t stream) {
+  using Z = Shape<D, kF8>;
+  const GdnKvCacheArgs& c = p.a.cache;
+  static unsigned done = 0;
+  cudaError_t e = set_smem_once(gdn_prefix_attention_kernel<D, kF8>, Z::kBytes, &done);
+  if (e != cudaSuccess) return e;
+  CUtensorMap mk = {}, mv = {};
+  if (c.num_pages > 0) {
+    const CUtensorMapDataType dt =
+        kF8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int rows = c.num_pages * (c.H << c.page_shift);
+    if (!gdn_make_map(&mk, c.k, dt, kF8 ? 1 : 2, D, rows, 1, D, Z::kElem, 1 << c.page_shift, true) ||
+        !gdn_make_map(&mv, c.v, dt, kF8 ? 1 : 2, D, rows, 1, D, Z::kElem, 1 << c.page_shift, true))
+      return cudaErrorInvalidValue;
+  }
+  e = launch_pdl(false, gdn_prefix_attention_kernel<D, kF8>, dim3(kCtas), dim3(kThreads), Z::kBytes,
+                 stream, p, mk, mv);
+  if (e != cudaSuccess) return e;
+  const long long threads = (long long)p.a.B * p.a.T * p.a.Hq * (D / 8);
+  const dim3 grid((unsigned)((threads + 255) / 256));
+  if (p.a.out_bf16)
+    return launch_pdl(true, gdn_prefix_merge_kernel<D, __nv_bfloat16>, grid, dim3(256), 0, stream, p);
+  return launch_pdl(true, gdn_prefix_merge_kernel<D, float>, grid, dim3(256), 0, stream, p);
 }
 
 }  // namespace
 
-size_t gdn_prefix_attention_bytes(int, int, int, int, int) { return 0; }
+size_t gdn_prefix_attention_bytes(int B, int T, int Hq, int H, int D) {
+  return layout_of(B, T, Hq, H, D).total;
+}
 
 cudaError_t gdn_launch_prefix_attention(const GdnAttnArgs& a, cudaStream_t stream) {
-  if (a.cache.D == 128) {
-    if (a.cache.f8) launch<128, true>(a, stream);
-    else launch<128, false>(a, stream);
-  } else {
-    if (a.cache.f8) launch<256, true>(a, stream);
-    else launch<256, false>(a, stream);
-  }
-  return cudaGetLastError();
+  const Layout y = layout_of(a.B, a.T, a.Hq, a.cache.H, a.cache.D);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  Params p;
+  p.a = a;
+  p.G = a.Hq / a.cache.H;
+  p.row_tiles_p = y.row_tiles_p;
+  p.row_tiles_s = y.row_tiles_s;
+  p.prefix_tiles = (a.prefix_len + kKeys - 1) / kKeys;
+  p.rows_p = y.rows_p;
+  p.rows_s = y.rows_s;
+  p.line = reinterpret_cast<long long*>(ws + y.line);
+  p.ml_p = reinterpret_cast<float2*>(ws + y.ml_p);
+  p.ml_s = reinterpret_cast<float2*>(ws + y.ml_s);
+  p.o_p = reinterpret_cast<float*>(ws + y.o_p);
+  p.o_s = reinterpret_cast<float*>(ws + y.o_s);
+  if (a.cache.D == 128)
+    return a.cache.f8 ? launch<128, true>(p, stream) : launch<128, false>(p, stream);
+  return a.cache.f8 ? launch<256, true>(p, stream) : launch<256, false>(p, stream);
 }
