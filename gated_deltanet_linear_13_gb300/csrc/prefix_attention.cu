@@ -48,6 +48,7 @@ namespace {
 constexpr int kCtas = 152;                 // one CTA an SM
 constexpr int kRows = 128, kKeys = 128;
 constexpr int kUnitCost = 2;
+constexpr long long kBlockBytes = 32ll << 20;
 constexpr int KB = 1024;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -65,7 +66,8 @@ struct Shape {
   // shared memory
   static constexpr int kRing = kQBytes;
   static constexpr int kMax = kRing + kSlots * kSlotBytes;           // [2][2][128] float
-  static constexpr int kQFac = kMax + 2048;                          // [128] float (8-bit)
+  static constexpr int kSum = kMax + 2048;                           // [128] float
+  static constexpr int kQFac = kSum + 512;                           // [128] float (8-bit)
   static constexpr int kScales = kQFac + (kF8 ? 512 : 0);            // [2][3][128] float (8-bit)
   static constexpr int kBars = kScales + (kF8 ? 3072 : 0);
   static constexpr int kMisc = kBars + 8 * (2 * kSlots + 12 + 1);
@@ -81,8 +83,9 @@ constexpr uint32_t TM_S = 0, TM_O = 256;
 struct Params {
   GdnAttnArgs a;
   int G, row_tiles_p, row_tiles_s, prefix_tiles;
+  int blocks, block_tiles;         // the prefix's key tiles, cut into blocks (the last shorter)
   int rows_p, rows_s;              // rows stored a part (<= 128)
-  float *o_p, *o_s;                // parts: [slot][rows][D]
+  float *o_p, *o_s;                // parts: [slot][D / 4][rows][4]
   float2 *ml_p, *ml_s;             // [slot][rows]: m (base 2), l
   long long* line;                 // [B + 1]: where each sequence's units start; the line's end
 };
@@ -97,6 +100,9 @@ __device__ __forceinline__ int tile_keys(const Params& p, int n, int rt) {
   return max(0, min(n, n - p.a.T + 1 + t));
 }
 __device__ __forceinline__ int key_tiles(int keys) { return (keys + kKeys - 1) / kKeys; }
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
 // a unit's length on the line
 __device__ __forceinline__ int unit_len(int tiles) { return tiles > 0 ? tiles + kUnitCost : 0; }
 __device__ __forceinline__ long long seq_len_on_line(const Params& p, int b) {
@@ -105,6 +111,17 @@ __device__ __forceinline__ long long seq_len_on_line(const Params& p, int b) {
   if (n > 0)
     for (int rt = 0; rt < p.row_tiles_s; ++rt) w += unit_len(key_tiles(tile_keys(p, n, rt)));
   return w * p.a.cache.H;
+}
+
+// The prefix's units lie in the order (head, block of keys, row tile): the row tiles of a block
+// side by side, so that the CTAs that read the same keys do so at the same time, out of L2.
+__device__ __forceinline__ int block_len(const Params& p, int blk) {
+  return unit_len(min(p.block_tiles, p.prefix_tiles - blk * p.block_tiles));
+}
+__device__ __forceinline__ long long head_len(const Params& p) {
+  if (p.prefix_tiles == 0) return 0;
+  return (long long)p.row_tiles_p *
+         ((long long)(p.blocks - 1) * unit_len(p.block_tiles) + block_len(p, p.blocks - 1));
 }
 
 // One CTA's piece of a unit.
@@ -119,44 +136,63 @@ struct Item {
 struct Walk {
   long long pos, end, at;   // at: where the current unit starts
   bool prefix;
-  int u, b, rt, h;
+  int b, blk, rt, h;
+  int len_b, len;           // the last sequence whose length was read, and it
 
   __device__ void start(const Params& p, long long lo, long long hi, int b0, long long at0) {
     pos = lo; end = hi;
-    const long long wp = unit_len(p.prefix_tiles), units = (long long)p.a.cache.H * p.row_tiles_p;
-    prefix = p.prefix_tiles > 0 && lo < wp * units;
-    u = prefix ? (int)(lo / wp) : 0;
-    b = prefix ? 0 : b0; rt = 0; h = 0;
-    at = prefix ? u * wp : at0;
+    const long long hl = head_len(p);
+    prefix = lo < hl * p.a.cache.H;
+    b = prefix ? 0 : b0; blk = 0; rt = 0; h = 0;
+    len_b = -1;
+    at = at0;
+    if (prefix) {
+      h = (int)quotient(lo, hl);
+      long long rest = lo - h * hl;
+      const long long bl = (long long)p.row_tiles_p * unit_len(p.block_tiles);
+      blk = min((int)quotient(rest, bl), p.blocks - 1);
+      rest -= blk * bl;
+      rt = (int)quotient(rest, block_len(p, blk));
+      at = h * hl + blk * bl + (long long)rt * block_len(p, blk);
+    }
   }
   __device__ bool next(const Params& p, Item* it) {
     const int H = p.a.cache.H;
     while (at < end) {
-      int keys, n = 0;
+      int keys, tiles, base = 0, n = 0;
       if (prefix) {
         keys = p.a.prefix_len;
+        base = blk * p.block_tiles;
+        tiles = min(p.block_tiles, p.prefix_tiles - base);
+        it->unit = ((long long)h * p.blocks + blk) * p.row_tiles_p + rt;
       } else {
         if (b >= p.a.B) return false;
-        n = own_len(p.a, b);
+        if (b != len_b) {
+          len_b = b;
+          len = own_len(p.a, b);
+        }
+        n = len;
         keys = n > 0 ? tile_keys(p, n, rt) : 0;
-      }
-      const int tiles = key_tiles(keys), len = unit_len(tiles);
-      it->prefix = prefix;
-      it->keys = keys; it->n = n;
-      if (prefix) {
-        it->h = u / p.row_tiles_p; it->rt = u % p.row_tiles_p; it->b = 0; it->unit = u;
-      } else {
-        it->h = h; it->rt = rt; it->b = b;
+        tiles = key_tiles(keys);
         it->unit = ((long long)b * p.row_tiles_s + rt) * H + h;
       }
+      it->prefix = prefix;
+      it->keys = keys; it->n = n;
+      it->h = h; it->rt = rt; it->b = b;
       const long long first = at + kUnitCost;
       const long long j0 = pos > first ? pos - first : 0;
       const long long j1 = end > first ? end - first : 0;
-      it->j0 = (int)(j0 < tiles ? j0 : tiles);
-      it->j1 = (int)(j1 < tiles ? j1 : tiles);
-      at += len;
+      it->j0 = base + (int)(j0 < tiles ? j0 : tiles);
+      it->j1 = base + (int)(j1 < tiles ? j1 : tiles);
+      at += unit_len(tiles);
       if (prefix) {
-        if (++u == H * p.row_tiles_p) { prefix = false; u = 0; }
+        if (++rt == p.row_tiles_p) {
+          rt = 0;
+          if (++blk == p.blocks) {
+            blk = 0;
+            if (++h == H) { h = 0; prefix = false; }
+          }
+        }
       } else if (n <= 0) {
         ++b; rt = 0; h = 0;
       } else if (++h == H) {
@@ -172,9 +208,9 @@ struct Walk {
 // Row r of an item: its token (of B T), head within the group, keys seen; false past the rows.
 __device__ __forceinline__ bool item_row(const Params& p, const Item& it, int r, int* token, int* g,
                                          int* lim) {
-  const long long R = (long long)it.rt * kRows + r;
-  const int t = (int)(R / p.G);
-  *g = (int)(R - (long long)t * p.G);
+  const unsigned R = (unsigned)it.rt * kRows + r;     // rows are counted in 32 bits
+  const int t = (int)(R / (unsigned)p.G);
+  *g = (int)(R - (unsigned)t * p.G);
   if (it.prefix) {
     *token = t;
     *lim = p.a.prefix_len;
@@ -282,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) sScan[warp] = sum;
   __syncthreads();
-  const long long wp = (long long)unit_len(p.prefix_tiles) * p.a.cache.H * p.row_tiles_p;
+  const long long wp = head_len(p) * p.a.cache.H;
   long long W = wp;
   for (int i = 0; i < kThreads / 32; ++i) W += sScan[i];
   const int parts = (int)(W < kCtas ? W : kCtas), c = blockIdx.x;
@@ -321,13 +357,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (c == 0 && tid == 0) p.line[p.a.B] = W;
   }
+  pdl_trigger();                                      // the merge may be set up
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *sTmem;
   Walk walk;
   walk.start(p, lo, hi, *sB0, *sAt0);
-  Item it;
+  Item it = {};
 
   if (warp == 0) {
     // =================================================== producer
@@ -521,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     float* sMax = reinterpret_cast<float*>(smem + Z::kMax);
+    float* sSum = reinterpret_cast<float*>(smem + Z::kSum);
     float* sQFac = reinterpret_cast<float*>(smem + Z::kQFac);
     // the scale's sign goes into Q, and so does a scale of zero
     const float coef = p.a.scale == 0.0f ? 1.0f : fabsf(p.a.scale) * kLog2e;
@@ -529,20 +567,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     // bf16: P up to 2^kSlack.  8-bit: P up to 2^15 (of e5m2's 57344), its reference 12 below
     constexpr float kSlack = kF8 ? 3.0f : 8.0f, kLift = kF8 ? 12.0f : 0.0f;
     uint32_t g = 0;
-    while (walk.next(p, &it)) {
-      // ---- Q: the item's rows, gathered into the swizzled K-major layout
-      {
+    // Q: an item's rows, gathered into the swizzled K-major layout
+    auto load_q = [&](const Item& it) {
         constexpr int L = D / 8, kPer = 32 / L;       // lanes a row, rows a pass
-#pragma unroll 4
-        for (int i = 0; i < 16; i += kPer) {
-          const int row = sw * 16 + i + lane / L, l = lane % L;
-          int token, gh, lim;
-          const bool ok = item_row(p, it, row, &token, &gh, &lim);
-          uint4 u = make_uint4(0, 0, 0, 0);
-          if (ok)
-            u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) +
-                                                token * p.a.q_stride +
-                                                (long long)(it.h * p.G + gh) * D + l * 8);
+        const int l = lane % L;
+        const long long left = (long long)(it.prefix ? p.a.B : 1) * p.a.T * p.G -
+                               (long long)it.rt * kRows;
+        const int n = left < kRows ? (int)left : kRows;   // the item's rows, dealt to the warps
+        const int first = sw * kPer + lane / L;
+        uint4 qv[16 / kPer];                          // every load before the first use
+#pragma unroll
+        for (int i = 0; i < 16 / kPer; ++i) {
+          const int row = first + i * (8 * kPer);
+          qv[i] = make_uint4(0, 0, 0, 0);
+          if (row < n) {
+            int token, gh, lim;
+            item_row(p, it, row, &token, &gh, &lim);
+            qv[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) +
+                                                    token * p.a.q_stride +
+                                                    (long long)(it.h * p.G + gh) * D + l * 8);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16 / kPer; ++i) {
+          const int row = first + i * (8 * kPer);
+          if (sw * kPer + i * (8 * kPer) >= n) break;     // (uniform; the rest feeds no live row)
+          uint4 u = qv[i];
           u.x = (u.x & keep) ^ flip; u.y = (u.y & keep) ^ flip;
           u.z = (u.z & keep) ^ flip; u.w = (u.w & keep) ^ flip;
           if constexpr (!kF8) {
@@ -593,11 +643,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         fence_proxy_async_smem();
-        tc_fence_before();                            // the previous item's reads of O
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_q);
         if constexpr (kF8) named_bar_sync(5, 32 * kSoftmaxWarps);
-      }
+    };
+    bool more = walk.next(p, &it);
+    if (more) load_q(it);
+    while (more) {
       int token, gh, lim;
       const bool live = item_row(p, it, r, &token, &gh, &lim);
       if (!live) lim = 0;
@@ -712,30 +764,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (kF8) mbar_arrive(bar_xe + 8 * buf);
         }
       }
+      // ---- the next item's Q (every score of this item is done), so that its first scores
+      // run beside this item's end; its first P waits for this thread, so O stays
+      Item done = it;
+      more = walk.next(p, &it);
+      if (more) load_q(it);
       // ---- the part: O, m, l of the item's rows
       wait(bar_pv + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, sAbort);
       if (any_live) {
         tc_fence_after();
-        float* sl = sMax + (g & 1) * 256;             // the other buffer is the last tile's
-        sl[half * 128 + r] = l;
+        if (half == 1) sSum[r] = l;
         named_bar_sync(1 + quarter, 64);
-        l += sl[(1 - half) * 128 + r];
-        const int stored = it.prefix ? p.rows_p : p.rows_s;
-        const long long row = (it.unit + c) * stored + r;
-        float* op = (it.prefix ? p.o_p : p.o_s) + row * D + half * (D / 2);
+        if (half == 0) l += sSum[r];
+        // lanes hold consecutive rows: 16 bytes a row side by side
+        const int stored = done.prefix ? p.rows_p : p.rows_s;
+        const long long slot = done.unit + c;
+        float4* op = reinterpret_cast<float4*>(done.prefix ? p.o_p : p.o_s) +
+                     (slot * (D / 4) + half * (D / 8)) * stored + r;
 #pragma unroll 1
-        for (int i = 0; i < D / 2; i += 32) {
+        for (int i = 0; i < D / 8; i += 8) {
           float o[32];
-          tmem_ld32(tmem + TM_O + lane_base + half * (D / 2) + i, o);
+          tmem_ld32(tmem + TM_O + lane_base + half * (D / 2) + 4 * i, o);
           tmem_wait_ld();
           if (live) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              reinterpret_cast<float4*>(op + i)[e] =
+              op[(long long)(i + e) * stored] =
                   make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
-        if (live && half == 0) (it.prefix ? p.ml_p : p.ml_s)[row] = make_float2(m, l);
+        if (live && half == 0) (done.prefix ? p.ml_p : p.ml_s)[slot * stored + r] = make_float2(m, l);
+        tc_fence_before();
       }
     }
   }
@@ -746,74 +805,128 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------------------- the merge
 //
-// One row (token, head) a group of kLanes threads: the parts of its prefix unit and of its own
-// unit, found from the line's layout.
+// A block takes eight rows of one head (the parts lie with consecutive rows side by side) and 64
+// columns; its eight warps share out the rows' parts, found from the line's layout, so that the
+// parts of a row cut into many (few rows, a long prefix) are read at the same time, and join
+// what they have in shared memory.
 template <int D, typename Tout>
 __global__ void __launch_bounds__(256) gdn_prefix_merge_kernel(const Params p) {
-  constexpr int kLanes = D / 8;
+  constexpr int kAhead = 2, kVec = 4;                 // parts in flight, 16-byte vectors a lane
+  __shared__ float4 s_acc[8][16][8];                  // [warp][vector of the 64 columns][row]
+  __shared__ float2 s_ml[8][8];
+  const unsigned rows = (unsigned)p.a.B * p.a.T * p.G;   // of a head
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r8 = lane & 7;
+  const unsigned R0 = blockIdx.x * 8u + r8, R = R0 < rows ? R0 : rows - 1;
+  const int cg = blockIdx.z * 16 + (lane >> 3), h = blockIdx.y, H = p.a.cache.H;
+  const int token = (int)(R / (unsigned)p.G), gh = (int)(R - (unsigned)token * p.G);
+  const int b = token / p.a.T, t = token - b * p.a.T;
+  const int raw = p.a.kv_len[b], n = own_len(p.a, b);
   pdl_wait();
-  const long long rows = (long long)p.a.B * p.a.T * p.a.Hq;
-  const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / kLanes;
-  const int l8 = threadIdx.x % kLanes;
-  if (row >= rows) return;
-  const int token = (int)(row / p.a.Hq), hq = (int)(row % p.a.Hq);
-  const int h = hq / p.G, gh = hq % p.G, b = token / p.a.T, t = token % p.a.T, H = p.a.cache.H;
   const long long W = p.line[p.a.B];
+  const long long at_b = p.line[b];
   const int parts = (int)(W < kCtas ? W : kCtas);
-  float acc[8] = {}, m = -INFINITY, l = 0.0f;
+  float acc[4 * kVec] = {}, m = -INFINITY, l = 0.0f;
+  // the parts c0 + skip, + step, ... of a unit
   auto join = [&](long long at, int tiles, long long unit, const float* o, const float2* ml,
-                  int stored, int r) {
+                  int stored, int r, int skip, int step) {
     // the CTAs that hold the first and the last of the unit's tiles
     const long long x0 = at + kUnitCost, x1 = x0 + tiles - 1;
-    const int c0 = (int)(((x0 + 1) * parts - 1) / W), c1 = (int)(((x1 + 1) * parts - 1) / W);
-    for (int c = c0; c <= c1; ++c) {
-      const long long at_row = (unit + c) * stored + r;
-      const float2 v = ml[at_row];
-      const float4* src = reinterpret_cast<const float4*>(o + at_row * D + l8 * 8);
-      const float4 a = src[0], d = src[1];
-      if (v.x == -INFINITY) continue;                 // no key seen
-      const float mn = fmaxf(m, v.x);
-      const float f = m == -INFINITY ? 0.0f : ex2_approx(m - mn), w = ex2_approx(v.x - mn);
-      m = mn;
-      l = l * f + v.y * w;
-      const float x[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
+    const int c0 = (int)quotient((x0 + 1) * parts - 1, W);
+    const int c1 = (int)quotient((x1 + 1) * parts - 1, W);
+    for (int c = c0 + skip; c <= c1; c += kAhead * step) {
+      float2 v[kAhead];
+      float4 x[kAhead][kVec];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = acc[e] * f + x[e] * w;
+      for (int i = 0; i < kAhead; ++i) {
+        const long long slot = unit + min(c + i * step, c1);
+        const float4* src = reinterpret_cast<const float4*>(o) + (slot * (D / 4) + cg) * stored + r;
+        v[i] = ml[slot * stored + r];
+#pragma unroll
+        for (int q = 0; q < kVec; ++q) x[i][q] = src[(long long)(4 * q) * stored];
+        if (c + i * step > c1) v[i] = make_float2(-INFINITY, 0.0f);
+      }
+      float mn = m;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) mn = fmaxf(mn, v[i].x);
+      if (mn == -INFINITY) continue;                  // no key seen
+      const float f = ex2_approx(m - mn);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < 4 * kVec; ++e) acc[e] *= f;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (v[i].x == -INFINITY) continue;            // its O holds nothing
+        const float w = ex2_approx(v[i].x - mn);
+        l += v[i].y * w;
+#pragma unroll
+        for (int q = 0; q < kVec; ++q) {
+          acc[4 * q] += x[i][q].x * w;
+          acc[4 * q + 1] += x[i][q].y * w;
+          acc[4 * q + 2] += x[i][q].z * w;
+          acc[4 * q + 3] += x[i][q].w * w;
+        }
+      }
     }
   };
-  const int n_raw = p.a.kv_len[b];
-  if (n_raw >= 0 && W > 0) {
+  if (raw >= 0 && W > 0) {
     if (p.prefix_tiles > 0) {
-      const long long R = (long long)token * p.G + gh;
-      const long long unit = (long long)h * p.row_tiles_p + R / kRows;
-      join(unit * unit_len(p.prefix_tiles), p.prefix_tiles, unit, p.o_p, p.ml_p, p.rows_p,
-           (int)(R % kRows));
+      const int rt = R / kRows;
+      const long long hl = head_len(p), bl = (long long)p.row_tiles_p * unit_len(p.block_tiles);
+      const bool whole = p.blocks >= 8;               // a warp takes whole blocks, or parts of each
+      for (int blk = whole ? warp : 0; blk < p.blocks; blk += whole ? 8 : 1)
+        join(h * hl + blk * bl + (long long)rt * block_len(p, blk),
+             min(p.block_tiles, p.prefix_tiles - blk * p.block_tiles),
+             ((long long)h * p.blocks + blk) * p.row_tiles_p + rt, p.o_p, p.ml_p, p.rows_p,
+             R % kRows, whole ? 0 : (warp + blk) & 7, whole ? 1 : 8);
     }
-    const int n = own_len(p.a, b), R = t * p.G + gh, rt = R / kRows;
+    const int r = t * p.G + gh, rt = r / kRows;
     const int tiles = n > 0 ? key_tiles(tile_keys(p, n, rt)) : 0;
     if (tiles > 0) {
-      long long at = p.line[b];
+      long long at = at_b;
       for (int i = 0; i < rt; ++i) at += (long long)H * unit_len(key_tiles(tile_keys(p, n, i)));
       at += (long long)h * unit_len(tiles);
       join(at, tiles, ((long long)b * p.row_tiles_s + rt) * H + h, p.o_s, p.ml_s, p.rows_s,
-           R % kRows);
+           r % kRows, (warp + 4) & 7, 8);
     }
+  }
+#pragma unroll
+  for (int q = 0; q < kVec; ++q)
+    s_acc[warp][4 * q + (lane >> 3)][r8] =
+        make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
+  if (lane < 8) s_ml[warp][lane] = make_float2(m, l);
+  __syncthreads();
+  // 128 threads: a row and a 16-byte vector of the 64 columns each
+  const int vec = threadIdx.x >> 3;
+  if (threadIdx.x >= 128 || R0 >= rows) return;
+  float2 v[8];
+  m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = s_ml[i][r8];
+    m = fmaxf(m, v[i].x);
+  }
+  l = 0.0f;
+  float y[4] = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (v[i].x == -INFINITY) continue;
+    const float w = ex2_approx(v[i].x - m);
+    const float4 x = s_acc[i][vec][r8];
+    l += v[i].y * w;
+    y[0] += x.x * w; y[1] += x.y * w; y[2] += x.z * w; y[3] += x.w * w;
   }
   // l is NaN where a score is, 0 where no key is seen
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  Tout* out = static_cast<Tout*>(p.a.out) + row * D + l8 * 8;
-  if constexpr (sizeof(Tout) == 2) {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-    reinterpret_cast<float4*>(out)[0] =
-        make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-    reinterpret_cast<float4*>(out)[1] =
-        make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv);
-  }
-  if (p.a.lse && l8 == 0) p.a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+  const long long row = (long long)token * p.a.Hq + h * p.G + gh;
+  Tout* out = static_cast<Tout*>(p.a.out) + row * D + blockIdx.z * 64 + vec * 4;
+  if constexpr (sizeof(Tout) == 2)
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv));
+  else
+    *reinterpret_cast<float4*>(out) = make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+  if (p.a.lse && blockIdx.z == 0 && vec == 0)
+    p.a.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ------------------------------------------------------------------------------- host side
@@ -832,7 +945,9 @@ Layout layout_of(int B, int T, int Hq, int H, int D) {
   y.row_tiles_s = (int)((rs + kRows - 1) / kRows);
   y.rows_p = (int)(rp < kRows ? rp : kRows);
   y.rows_s = (int)(rs < kRows ? rs : kRows);
-  const size_t np = ((size_t)H * y.row_tiles_p + kCtas) * y.rows_p;
+  size_t up_units = (size_t)H * y.row_tiles_p;        // at most kCtas more of them by blocks
+  if (up_units < kCtas) up_units = kCtas;
+  const size_t np = (up_units + kCtas) * y.rows_p;
   const size_t ns = ((size_t)B * y.row_tiles_s * H + kCtas) * y.rows_s;
   size_t off = 0;
   y.line = off; off += up(8 * ((size_t)B + 1));
@@ -863,8 +978,7 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
   e = launch_pdl(false, gdn_prefix_attention_kernel<D, kF8>, dim3(kCtas), dim3(kThreads), Z::kBytes,
                  stream, p, mk, mv);
   if (e != cudaSuccess) return e;
-  const long long threads = (long long)p.a.B * p.a.T * p.a.Hq * (D / 8);
-  const dim3 grid((unsigned)((threads + 255) / 256));
+  const dim3 grid((unsigned)(((long long)p.a.B * p.a.T * p.G + 7) / 8), (unsigned)c.H, D / 64);
   if (p.a.out_bf16)
     return launch_pdl(true, gdn_prefix_merge_kernel<D, __nv_bfloat16>, grid, dim3(256), 0, stream, p);
   return launch_pdl(true, gdn_prefix_merge_kernel<D, float>, grid, dim3(256), 0, stream, p);
@@ -885,6 +999,17 @@ cudaError_t gdn_launch_prefix_attention(const GdnAttnArgs& a, cudaStream_t strea
   p.row_tiles_p = y.row_tiles_p;
   p.row_tiles_s = y.row_tiles_s;
   p.prefix_tiles = (a.prefix_len + kKeys - 1) / kKeys;
+  // several row tiles of a prefix that L2 does not hold beside everything else: blocks of keys
+  // of about one CTA's part
+  const long long prefix_bytes = 2ll * a.prefix_len * a.cache.H * a.cache.D * (a.cache.f8 ? 1 : 2);
+  p.blocks = 1;
+  if (y.row_tiles_p > 1 && prefix_bytes > kBlockBytes) {
+    p.blocks = kCtas / (y.row_tiles_p * a.cache.H);
+    if (p.blocks < 1) p.blocks = 1;
+    if (p.blocks > p.prefix_tiles) p.blocks = p.prefix_tiles;
+  }
+  p.block_tiles = p.prefix_tiles ? (p.prefix_tiles + p.blocks - 1) / p.blocks : 1;
+  if (p.prefix_tiles) p.blocks = (p.prefix_tiles + p.block_tiles - 1) / p.block_tiles;
   p.rows_p = y.rows_p;
   p.rows_s = y.rows_s;
   p.line = reinterpret_cast<long long*>(ws + y.line);
