@@ -164,6 +164,9 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _need(t: Optional[torch.Tensor], name: str, shape, dtype, device):
+    if (t is not None and t.dtype is dtype and t.shape == shape and t.device == device and
+            t.is_contiguous()):
+        return                       # the usual case, ahead of finding out what is wrong
     if t is None:
         raise ValueError(f"{name} is required")
     if tuple(t.shape) != tuple(shape):
@@ -180,6 +183,14 @@ def _stream(stream) -> int:
     if stream is None:
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _stream_of(stream, device: torch.device) -> int:
+    """The raw stream; by default the current one of the tensors' device (a lookup without the
+    Stream object, whose making costs as much as a launch)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return _stream(stream)
 
 
 def _check(status: int, where: str):
@@ -634,43 +645,47 @@ def gdn_state_checkpoint(op: str, state, conv_state, slot_state, slot_conv_state
 
 # ---------------------------------------------------------------- full-attention layers
 
-def _kv_cache(k_cache, v_cache, k_exp, v_exp) -> GdnKvCache:
-    """The C struct of a paged cache [num_pages, H, page_size, D]: bf16, or float8_e4m3fn codes
-    with uint8 exponents [num_pages, H, page_size]."""
-    if k_cache.device.type != "cuda":
+def _kv_cache(k_cache, v_cache, k_exp, v_exp):
+    """(C struct, device) of a paged cache [num_pages, H, page_size, D]: bf16, or float8_e4m3fn
+    codes with uint8 exponents [num_pages, H, page_size]."""
+    dev, shape, dtype = k_cache.device, k_cache.shape, k_cache.dtype
+    if dev.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
-    if k_cache.dim() != 4:
-        raise ValueError(f"k_cache: shape {tuple(k_cache.shape)}, expected 4 dimensions")
-    if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-        raise TypeError(f"k_cache: dtype {k_cache.dtype}, expected bfloat16 or float8_e4m3fn")
-    dev, shape = k_cache.device, tuple(k_cache.shape)
-    _need(k_cache, "k_cache", shape, k_cache.dtype, dev)
-    _need(v_cache, "v_cache", shape, k_cache.dtype, dev)
-    fmt = GDN_KV_BF16
-    if k_cache.dtype == torch.float8_e4m3fn:
-        fmt = GDN_KV_E4M3
+    if len(shape) != 4:
+        raise ValueError(f"k_cache: shape {tuple(shape)}, expected 4 dimensions")
+    f8 = dtype is torch.float8_e4m3fn
+    if not f8 and dtype is not torch.bfloat16:
+        raise TypeError(f"k_cache: dtype {dtype}, expected bfloat16 or float8_e4m3fn")
+    _need(k_cache, "k_cache", shape, dtype, dev)
+    _need(v_cache, "v_cache", shape, dtype, dev)
+    pages, heads, page_size, d = shape
+    if f8:
         _need(k_exp, "k_exp", shape[:3], torch.uint8, dev)
         _need(v_exp, "v_exp", shape[:3], torch.uint8, dev)
-    elif k_exp is not None or v_exp is not None:
+        return GdnKvCache(pages, page_size, heads, d, GDN_KV_E4M3, k_cache.data_ptr(),
+                          v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr()), dev
+    if k_exp is not None or v_exp is not None:
         raise ValueError("a bf16 cache has no exponents: k_exp and v_exp must be None")
-    pages, heads, page_size, d = shape
-    return GdnKvCache(pages, page_size, heads, d, fmt, _ptr(k_cache), _ptr(v_cache),
-                      _ptr(k_exp), _ptr(v_exp))
+    return GdnKvCache(pages, page_size, heads, d, GDN_KV_BF16, k_cache.data_ptr(),
+                      v_cache.data_ptr(), None, None), dev
 
 
 def _token_stride(t: torch.Tensor, name: str, shape, dtype, device) -> int:
     """The token stride (elements) of t [..., H, D], whose heads are dense and whose leading
     dimensions lie one token after the other."""
-    if tuple(t.shape) != tuple(shape):
+    H, D = shape[-2:]
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return H * D
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
-    H, D = shape[-2:]
-    if (D > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != D):
+    strides = t.stride()
+    if (D > 1 and strides[-1] != 1) or (H > 1 and strides[-2] != D):
         raise ValueError(f"{name}: the last two dimensions must be dense")
-    lead, stride = [(n, s) for n, s in zip(t.shape[:-2], t.stride()[:-2]) if n > 1], H * D
+    lead, stride = [(n, s) for n, s in zip(shape[:-2], strides) if n > 1], H * D
     if lead:
         stride = lead[-1][1]
         for (_, s), (n, inner) in zip(lead[:-1], lead[1:]):
@@ -685,15 +700,15 @@ def gdn_kv_cache_append(k, v, k_cache, v_cache, slots, *, k_exp=None, v_exp=None
     fine) to their ``slots`` [n] of the paged cache k_cache, v_cache [num_pages, H, page_size,
     D]: bf16, or float8_e4m3fn with k_exp, v_exp (see gdn_kv_cache_append in include/gdn.h)."""
     L = load_library()
-    c = _kv_cache(k_cache, v_cache, k_exp, v_exp)
-    n, dev = slots.shape[0], k_cache.device
+    c, dev = _kv_cache(k_cache, v_cache, k_exp, v_exp)
+    n = slots.shape[0]
     shape = (n, c.num_kv_heads, c.head_dim)
     _need(slots, "slots", (n,), torch.int32, dev)
     dt = _dt(k)
     ks = _token_stride(k, "k", shape, k.dtype, dev)
     vs = _token_stride(v, "v", shape, k.dtype, dev)
-    st = L.gdn_kv_cache_append(ctypes.byref(c), n, dt, _ptr(k), ks, _ptr(v), vs, _ptr(slots),
-                               _stream(stream))
+    st = L.gdn_kv_cache_append(ctypes.byref(c), n, dt, k.data_ptr(), ks, v.data_ptr(), vs,
+                               slots.data_ptr(), _stream_of(stream, dev))
     _check(st, "gdn_kv_cache_append")
 
 
@@ -702,14 +717,14 @@ def gdn_kv_cache_read(k_cache, v_cache, slots, k_out, v_out, *, k_exp=None, v_ex
     """Gather ``slots`` [n] of the cache into k_out, v_out [n, H, D] (bf16 or fp32); negative
     slots read as zeros.  Returns (k_out, v_out)."""
     L = load_library()
-    c = _kv_cache(k_cache, v_cache, k_exp, v_exp)
-    n, dev = slots.shape[0], k_cache.device
+    c, dev = _kv_cache(k_cache, v_cache, k_exp, v_exp)
+    n = slots.shape[0]
     _need(slots, "slots", (n,), torch.int32, dev)
     dt = _dt(k_out)
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         _need(t, name, (n, c.num_kv_heads, c.head_dim), k_out.dtype, dev)
-    st = L.gdn_kv_cache_read(ctypes.byref(c), n, _ptr(slots), dt, _ptr(k_out), _ptr(v_out),
-                             _stream(stream))
+    st = L.gdn_kv_cache_read(ctypes.byref(c), n, slots.data_ptr(), dt, k_out.data_ptr(),
+                             v_out.data_ptr(), _stream_of(stream, dev))
     _check(st, "gdn_kv_cache_read")
     return k_out, v_out
 
@@ -730,11 +745,10 @@ def gdn_prefix_attention(q, k_cache, v_cache, out, *, pages, kv_len, prefix_page
     kv_len [B] (own tokens, the T new ones included), out [B, T, Hq, D] bf16 or fp32, lse
     [B, T, Hq] fp32 or None; scale defaults to 1 / sqrt(D).  Returns ``out``."""
     L = load_library()
-    c = _kv_cache(k_cache, v_cache, k_exp, v_exp)
+    c, dev = _kv_cache(k_cache, v_cache, k_exp, v_exp)
     if q.dim() != 4:
         raise ValueError(f"q: shape {tuple(q.shape)}, expected 4 dimensions")
     B, T, Hq, D = q.shape
-    dev = k_cache.device
     qs = _token_stride(q, "q", (B, T, Hq, c.head_dim), torch.bfloat16, dev)
     dt = _dt(out)
     _need(out, "out", (B, T, Hq, D), out.dtype, dev)
@@ -752,14 +766,14 @@ def gdn_prefix_attention(q, k_cache, v_cache, out, *, pages, kv_len, prefix_page
             raise ValueError("prefix_pages holds fewer tokens than prefix_len")
     if lse is not None:
         _need(lse, "lse", (B, T, Hq), torch.float32, dev)
-    need = int(L.gdn_prefix_attention_workspace_size(B, T, Hq, c.num_kv_heads, D))
-    if need and workspace is None:
+    if workspace is None:
+        need = int(L.gdn_prefix_attention_workspace_size(B, T, Hq, c.num_kv_heads, D))
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = workspace.numel() * workspace.element_size()
     st = L.gdn_prefix_attention(ctypes.byref(c), B, T, Hq, _ptr(q), qs, _ptr(prefix_pages),
                                 int(prefix_len), _ptr(pages), pages.shape[1], _ptr(kv_len),
                                 float(D ** -0.5 if scale is None else scale), dt, _ptr(out),
-                                _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream))
+                                _ptr(lse), _ptr(workspace), ws_bytes, _stream_of(stream, dev))
     _check(st, "gdn_prefix_attention")
     return out
 
@@ -801,14 +815,15 @@ def gdn_token_logprobs(logits, targets, logprobs, entropy=None, *, top_ids=None,
         k = top_ids.shape[1] if top_ids.dim() == 2 else -1
         _need(top_ids, "top_ids", (N, k), torch.int32, dev)
         _need(top_logprobs, "top_logprobs", (N, k), torch.float32, dev)
-    need = int(L.gdn_token_logprobs_workspace_size(N, V, dt, k))
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is None:
+        need = int(L.gdn_token_logprobs_workspace_size(N, V, dt, k))
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = L.gdn_token_logprobs(N, V, dt, _ptr(logits), logits.stride(0) if N > 1 else V,
                               _ptr(targets), float(scale), _ptr(logprobs), _ptr(entropy), k,
                               _ptr(top_ids), _ptr(top_logprobs), _ptr(workspace), ws_bytes,
-                              _stream(stream))
+                              _stream_of(stream, dev))
     _check(st, "gdn_token_logprobs")
 
 
