@@ -20,8 +20,8 @@
 // 8-bit cache: the codes are the operands as they lie in memory, nothing is converted on the way
 // to the tensor cores.  A bf16 element of Q, scaled by a power of two per row, is the sum of two
 // e4m3 numbers (4 + 4 significant bits; only elements below 2^-10 of the row's largest lose
-// bits), so S is two 8-bit products at twice the bf16 rate.  P takes three e5m2 terms (3 + 3 + 3
-// bits; e5m2 for its range: the smallest probabilities matter when a few keys outweigh
+// bits), so S is two 8-bit products at twice the bf16 rate.  P takes three e5m2 terms (3 bits
+// each and the terms' signs: 11 bits; e5m2 for its range: the smallest probabilities matter when a few keys outweigh
 // thousands).  The keys' scales multiply the scores; the values' scales 2^e_j go into the
 // exponent, P'_j = 2^(t_j + e_j - m) with m bounding t_j + e_j, and come out of the row sum
 // again, l = sum_j P'_j 2^(-e_j).
@@ -250,17 +250,20 @@ __device__ __forceinline__ uint32_t half2_to_e5m2(uint32_t a) {
                                     __NV_E5M2);
 }
 
-// Four numbers of [0, 57344] as sums of three e5m2 numbers (bytes of t0, t1, t2).  e5m2 is the
-// upper byte of fp16: the first two terms take the leading bits by truncation (the differences
-// are exact in fp16), the last is rounded.
+// Four numbers of [0, 2^15] as sums of three e5m2 numbers (bytes of t0, t1, t2).  e5m2 is the
+// upper byte of fp16, so a term is its fp16 number rounded at bit 8 (the differences are exact in
+// fp16).  Rounding leaves a signed rest of at most half a unit, so three terms of three bits hold
+// all eleven bits of fp16, down to e5m2's least number 2^-16.
 __device__ __forceinline__ void split_e5m2(const float (&x)[4], uint32_t* t0, uint32_t* t1,
                                            uint32_t* t2) {
+  constexpr uint32_t kHalf = 0x00800080u, kTop = 0xff00ff00u;
   const uint32_t a = pack_half(x[0], x[1]), b = pack_half(x[2], x[3]);
-  const uint32_t ra = half2_sub(a, a & 0xff00ff00u), rb = half2_sub(b, b & 0xff00ff00u);
-  *t0 = __byte_perm(a, b, 0x7531);
-  *t1 = __byte_perm(ra, rb, 0x7531);
-  *t2 = half2_to_e5m2(half2_sub(ra, ra & 0xff00ff00u)) |
-        half2_to_e5m2(half2_sub(rb, rb & 0xff00ff00u)) << 16;
+  const uint32_t ah = a + kHalf, bh = b + kHalf;
+  const uint32_t ra = half2_sub(a, ah & kTop), rb = half2_sub(b, bh & kTop);
+  const uint32_t am = ra + kHalf, bm = rb + kHalf;
+  *t0 = __byte_perm(ah, bh, 0x7531);
+  *t1 = __byte_perm(am, bm, 0x7531);
+  *t2 = half2_to_e5m2(half2_sub(ra, am & kTop)) | half2_to_e5m2(half2_sub(rb, bm & kTop)) << 16;
 }
 
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 || warp == 3) {
     // =================================================== producers: warp 0 K, warp 3 V.  The ring
     // holds, tile by tile of an item of n: K_0, K_1 V_0, K_2 V_1, ..., K_(n-1) V_(n-2), V_(n-1).
-    const bool is_v = warp == 3, leader = elect_one();
+    const bool is_v = warp == 3;
     const CUtensorMap* map = is_v ? &map_v : &map_k;
     const int shift = p.a.cache.page_shift, per = kKeys >> shift, page = 1 << shift;
     const int head_rows = p.a.cache.H << shift;       // rows of a page, all heads
@@ -397,17 +400,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t slot = ring % Z::kSlots, use = ring / Z::kSlots;
         if (use > 0) wait(bar_empty + 8 * slot, (use - 1) & 1, sAbort);
         if (__any_sync(0xffffffffu, *sAbort)) return;
-        if (leader) mbar_arrive_expect_tx(bar_full + 8 * slot, Z::kSlotBytes);
+        if (lane == 0) mbar_arrive_expect_tx(bar_full + 8 * slot, Z::kSlotBytes);
         const uint32_t dst = sb + Z::kRing + slot * Z::kSlotBytes;
-        for (int i = 0; i < per; ++i) {
-          const int at = __shfl_sync(0xffffffffu, row, i);
-          if (leader) {
+        __syncwarp();
+        if (lane < per) {
 #pragma unroll
-            for (int k = 0; k < Z::kSlotBytes / (16 * KB); ++k)
-              tma_load_3d(dst + k * 16 * KB + (i << (shift + 7)), map,
-                          (s * (Z::kSlotBytes / (16 * KB)) + k) * Z::kElem, at, 0,
-                          bar_full + 8 * slot);
-          }
+          for (int k = 0; k < Z::kSlotBytes / (16 * KB); ++k)
+            tma_load_3d(dst + k * 16 * KB + (lane << (shift + 7)), map,
+                        (s * (Z::kSlotBytes / (16 * KB)) + k) * Z::kElem, row, 0,
+                        bar_full + 8 * slot);
         }
         __syncwarp();
         last = ring + 1;
@@ -577,8 +578,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float coef = p.a.scale == 0.0f ? 1.0f : fabsf(p.a.scale) * kLog2e;
     const uint32_t flip = p.a.scale < 0.0f ? 0x80008000u : 0u;
     const uint32_t keep = p.a.scale == 0.0f ? 0u : ~0u;
-    // bf16: P up to 2^kSlack.  8-bit: P up to 2^15 (of e5m2's 57344), its reference 12 below
-    constexpr float kSlack = kF8 ? 3.0f : 8.0f, kLift = kF8 ? 12.0f : 0.0f;
+    // P may reach 2^kSlack over the reference: bf16 has fp32's range, so 32 leaves O and l far
+    // from overflow and a raise to rows whose first tile says little; e5m2 ends at 57344, so the
+    // reference lies kLift below the maximum and P starts at 2^kLift
+    constexpr float kSlack = kF8 ? 7.0f : 32.0f, kLift = kF8 ? 8.0f : 0.0f;
     uint32_t g = 0;
     // Q: an item's rows, dealt to the warps and gathered into the swizzled K-major layout (small
     // loops: this code runs once an item and its instructions come from L2).  8-bit: a row's
@@ -711,7 +714,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                   make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
-        if (live && half == 0) (done.prefix ? p.ml_p : p.ml_s)[slot * stored + r] = make_float2(m, l);
+        // m = -inf says that the row saw nothing; a row of NaN scores did
+        if (live && half == 0)
+          (done.prefix ? p.ml_p : p.ml_s)[slot * stored + r] = make_float2(l == l ? m : 0.0f, l);
         tc_fence_before();
       }
       if (!more) break;

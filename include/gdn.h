@@ -474,8 +474,8 @@ gdn_status gdn_kv_cache_read(const gdn_kv_cache* cache, int32_t n, const int32_t
  * codes).  Cache entries at and past a sequence's length may hold anything, NaN included.
  * The lengths stay on the device, so a captured graph can be replayed as they grow.
  * Accuracy: exact products of bf16 (or e4m3) operands, fp32 scores and softmax statistics; the
- * probabilities are rounded to bf16 (bf16 cache) or to nine significant bits (e4m3 cache) as
- * operands of the second product.
+ * probabilities enter the second product with 16 significant bits (bf16 cache: two bf16 terms)
+ * or 11 (e4m3 cache: three e5m2 terms), down to 2^-24 of their row's first tile's largest there.
  */
 size_t gdn_prefix_attention_workspace_size(int32_t batch, int32_t seqlen, int32_t num_heads,
                                            int32_t num_kv_heads, int32_t head_dim);

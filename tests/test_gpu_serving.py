@@ -425,6 +425,30 @@ def test_attention_records_bad_lengths_and_pages(gdn):
     assert torch.equal(good, again)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "f8"])
+def test_attention_nan_stays_in_its_rows(gdn, fmt):
+    """A query with a NaN or an infinity makes its own rows NaN, and a NaN key the rows that see
+    it; the other rows keep their bits."""
+    case = _attention_case(2, 3, 8, 2, 128, 300, [3, 200], 32, fmt, seed=61)
+    good, glse = _attend(gdn, case)
+    q = case["q"].clone()
+    q[0, 1, 3, 5] = math.nan
+    q[1, 2, 6, 0] = math.inf
+    out, lse = _attend(gdn, case, q=q)
+    bad = torch.zeros(q.shape[:3], dtype=torch.bool, device="cuda")
+    bad[0, 1, 3] = bad[1, 2, 6] = True
+    assert bool(out[bad].isnan().all()) and bool(lse[bad].isnan().all())
+    assert torch.equal(out[~bad], good[~bad]) and torch.equal(lse[~bad], glse[~bad])
+    # the last own token of sequence 1: seen by its last query alone
+    page, off = case["pages"][1][199 // 32], 199 % 32
+    case["cache"]["k"].view(torch.uint8)[page, 0, off] = 0x7f if fmt == "f8" else 0xff
+    out, lse = _attend(gdn, case)
+    bad = torch.zeros(q.shape[:3], dtype=torch.bool, device="cuda")
+    bad[1, 2, :4] = True
+    assert bool(lse[bad].isnan().all()) and bool(out[bad].isnan().all())
+    assert torch.equal(out[~bad], good[~bad])
+
+
 def test_attention_no_tokens(gdn):
     case = _attention_case(1, 1, 4, 1, 128, 16, [1], 16, "bf16", seed=51)
     q = case["q"][:, :0]
