@@ -6,18 +6,19 @@
 // entropy is ln 2 (log2 z - w / z): centred on m, so that nothing cancels and nothing overflows
 // however large the logits are.
 //
-// The alternatives ride along: a CTA holds a threshold, a lower bound of the k-th best, and only
-// logits at or above it go to a buffer in shared memory: almost none after the first ones.  The
-// first threshold comes from the threads' maxima over their first logits: the least over the
-// CTA's 8 warps of the ceil(k / 8)-th largest of a warp's, which at least k logits reach.  When
-// the buffer fills, the best k stay and the k-th is the new threshold.  A logit and its index make
-// one 64-bit key, ordered by value (NaN first, -0 equal to 0) and then by lower index; keys are
-// distinct, so what is kept does not depend on the order in which threads arrive.
+// The alternatives ride along as vectors of 16 bytes, each under its largest logit: the k vectors
+// with the largest ones hold the k best logits.  (A logit of another vector is beaten by the
+// largest of each of the k.  Vectors are consecutive, so this holds for equal values too, which go
+// by the lower index.)  A warp keeps its best 32 vectors in order, one a lane, and one vote a
+// vector and warp almost always says that nothing changes.  A single better one is inserted (a
+// ballot gives its place, a shuffle moves the rest up); many at once are sorted and merged, 32 at a
+// time.  A value and an index make one 64-bit key, ordered by value (NaN first, -0 equal to 0) and
+// then by lower index; keys are distinct, so the result depends on no order of execution.
 //
-// All rows lie on one line of granules (kThreads x 32 bytes, the last of a row shorter); CTA c of
-// the grid takes the c-th equal part of it, so one long row fills the GPU as well as a thousand.
-// A CTA's piece of a row leaves its statistics and best k; a second, small kernel joins a row's
-// pieces.
+// All rows lie on one line of granules (32 lanes x 32 bytes, the last of a row shorter), cut into
+// equal parts, a warp's each, so that one long row fills the GPU as well as twenty thousand short
+// ones; no warp waits for another.  What a warp has of a row leaves its statistics and best k
+// vectors; a second, small kernel joins a row's pieces and reads the logits of its best vectors.
 //
 // Bound by memory: each logit is read once.  At the copy rate an SM gets 12 bf16 logits a cycle,
 // for which it can issue 128 lane operations; a logit takes about six (packed fp32 pairs where
@@ -41,15 +42,15 @@ namespace {
 typedef unsigned long long Key;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 4, kCtas = 152 * kCtasPerSm;
-constexpr int kBuffer = 1024;              // candidates (of keys) in shared memory
+constexpr int kCtasPerSm = 4, kParts = 152 * kCtasPerSm * kWarps;
+constexpr int kLogitsAhead = 4;            // of a lane, in the joining kernel
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <typename T>
 struct Granule {
   static constexpr int kVec = 16 / (int)sizeof(T);     // logits of a 16-byte vector
-  static constexpr int kPer = 2 * kVec;                // of a thread
-  static constexpr int kLogits = kThreads * kPer;
+  static constexpr int kPer = 2 * kVec;                // of a lane
+  static constexpr int kLogits = 32 * kPer;
 };
 
 // m = -inf: no logit above -inf.  A NaN among the logits: z is NaN.
@@ -88,82 +89,65 @@ __device__ __forceinline__ float bits_value(uint32_t u) {
   return u == 0xffffffffu ? NAN : __uint_as_float((u & 0x80000000u) ? u & 0x7fffffffu : ~u);
 }
 
-// A lower bound of the k-th largest of the CTA's `mine` (as order bits): see above.  Two barriers.
-__device__ __forceinline__ uint32_t kth_bound(uint32_t mine, int k, uint32_t* s_warp) {
-  uint32_t top = 0;
-  for (int i = 0; i < (k + kWarps - 1) / kWarps; ++i) {
-    top = __reduce_max_sync(0xffffffffu, mine);
-    // one holder of the maximum leaves
-    const uint32_t who = __ballot_sync(0xffffffffu, mine == top);
-    if ((threadIdx.x & 31) == __ffs(who) - 1) mine = 0;
-  }
-  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = top;
-  __syncthreads();
-  uint32_t least = s_warp[0];
-#pragma unroll
-  for (int i = 1; i < kWarps; ++i) least = min(least, s_warp[i]);
-  __syncthreads();
-  return least;
-}
+__device__ __forceinline__ Key key_max(Key a, Key b) { return a > b ? a : b; }
+__device__ __forceinline__ Key key_min(Key a, Key b) { return a > b ? b : a; }
 
-struct TopShared {
-  Key buf[kBuffer];
-  Key best[32];
-  uint32_t warp[kWarps];
-  int count;
+// The warp's best 32 keys so far, lane i the i-th (0: none); `floor` is the k-th.
+struct Best {
+  Key mine, floor;
+
+  __device__ __forceinline__ void start() { mine = floor = 0; }
+  __device__ __forceinline__ void set_floor(int k) {
+    floor = __shfl_sync(0xffffffffu, mine, k - 1);
+  }
+  __device__ __forceinline__ static Key exchange(Key x, int o, bool larger) {
+    const Key y = __shfl_xor_sync(0xffffffffu, x, o);
+    return larger ? key_max(x, y) : key_min(x, y);
+  }
+  // 32 keys, one a lane, into descending order (bitonic)
+  __device__ __forceinline__ static Key sorted(Key x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int n = 2; n <= 32; n <<= 1)
+#pragma unroll
+      for (int o = n >> 1; o > 0; o >>= 1)
+        x = exchange(x, o, ((lane & o) == 0) == ((lane & n) == 0 || n == 32));
+    return x;
+  }
+  // 32 keys in descending order join
+  __device__ __forceinline__ void join(Key other, int k) {
+    const int lane = threadIdx.x & 31;
+    mine = key_max(mine, __shfl_sync(0xffffffffu, other, 31 - lane));   // the best 32, bitonic
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine = exchange(mine, o, (lane & o) == 0);
+    set_floor(k);
+  }
+  // each lane's key, those above the floor join (all lanes)
+  __device__ __forceinline__ void offer(Key key, int k) {
+    uint32_t who = __ballot_sync(0xffffffffu, key > floor);
+    if (__popc(who) > 6) {                 // about what sorting and merging costs in insertions
+      join(sorted(key > floor ? key : 0), k);
+      return;
+    }
+    const int lane = threadIdx.x & 31;
+    while (who) {
+      const Key one = __shfl_sync(0xffffffffu, key, __ffs(who) - 1);
+      who &= who - 1;
+      const int place = __popc(__ballot_sync(0xffffffffu, mine > one));
+      const Key up = __shfl_up_sync(0xffffffffu, mine, 1);
+      mine = lane < place ? mine : lane == place ? one : up;
+    }
+    set_floor(k);
+  }
 };
 
-// The best k of the buffered keys, in order, at the buffer's start; `count` becomes at most k.
-// All threads; a key's rank is the number of larger ones.
-__device__ __forceinline__ void compact(TopShared* s, int k) {
-  __syncthreads();
-  const int n = min(s->count, kBuffer);
-  if (threadIdx.x < 32) s->best[threadIdx.x] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const Key mine = s->buf[i];
-    int rank = 0;
-#pragma unroll 8
-    for (int j = 0; j < n; ++j) rank += s->buf[j] > mine;
-    if (rank < k) s->best[rank] = mine;
-  }
-  __syncthreads();
-  if (threadIdx.x < k) s->buf[threadIdx.x] = s->best[threadIdx.x];
-  if (threadIdx.x == 0) s->count = min(n, k);
-  __syncthreads();
-}
-
-// Offers the thread's keys (key_at(e), e < n <= 32) above *floor to the buffer; when it is full,
-// the best k stay, the floor rises and what is left is offered again.  All threads.
-template <int n, typename F>
-__device__ __forceinline__ void offer(TopShared* s, int k, bool any, Key* floor, F key_at) {
-  uint32_t left = any ? (n == 32 ? ~0u : (1u << n) - 1) : 0u;
-  for (;;) {
-    if (left) {
-#pragma unroll
-      for (int e = 0; e < n; ++e) {
-        if (!(left >> e & 1)) continue;
-        const Key key = key_at(e);
-        if (key > *floor) {
-          const int at = atomicAdd(&s->count, 1);
-          if (at >= kBuffer) continue;                // stays on the list
-          s->buf[at] = key;
-        }
-        left &= ~(1u << e);
-      }
-    }
-    if (!__syncthreads_or(left != 0)) return;
-    compact(s, k);
-    *floor = s->buf[k - 1];                           // (it was full: there are k)
-  }
-}
-
 struct Pieces {                            // how the line is cut
-  long long granules;                      // of a row
-  int ctas;                                // that have a part
+  long long total;                         // granules of all rows
+  int granules;                            // of a row
+  int parts;                               // equal parts of the line, a warp's each
   float c;                                 // scale log2 e
-  float4* stats;                           // [row + cta]: m, z, w
-  Key* keys;                               // [row + cta][k]
+  float4* stats;                           // [row + part]: m, z, w
+  Key* keys;                               // [row + part][k]: vectors, in order
 };
 
 __device__ __forceinline__ unsigned long long pair(float a, float b) {
@@ -195,6 +179,34 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The largest logits of two vectors (NaN where there is one) and the least of both.
+__device__ __forceinline__ float top_of(uint32_t hi) {
+  return max_nan(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+}
+__device__ __forceinline__ void range(const uint4& u, const uint4& v, const __nv_bfloat16*,
+                                      const float*, float (&top)[2], float* least) {
+  top[0] = top_of(max2_nan(max2_nan(u.x, u.y), max2_nan(u.z, u.w)));
+  top[1] = top_of(max2_nan(max2_nan(v.x, v.y), max2_nan(v.z, v.w)));
+  const uint32_t lo = min2(min2(min2(u.x, u.y), min2(u.z, u.w)), min2(min2(v.x, v.y), min2(v.z, v.w)));
+  *least = fminf(__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u));
+}
+__device__ __forceinline__ void range(const uint4&, const uint4&, const float*, const float* f,
+                                      float (&top)[2], float* least) {
+  top[0] = max_nan(max_nan(f[0], f[1]), max_nan(f[2], f[3]));
+  top[1] = max_nan(max_nan(f[4], f[5]), max_nan(f[6], f[7]));
+  *least = fminf(fminf(fminf(f[0], f[1]), fminf(f[2], f[3])),
+                 fminf(fminf(f[4], f[5]), fminf(f[6], f[7])));
+}
 
 __device__ __forceinline__ void widen(const uint4& u, const __nv_bfloat16*, float* x) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -210,11 +222,13 @@ __device__ __forceinline__ void widen(const uint4& u, const float*, float* x) {
   x[2] = __uint_as_float(u.z);
   x[3] = __uint_as_float(u.w);
 }
-__device__ __forceinline__ uint4 no_logits(const __nv_bfloat16*) {
-  return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-}
-__device__ __forceinline__ uint4 no_logits(const float*) {
-  return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+template <typename T>
+__device__ __forceinline__ uint4 load_inner(const T* at) {
+  uint4 u;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "l"(at));
+  return u;
 }
 
 // 16 bytes of logits from the 16-byte boundary at or below row + i on (i: the index of the first,
@@ -222,80 +236,89 @@ __device__ __forceinline__ uint4 no_logits(const float*) {
 template <typename T>
 __device__ __forceinline__ uint4 load_vec(const T* row, long long i, int V) {
   constexpr int kVec = Granule<T>::kVec;
-  if (i >= 0 && i + kVec <= V) {
-    uint4 u;
-    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];\n"
-                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                 : "l"(row + i));
-    return u;
-  }
-  uint4 u = no_logits(row);
-  if (i + kVec <= 0 || i >= V) return u;
-  T* e = reinterpret_cast<T*>(&u);
+  if (i >= 0 && i + kVec <= V) return load_inner(row + i);
+  uint32_t w[4];
+  constexpr int kWord = kVec / 4;                     // logits of a 32-bit word
 #pragma unroll
-  for (int q = 0; q < kVec; ++q)
-    if (i + q >= 0 && i + q < V) e[q] = row[i + q];
-  return u;
+  for (int q = 0; q < 4; ++q) {
+    w[q] = kWord == 2 ? 0xff80ff80u : 0xff800000u;    // -inf
+#pragma unroll
+    for (int b = 0; b < kWord; ++b) {
+      const long long at = i + q * kWord + b;
+      if (at < 0 || at >= V) continue;
+      if constexpr (kWord == 1) w[q] = reinterpret_cast<const uint32_t*>(row)[at];
+      else
+        w[q] = (w[q] & (0xffff0000u >> (16 * b))) |
+               (uint32_t)reinterpret_cast<const uint16_t*>(row)[at] << (16 * b);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T>
+__device__ __forceinline__ int shift_of(const T* row) {   // logits from its 16-byte boundary to a row
+  return (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
 }
 
 template <typename T, bool kTop, bool kEntropy>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     gdn_token_logprobs_kernel(GdnLogprobArgs a, Pieces p) {
   using G = Granule<T>;
-  __shared__ TopShared s_top;
-  __shared__ Stats s_stats[kWarps];
-  const int tid = threadIdx.x, cta = blockIdx.x;
+  constexpr int kDepth = 2;                           // granules on the way
+  const int lane = threadIdx.x & 31, part = blockIdx.x * kWarps + (threadIdx.x >> 5);
   pdl_trigger();                                      // the joining kernel may be set up
-  const long long total = p.granules * a.N;
-  long long at = total * cta / p.ctas;
-  const long long end = total * (cta + 1) / p.ctas;
-  int row = (int)(at / p.granules);
-  long long q = at - row * p.granules;                // granule of the row
+  if (part >= p.parts) return;
+  const long long start = p.total * part / p.parts;
+  int left = (int)(p.total * (part + 1) / p.parts - start);
+  int row = (int)(start / p.granules);
+  int q = (int)(start - (long long)row * p.granules); // granule of the row
   const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
-  // the row's first vector starts at its 16-byte boundary: `shift` logits before it
-  auto shift_of = [&](const T* r) {
-    return (int)((reinterpret_cast<uintptr_t>(r) & 15) / sizeof(T));
-  };
-  int shift = shift_of(x);
-  auto index = [&](long long g, int v) {
-    return (g * 2 + v) * (long long)(kThreads * G::kVec) + tid * G::kVec - shift;
-  };
-  uint4 next[2];
+  // the granules ahead: (row, granule) of the next to be loaded and this lane's place in it
+  const T* ax = x;
+  int aq = q, aleft = left;
+  const T* ap = ax - shift_of(ax) + (long long)aq * G::kLogits + lane * G::kVec;
+  uint4 ahead[kDepth][2];
+  auto load = [&](uint4 (&to)[2]) {
+    if (aleft <= 0) return;
+    if (aq > 0 && aq + 2 < p.granules) {              // all of it the row's
 #pragma unroll
-  for (int v = 0; v < 2; ++v) next[v] = load_vec(x, index(q, v), a.V);
-  while (at < end) {
-    // ---- this CTA's piece of a row: granules [q, q1)
-    const long long left = end - at;
-    const long long q1 = q + left < p.granules ? q + left : p.granules;
+      for (int v = 0; v < 2; ++v) to[v] = load_inner(ap + v * 32 * G::kVec);
+    } else {
+#pragma unroll
+      for (int v = 0; v < 2; ++v) to[v] = load_vec(ax, ap - ax + v * 32 * G::kVec, a.V);
+    }
+    --aleft;
+    ap += G::kLogits;
+    if (++aq == p.granules) {
+      aq = 0;
+      ax += a.row_stride;
+      ap = ax - shift_of(ax) + lane * G::kVec;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i) load(ahead[i]);
+  const unsigned long long c2 = pair(p.c, p.c);
+  while (left > 0) {
+    // ---- this warp's granules of a row
     float m = -INFINITY;
     unsigned long long z2 = 0, w2 = 0;                // pairs of sums
     bool nan = false;
-    Key floor = 0;
-    bool first = true;
-    const unsigned long long c2 = pair(p.c, p.c);
-    for (; q < q1; ++q, ++at) {
-      uint4 now[2] = {next[0], next[1]};
-      const long long i0 = index(q, 0), i1 = index(q, 1);
-      // the granule after this one, of this row or the next
-      if (at + 1 < end) {
-        if (q + 1 == p.granules) {
-          const T* nx = x + a.row_stride;
-          const int keep = shift;
-          shift = shift_of(nx);
+    Best best;
+    best.start();
+    float floor = -INFINITY;                          // the value of the best ones' floor
+    const int q0 = q, q1 = q + left < p.granules ? q + left : p.granules;
+    for (; q < q1; ++q) {
+      float f[G::kPer], tops[2], least;
+      widen(ahead[0][0], x, f);
+      widen(ahead[0][1], x, f + G::kVec);
+      range(ahead[0][0], ahead[0][1], x, f, tops, &least);
 #pragma unroll
-          for (int v = 0; v < 2; ++v) next[v] = load_vec(nx, index(0, v), a.V);
-          shift = keep;
-        } else {
-#pragma unroll
-          for (int v = 0; v < 2; ++v) next[v] = load_vec(x, index(q + 1, v), a.V);
-        }
+      for (int i = 0; i + 1 < kDepth; ++i) {
+        ahead[i][0] = ahead[i + 1][0];
+        ahead[i][1] = ahead[i + 1][1];
       }
-      float f[G::kPer];
-      widen(now[0], x, f);
-      widen(now[1], x, f + G::kVec);
-      float top = f[0];
-#pragma unroll
-      for (int e = 1; e < G::kPer; ++e) top = max_nan(top, f[e]);
+      load(ahead[kDepth - 1]);
+      const float top = max_nan(tops[0], tops[1]);
       nan = nan || top != top;
       if (top > m) {                                  // seldom after the first granules
         const float d = (m - top) * p.c, s = ptx::ex2_approx(d);
@@ -308,8 +331,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         m = top;
       }
-      if (m != -INFINITY) {
-        const unsigned long long minus_m = pair(-m, -m);
+      const unsigned long long minus_m = pair(-m, -m);
+      if (!kEntropy || (least > -1e30f && m < 1e30f)) {   // no t is infinite
+        if (m != -INFINITY) {
+#pragma unroll
+          for (int e = 0; e < G::kPer; e += 2) {
+            const unsigned long long t2 = mul2(add2(pair(f[e], f[e + 1]), minus_m), c2);
+            float t0, t1;
+            unpair(t2, &t0, &t1);
+            const unsigned long long e2 = pair(ptx::ex2_approx(t0), ptx::ex2_approx(t1));
+            z2 = add2(z2, e2);
+            if (kEntropy) w2 = fma2(e2, t2, w2);
+          }
+        }
+      } else if (m != -INFINITY) {
 #pragma unroll
         for (int e = 0; e < G::kPer; e += 2) {
           float t0, t1;
@@ -317,75 +352,115 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           const unsigned long long e2 = pair(ptx::ex2_approx(t0), ptx::ex2_approx(t1));
           z2 = add2(z2, e2);
           // 0 * -inf is no part of the sum
-          if (kEntropy) w2 = fma2(e2, pair(fmaxf(t0, -1000.0f), fmaxf(t1, -1000.0f)), w2);
+          w2 = fma2(e2, pair(fmaxf(t0, -1000.0f), fmaxf(t1, -1000.0f)), w2);
         }
       }
       if constexpr (kTop) {
-        if (first) {
-          if (tid == 0) s_top.count = 0;
-          const uint32_t bound = kth_bound(order_bits(top), a.top_k, s_top.warp);
-          floor = bound ? ((Key)bound << 32) - 1 : 0;
-          first = false;
+        // (as long as there are fewer than k, the floor's value is the order's least: NaN)
+        if (q == q0 || __any_sync(0xffffffffu, !(top < floor))) {
+          const int v0 = q * 64 + lane;               // the vectors' indices in the row
+          best.offer(order_key(tops[0], v0), a.top_k);
+          best.offer(order_key(tops[1], v0 + 32), a.top_k);
+          floor = bits_value((uint32_t)(best.floor >> 32));
         }
-        auto key_at = [&](int e) {
-          return order_key(f[e], (int)(e < G::kVec ? i0 + e : i1 + e - G::kVec));
-        };
-        // (index 0 ranks first among equal values)
-        offer<G::kPer>(&s_top, a.top_k, order_key(top, 0) > floor, &floor, key_at);
       }
     }
-    // ---- the piece's statistics and best k
+    left -= q1 - q0;
+    // ---- the statistics and best k of them
     float z0, z1, w0, w1;
     unpair(z2, &z0, &z1);
     unpair(w2, &w0, &w1);
-    Stats st{m, nan ? NAN : z0 + z1, w0 + w1};
-    st = warp_merge(st, p.c);
-    if ((tid & 31) == 0) s_stats[tid >> 5] = st;
-    __syncthreads();
-    if (tid == 0) {
-#pragma unroll
-      for (int i = 1; i < kWarps; ++i) st = merge(st, s_stats[i], p.c);
-      p.stats[(long long)row + cta] = make_float4(st.m, st.z, st.w, 0.0f);
-    }
-    if constexpr (kTop) {
-      compact(&s_top, a.top_k);
-      if (tid < a.top_k)
-        p.keys[((long long)row + cta) * a.top_k + tid] = tid < s_top.count ? s_top.buf[tid] : 0;
-    }
-    __syncthreads();
+    const Stats st = warp_merge(Stats{m, nan ? NAN : z0 + z1, w0 + w1}, p.c);
+    const long long slot = (long long)row + part;
+    if (lane == 0) p.stats[slot] = make_float4(st.m, st.z, st.w, 0.0f);
+    if (kTop && lane < a.top_k) p.keys[slot * a.top_k + lane] = best.mine;
     if (q == p.granules) {
       q = 0;
       ++row;
       x += a.row_stride;
-      shift = shift_of(x);
     }
   }
 }
 
-// Joins a row's pieces: one CTA a row (a warp's worth without alternatives).
-template <typename T, bool kTop>
-__global__ void __launch_bounds__(kTop ? kThreads : 32)
-    gdn_token_logprobs_join_kernel(GdnLogprobArgs a, Pieces p) {
-  const int row = blockIdx.x, tid = threadIdx.x;
+// Joins a row's pieces: kRowWarps warps a row (1: a few pieces; 8: many, which the warps share).
+template <typename T, bool kTop, int kRowWarps>
+__global__ void __launch_bounds__(kThreads) gdn_token_logprobs_join_kernel(GdnLogprobArgs a, Pieces p) {
+  __shared__ Stats s_stats[kWarps];
+  __shared__ Key s_best[kWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = kRowWarps == 1 ? 0 : warp;
+  const long long row = kRowWarps == 1 ? (long long)blockIdx.x * kWarps + warp : blockIdx.x;
+  if (row >= a.N) return;                             // (whole blocks where warps share a row)
   const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
-  const long long total = p.granules * a.N, x0 = row * p.granules, x1 = x0 + p.granules - 1;
-  // the CTAs that hold the row's first and last granule
-  const int c0 = (int)(((x0 + 1) * p.ctas - 1) / total), c1 = (int)(((x1 + 1) * p.ctas - 1) / total);
+  const long long x0 = row * p.granules, x1 = x0 + p.granules - 1;
+  // the parts that hold the row's first and last granule
+  const int c0 = (int)(((x0 + 1) * p.parts - 1) / p.total);
+  const int pieces = (int)(((x1 + 1) * p.parts - 1) / p.total) - c0 + 1;
+  const int id = a.logprobs && sub == 0 ? a.targets[row] : -1;
   pdl_wait();
   Stats st{-INFINITY, 0.0f, 0.0f};
-  if (tid < 32) {
-    for (int c = c0 + tid; c <= c1; c += 32) {
-      const float4 v = p.stats[(long long)row + c];
+  Best best;
+  best.start();
+  for (int i0 = sub * 32; i0 < pieces; i0 += kRowWarps * 32) {
+    const bool mine = i0 + lane < pieces;
+    const long long slot = row + c0 + i0 + lane;
+    if (mine) {
+      const float4 v = p.stats[slot];
       st = merge(st, Stats{v.x, v.y, v.z}, p.c);
     }
-    st = warp_merge(st, p.c);
+    if constexpr (kTop) {
+      // 32 lists a turn, one a lane: their first keys, then the next of those whose last one
+      // was good enough
+      const int k = a.top_k;
+      const Key* keys = p.keys + slot * k;
+      Key key = mine ? keys[0] : 0;
+      for (int i = 1; __any_sync(0xffffffffu, key > best.floor); ++i) {
+        const bool more = key > best.floor && i < k;
+        best.offer(key, k);
+        key = more ? keys[i] : 0;
+      }
+    }
+  }
+  st = warp_merge(st, p.c);
+  if constexpr (kRowWarps > 1) {
+    if (lane == 0) s_stats[warp] = st;
+    if (kTop) s_best[warp][lane] = best.mine;
+    __syncthreads();
+    if (warp > 0) return;
+    st = warp_merge(lane < kWarps ? s_stats[lane] : Stats{-INFINITY, 0.0f, 0.0f}, p.c);
+    if constexpr (kTop)
+      for (int i = 1; i < kWarps; ++i)
+        if (__any_sync(0xffffffffu, s_best[i][lane] > best.floor)) best.join(s_best[i][lane], a.top_k);
+  }
+  if constexpr (kTop) {
+    // the logits of the best k vectors, a lane one at a time
+    constexpr int kVec = Granule<T>::kVec;
+    const int shift = shift_of(x), n = a.top_k * kVec;
+    const Key vector = best.mine;
+    best.start();
+    for (int i0 = 0; i0 < n; i0 += 32 * kLogitsAhead) {
+      Key key[kLogitsAhead];
+#pragma unroll
+      for (int j = 0; j < kLogitsAhead; ++j) {
+        const int i = i0 + j * 32 + lane;
+        const Key v = __shfl_sync(0xffffffffu, vector, (i / kVec) & 31);
+        const long long at = (long long)(uint32_t)~(uint32_t)v * kVec + i % kVec - shift;
+        key[j] = i < n && v != 0 && at >= 0 && at < a.V ? order_key(ld_elem(x + at), (int)at) : 0;
+      }
+#pragma unroll 1
+      for (int j = 0; j < kLogitsAhead; ++j) {
+        Key one = key[0];
+#pragma unroll
+        for (int i = 1; i < kLogitsAhead; ++i) one = j == i ? key[i] : one;
+        best.offer(one, a.top_k);
+      }
+    }
   }
   const bool dead = st.m == -INFINITY && st.z == 0.0f;  // every logit -inf
   const float log2z = log2f(st.z);
   auto logp = [&](float v) { return dead ? -INFINITY : (v - st.m) * a.scale - kLn2 * log2z; };
-  if (tid == 0) {
+  if (lane == 0) {
     if (a.logprobs) {
-      const int id = a.targets[row];
       float lp = 0.0f;
       if (id >= a.V) {
         atomicOr(&g_err_lp, kErrIndex);
@@ -397,49 +472,33 @@ __global__ void __launch_bounds__(kTop ? kThreads : 32)
     }
     if (a.entropy) a.entropy[row] = dead ? 0.0f : kLn2 * (log2z - st.w / st.z);
   }
-  if constexpr (kTop) {
-    __shared__ TopShared s_top;
-    const int k = a.top_k;
-    const long long n = (long long)(c1 - c0 + 1) * k;
-    const Key* keys = p.keys + ((long long)row + c0) * k;   // the pieces' lists lie side by side
-    Key best = 0;
-    for (long long i = tid; i < n; i += kThreads) {
-      const Key key = keys[i];
-      best = key > best ? key : best;
-    }
-    if (tid == 0) s_top.count = 0;
-    const uint32_t bound = kth_bound((uint32_t)(best >> 32), k, s_top.warp);
-    Key floor = bound ? ((Key)bound << 32) - 1 : 0;
-    for (long long i0 = 0; i0 < n; i0 += kThreads) {
-      const Key key = i0 + tid < n ? keys[i0 + tid] : 0;
-      offer<1>(&s_top, k, key > floor, &floor, [&](int) { return key; });
-    }
-    compact(&s_top, k);
-    if (tid < k) {
-      const Key key = s_top.buf[tid];
-      const uint32_t bits = (uint32_t)(key >> 32);
-      a.top_ids[(long long)row * k + tid] = (int)~(uint32_t)key;
-      a.top_logprobs[(long long)row * k + tid] = logp(bits_value(bits));
-    }
+  if (kTop && lane < a.top_k) {
+    a.top_ids[row * a.top_k + lane] = (int)~(uint32_t)best.mine;
+    a.top_logprobs[row * a.top_k + lane] = logp(bits_value((uint32_t)(best.mine >> 32)));
   }
 }
 
-template <typename T>
-long long granules_of(int V) {             // with up to a vector's worth of shift
-  return ((long long)V + Granule<T>::kVec - 1 + Granule<T>::kLogits - 1) / Granule<T>::kLogits;
+int granules_of(int V, int bf16) {         // with up to a vector's worth of shift
+  const int vec = bf16 ? Granule<__nv_bfloat16>::kVec : Granule<float>::kVec;
+  const int per = bf16 ? Granule<__nv_bfloat16>::kLogits : Granule<float>::kLogits;
+  return (int)(((long long)V + vec - 1 + per - 1) / per);
 }
-long long granules_of(int V, int bf16) {
-  return bf16 ? granules_of<__nv_bfloat16>(V) : granules_of<float>(V);
-}
-size_t stats_bytes(int N) { return (sizeof(float4) * ((size_t)N + kCtas) + 255) & ~(size_t)255; }
+
+size_t slots(int N) { return (size_t)N + kParts; }
+size_t stats_bytes(int N) { return (sizeof(float4) * slots(N) + 255) & ~(size_t)255; }
 
 template <typename T, bool kTop, bool kEntropy>
 cudaError_t launch(const GdnLogprobArgs& a, const Pieces& p, cudaStream_t stream) {
-  gdn_token_logprobs_kernel<T, kTop, kEntropy><<<p.ctas, kThreads, 0, stream>>>(a, p);
+  const int grid = (p.parts + kWarps - 1) / kWarps;
+  gdn_token_logprobs_kernel<T, kTop, kEntropy><<<grid, kThreads, 0, stream>>>(a, p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_pdl(true, gdn_token_logprobs_join_kernel<T, kTop>, dim3((unsigned)a.N),
-                    dim3(kTop ? kThreads : 32), 0, stream, a, p);
+  // a row's pieces: about parts / rows
+  if (grid > a.N)
+    return launch_pdl(true, gdn_token_logprobs_join_kernel<T, kTop, kWarps>, dim3((unsigned)a.N),
+                      dim3(kThreads), 0, stream, a, p);
+  return launch_pdl(true, gdn_token_logprobs_join_kernel<T, kTop, 1>,
+                    dim3((unsigned)((a.N + kWarps - 1ll) / kWarps)), dim3(kThreads), 0, stream, a, p);
 }
 
 template <typename T>
@@ -454,14 +513,14 @@ cudaError_t launch(const GdnLogprobArgs& a, const Pieces& p, cudaStream_t stream
 size_t gdn_token_logprobs_bytes(int N, int V, int bf16, int top_k) {
   (void)V;
   (void)bf16;
-  return stats_bytes(N) + sizeof(Key) * top_k * ((size_t)N + kCtas);
+  return stats_bytes(N) + sizeof(Key) * top_k * slots(N);
 }
 
 cudaError_t gdn_launch_token_logprobs(const GdnLogprobArgs& a, cudaStream_t stream) {
   Pieces p;
   p.granules = granules_of(a.V, a.bf16);
-  const long long total = p.granules * a.N;
-  p.ctas = (int)(total < kCtas ? total : kCtas);
+  p.total = (long long)p.granules * a.N;
+  p.parts = (int)(p.total < kParts ? p.total : kParts);
   p.c = a.scale * kLog2e;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.stats = reinterpret_cast<float4*>(ws);
