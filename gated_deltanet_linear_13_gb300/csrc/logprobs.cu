@@ -6,22 +6,23 @@
 // entropy is ln 2 (log2 z - w / z): centred on m, so that nothing cancels and nothing overflows
 // however large the logits are.
 //
-// The alternatives ride along as vectors of 16 bytes, each under its largest logit: the k vectors
-// with the largest ones hold the k best logits.  (A logit of another vector is beaten by the
-// largest of each of the k.  Vectors are consecutive, so this holds for equal values too, which go
-// by the lower index.)  A warp keeps its best 32 vectors in order, one a lane, and one vote a
-// vector and warp almost always says that nothing changes.  A single better one is inserted (a
-// ballot gives its place, a shuffle moves the rest up); many at once are sorted and merged, 32 at a
-// time.  A value and an index make one 64-bit key, ordered by value (NaN first, -0 equal to 0) and
-// then by lower index; keys are distinct, so the result depends on no order of execution.
+// The alternatives cost the pass one maximum a granule (the kilobyte that a warp takes at a time).
+// The k granules with the largest maxima hold the k best logits: a logit of another granule is
+// beaten by the largest of each of the k.  (Granules are consecutive, so this holds for equal
+// values too, which go by the lower index.)  The joining kernel finds them among the row's maxima,
+// reads them again (k kilobytes of a row of hundreds), narrows them down to k vectors of 16 bytes
+// in the same way, and takes the best k of those vectors' logits.  Each time a warp keeps the best
+// 32 in order, one a lane: a single better one is inserted (a ballot gives its place, a shuffle
+// moves the rest up), many at once are sorted and merged.  A value and an index make one 64-bit
+// key, ordered by value (NaN first, -0 equal to 0) and then by lower index; keys are distinct, so
+// the result depends on no order of execution.
 //
-// All rows lie on one line of granules (32 lanes x 32 bytes, the last of a row shorter), cut into
-// equal parts, a warp's each, so that one long row fills the GPU as well as twenty thousand short
-// ones; no warp waits for another.  What a warp has of a row leaves its statistics and best k
-// vectors; a second, small kernel joins a row's pieces and reads the logits of its best vectors.
+// All rows lie on one line of granules (the last of a row shorter), cut into equal parts, a warp's
+// each, so that one long row fills the GPU as well as twenty thousand short ones; no warp waits for
+// another.
 //
 // Bound by memory: each logit is read once.  At the copy rate an SM gets 12 bf16 logits a cycle,
-// for which it can issue 128 lane operations; a logit takes about six (packed fp32 pairs where
+// for which it can issue 128 lane operations; a logit takes about nine (packed fp32 pairs where
 // there are such instructions) and one of 16 exponentials a cycle.
 #include "common.cuh"
 #include "sm100_ptx.cuh"
@@ -43,7 +44,8 @@ typedef unsigned long long Key;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 4, kParts = 152 * kCtasPerSm * kWarps;
-constexpr int kLogitsAhead = 4;            // of a lane, in the joining kernel
+// loads ahead of a lane in the joining kernel: granules' maxima, granules, logits
+constexpr int kTopsAhead = 8, kGranulesAhead = 4, kLogitsAhead = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <typename T>
@@ -92,13 +94,14 @@ __device__ __forceinline__ float bits_value(uint32_t u) {
 __device__ __forceinline__ Key key_max(Key a, Key b) { return a > b ? a : b; }
 __device__ __forceinline__ Key key_min(Key a, Key b) { return a > b ? b : a; }
 
-// The warp's best 32 keys so far, lane i the i-th (0: none); `floor` is the k-th.
+// The warp's best 32 keys so far, lane i the i-th (0: none); `floor` is the k-th, or a larger one
+// that k keys of the row are known to reach.
 struct Best {
   Key mine, floor;
 
   __device__ __forceinline__ void start() { mine = floor = 0; }
   __device__ __forceinline__ void set_floor(int k) {
-    floor = __shfl_sync(0xffffffffu, mine, k - 1);
+    floor = key_max(floor, __shfl_sync(0xffffffffu, mine, k - 1));
   }
   __device__ __forceinline__ static Key exchange(Key x, int o, bool larger) {
     const Key y = __shfl_xor_sync(0xffffffffu, x, o);
@@ -125,6 +128,7 @@ struct Best {
   // each lane's key, those above the floor join (all lanes)
   __device__ __forceinline__ void offer(Key key, int k) {
     uint32_t who = __ballot_sync(0xffffffffu, key > floor);
+    if (who == 0) return;
     if (__popc(who) > 6) {                 // about what sorting and merging costs in insertions
       join(sorted(key > floor ? key : 0), k);
       return;
@@ -139,6 +143,33 @@ struct Best {
     }
     set_floor(k);
   }
+  // N keys of each lane.  The first time, the lanes' largest come first (32 distinct keys): the
+  // floor is then near its place, and few of the others pass it.
+  template <int N>
+  __device__ __forceinline__ void offer_all(Key (&key)[N], int k) {
+    if (__shfl_sync(0xffffffffu, mine, 0) == 0) {
+      Key top = key[0];
+#pragma unroll
+      for (int i = 1; i < N; ++i) top = key_max(top, key[i]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) key[i] = key[i] == top ? 0 : key[i];
+      mine = sorted(top > floor ? top : 0);
+      set_floor(k);
+    }
+    uint32_t any = 0;                      // (one copy of the code for all N)
+#pragma unroll
+    for (int i = 0; i < N; ++i) any |= key[i] > floor ? 1u << i : 0u;
+    any = __reduce_or_sync(0xffffffffu, any);
+#pragma unroll 1
+    while (any) {
+      const int i = __ffs(any) - 1;
+      any &= any - 1;
+      Key one = key[0];
+#pragma unroll
+      for (int j = 1; j < N; ++j) one = i == j ? key[j] : one;
+      offer(one, k);
+    }
+  }
 };
 
 struct Pieces {                            // how the line is cut
@@ -147,7 +178,7 @@ struct Pieces {                            // how the line is cut
   int parts;                               // equal parts of the line, a warp's each
   float c;                                 // scale log2 e
   float4* stats;                           // [row + part]: m, z, w
-  Key* keys;                               // [row + part][k]: vectors, in order
+  uint32_t* tops;                          // [row][granule]: the largest logit's order bits
 };
 
 __device__ __forceinline__ unsigned long long pair(float a, float b) {
@@ -189,23 +220,33 @@ __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
   asm("min.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// The largest logits of two vectors (NaN where there is one) and the least of both.
-__device__ __forceinline__ float top_of(uint32_t hi) {
-  return max_nan(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+// The largest (NaN if there is one) and the least of two vectors' logits.
+__device__ __forceinline__ uint32_t max_word(const uint4& u) {
+  return max2_nan(max2_nan(u.x, u.y), max2_nan(u.z, u.w));
+}
+__device__ __forceinline__ float max_half(uint32_t w) {
+  return max_nan(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 __device__ __forceinline__ void range(const uint4& u, const uint4& v, const __nv_bfloat16*,
-                                      const float*, float (&top)[2], float* least) {
-  top[0] = top_of(max2_nan(max2_nan(u.x, u.y), max2_nan(u.z, u.w)));
-  top[1] = top_of(max2_nan(max2_nan(v.x, v.y), max2_nan(v.z, v.w)));
+                                      const float*, float* top, float* least) {
+  *top = max_half(max2_nan(max_word(u), max_word(v)));
   const uint32_t lo = min2(min2(min2(u.x, u.y), min2(u.z, u.w)), min2(min2(v.x, v.y), min2(v.z, v.w)));
   *least = fminf(__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u));
 }
 __device__ __forceinline__ void range(const uint4&, const uint4&, const float*, const float* f,
-                                      float (&top)[2], float* least) {
-  top[0] = max_nan(max_nan(f[0], f[1]), max_nan(f[2], f[3]));
-  top[1] = max_nan(max_nan(f[4], f[5]), max_nan(f[6], f[7]));
+                                      float* top, float* least) {
+  *top = max_nan(max_nan(max_nan(f[0], f[1]), max_nan(f[2], f[3])),
+                 max_nan(max_nan(f[4], f[5]), max_nan(f[6], f[7])));
   *least = fminf(fminf(fminf(f[0], f[1]), fminf(f[2], f[3])),
                  fminf(fminf(f[4], f[5]), fminf(f[6], f[7])));
+}
+// one vector's largest
+__device__ __forceinline__ float vector_top(const uint4& u, const __nv_bfloat16*) {
+  return max_half(max_word(u));
+}
+__device__ __forceinline__ float vector_top(const uint4& u, const float*) {
+  return max_nan(max_nan(__uint_as_float(u.x), __uint_as_float(u.y)),
+                 max_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
 }
 
 __device__ __forceinline__ void widen(const uint4& u, const __nv_bfloat16*, float* x) {
@@ -300,28 +341,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const unsigned long long c2 = pair(p.c, p.c);
   while (left > 0) {
     // ---- this warp's granules of a row
-    float m = -INFINITY;
+    float m = -INFINITY, mc = 0.0f, off = 0.0f;
     unsigned long long z2 = 0, w2 = 0;                // pairs of sums
     bool nan = false;
-    Best best;
-    best.start();
-    float floor = -INFINITY;                          // the value of the best ones' floor
     const int q0 = q, q1 = q + left < p.granules ? q + left : p.granules;
+#pragma unroll kDepth
     for (; q < q1; ++q) {
-      float f[G::kPer], tops[2], least;
+      float f[G::kPer], top, least;
       widen(ahead[0][0], x, f);
       widen(ahead[0][1], x, f + G::kVec);
-      range(ahead[0][0], ahead[0][1], x, f, tops, &least);
+      range(ahead[0][0], ahead[0][1], x, f, &top, &least);
 #pragma unroll
       for (int i = 0; i + 1 < kDepth; ++i) {
         ahead[i][0] = ahead[i + 1][0];
         ahead[i][1] = ahead[i + 1][1];
       }
       load(ahead[kDepth - 1]);
-      const float top = max_nan(tops[0], tops[1]);
       nan = nan || top != top;
       if (top > m) {                                  // seldom after the first granules
-        const float d = (m - top) * p.c, s = ptx::ex2_approx(d);
+        const float d = (m - top) * p.c - off, s = ptx::ex2_approx(d);
         const unsigned long long s2 = pair(s, s);
         if (s != 0.0f) {
           w2 = mul2(fma2(z2, pair(d, d), w2), s2);
@@ -330,25 +368,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           w2 = z2 = 0;
         }
         m = top;
+        mc = m * p.c;
+        off = fabsf(m) < 1e30f ? fmaf(m, p.c, -mc) : 0.0f;   // m c - mc, exactly
       }
-      const unsigned long long minus_m = pair(-m, -m);
-      if (!kEntropy || (least > -1e30f && m < 1e30f)) {   // no t is infinite
-        if (m != -INFINITY) {
+      if (least > -1e30f && m < 1e30f) {              // nothing below is infinite
+        // t = x c - mc in one rounding; t - off is meant, which the sums make up for when m
+        // changes and at the end
+        const unsigned long long minus_mc = pair(-mc, -mc);
 #pragma unroll
-          for (int e = 0; e < G::kPer; e += 2) {
-            const unsigned long long t2 = mul2(add2(pair(f[e], f[e + 1]), minus_m), c2);
-            float t0, t1;
-            unpair(t2, &t0, &t1);
-            const unsigned long long e2 = pair(ptx::ex2_approx(t0), ptx::ex2_approx(t1));
-            z2 = add2(z2, e2);
-            if (kEntropy) w2 = fma2(e2, t2, w2);
-          }
+        for (int e = 0; e < G::kPer; e += 2) {
+          const unsigned long long t2 = fma2(pair(f[e], f[e + 1]), c2, minus_mc);
+          float t0, t1;
+          unpair(t2, &t0, &t1);
+          const unsigned long long e2 = pair(ptx::ex2_approx(t0), ptx::ex2_approx(t1));
+          z2 = add2(z2, e2);
+          if (kEntropy) w2 = fma2(e2, t2, w2);
         }
       } else if (m != -INFINITY) {
+        const unsigned long long minus_m = pair(-m, -m);
 #pragma unroll
         for (int e = 0; e < G::kPer; e += 2) {
           float t0, t1;
-          unpair(mul2(add2(pair(f[e], f[e + 1]), minus_m), c2), &t0, &t1);
+          unpair(fma2(add2(pair(f[e], f[e + 1]), minus_m), c2, pair(off, off)), &t0, &t1);
           const unsigned long long e2 = pair(ptx::ex2_approx(t0), ptx::ex2_approx(t1));
           z2 = add2(z2, e2);
           // 0 * -inf is no part of the sum
@@ -356,24 +397,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
       }
       if constexpr (kTop) {
-        // (as long as there are fewer than k, the floor's value is the order's least: NaN)
-        if (q == q0 || __any_sync(0xffffffffu, !(top < floor))) {
-          const int v0 = q * 64 + lane;               // the vectors' indices in the row
-          best.offer(order_key(tops[0], v0), a.top_k);
-          best.offer(order_key(tops[1], v0 + 32), a.top_k);
-          floor = bits_value((uint32_t)(best.floor >> 32));
-        }
+        const uint32_t bits = __reduce_max_sync(0xffffffffu, order_bits(top));
+        if (lane == 0) p.tops[(long long)row * p.granules + q] = bits;
       }
     }
     left -= q1 - q0;
-    // ---- the statistics and best k of them
+    // ---- their statistics
     float z0, z1, w0, w1;
     unpair(z2, &z0, &z1);
     unpair(w2, &w0, &w1);
-    const Stats st = warp_merge(Stats{m, nan ? NAN : z0 + z1, w0 + w1}, p.c);
-    const long long slot = (long long)row + part;
-    if (lane == 0) p.stats[slot] = make_float4(st.m, st.z, st.w, 0.0f);
-    if (kTop && lane < a.top_k) p.keys[slot * a.top_k + lane] = best.mine;
+    const float z = z0 + z1, up = ptx::ex2_approx(-off);
+    const Stats st = warp_merge(Stats{m, nan ? NAN : z * up, (w0 + w1 - off * z) * up}, p.c);
+    if (lane == 0) p.stats[(long long)row + part] = make_float4(st.m, st.z, st.w, 0.0f);
     if (q == p.granules) {
       q = 0;
       ++row;
@@ -399,26 +434,49 @@ __global__ void __launch_bounds__(kThreads) gdn_token_logprobs_join_kernel(GdnLo
   const int id = a.logprobs && sub == 0 ? a.targets[row] : -1;
   pdl_wait();
   Stats st{-INFINITY, 0.0f, 0.0f};
+  for (int i = sub * 32 + lane; i < pieces; i += kRowWarps * 32) {
+    const float4 v = p.stats[row + c0 + i];
+    st = merge(st, Stats{v.x, v.y, v.z}, p.c);
+  }
   Best best;
   best.start();
-  for (int i0 = sub * 32; i0 < pieces; i0 += kRowWarps * 32) {
-    const bool mine = i0 + lane < pieces;
-    const long long slot = row + c0 + i0 + lane;
-    if (mine) {
-      const float4 v = p.stats[slot];
-      st = merge(st, Stats{v.x, v.y, v.z}, p.c);
-    }
-    if constexpr (kTop) {
-      // 32 lists a turn, one a lane: their first keys, then the next of those whose last one
-      // was good enough
-      const int k = a.top_k;
-      const Key* keys = p.keys + slot * k;
-      Key key = mine ? keys[0] : 0;
-      for (int i = 1; __any_sync(0xffffffffu, key > best.floor); ++i) {
-        const bool more = key > best.floor && i < k;
-        best.offer(key, k);
-        key = more ? keys[i] : 0;
+  if constexpr (kTop) {
+    // the best k granules (every warp of the row finds them), then of each warp's share of those
+    // the vectors that may be among the best k
+    const int n = min(a.top_k, p.granules);
+    Key granules = (uint32_t)~lane;                   // all of them, where there are at most k
+    if (p.granules > a.top_k) {
+      const uint32_t* tops = p.tops + row * p.granules;
+      for (int q0 = 0; q0 < p.granules; q0 += 32 * kTopsAhead) {
+        Key key[kTopsAhead];
+#pragma unroll
+        for (int i = 0; i < kTopsAhead; ++i) {
+          const int q = q0 + i * 32 + lane;
+          key[i] = q < p.granules ? ((Key)tops[q] << 32) | (uint32_t)~q : 0;
+        }
+        best.offer_all(key, a.top_k);
       }
+      granules = best.mine;
+      // k logits reach the k-th granule's largest
+      const Key least = (best.floor >> 32) << 32;
+      best.start();
+      best.floor = least - 1;
+    }
+    for (int i0 = sub; i0 < n; i0 += kRowWarps * kGranulesAhead) {
+      Key key[2 * kGranulesAhead];
+#pragma unroll
+      for (int i = 0; i < kGranulesAhead; ++i) {
+        const int at = i0 + i * kRowWarps;
+        const int q = (int)~(uint32_t)__shfl_sync(0xffffffffu, granules, at & 31);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int vec = q * 64 + v * 32 + lane;
+          const uint4 u = at < n ? load_vec(x, (long long)vec * Granule<T>::kVec - shift_of(x), a.V)
+                                 : make_uint4(0, 0, 0, 0);
+          key[2 * i + v] = at < n ? order_key(vector_top(u, x), vec) : 0;
+        }
+      }
+      best.offer_all(key, a.top_k);
     }
   }
   st = warp_merge(st, p.c);
@@ -447,13 +505,7 @@ __global__ void __launch_bounds__(kThreads) gdn_token_logprobs_join_kernel(GdnLo
         const long long at = (long long)(uint32_t)~(uint32_t)v * kVec + i % kVec - shift;
         key[j] = i < n && v != 0 && at >= 0 && at < a.V ? order_key(ld_elem(x + at), (int)at) : 0;
       }
-#pragma unroll 1
-      for (int j = 0; j < kLogitsAhead; ++j) {
-        Key one = key[0];
-#pragma unroll
-        for (int i = 1; i < kLogitsAhead; ++i) one = j == i ? key[i] : one;
-        best.offer(one, a.top_k);
-      }
+      best.offer_all(key, a.top_k);
     }
   }
   const bool dead = st.m == -INFINITY && st.z == 0.0f;  // every logit -inf
@@ -484,8 +536,9 @@ int granules_of(int V, int bf16) {         // with up to a vector's worth of shi
   return (int)(((long long)V + vec - 1 + per - 1) / per);
 }
 
-size_t slots(int N) { return (size_t)N + kParts; }
-size_t stats_bytes(int N) { return (sizeof(float4) * slots(N) + 255) & ~(size_t)255; }
+size_t stats_bytes(int N) {
+  return (sizeof(float4) * ((size_t)N + kParts) + 255) & ~(size_t)255;
+}
 
 template <typename T, bool kTop, bool kEntropy>
 cudaError_t launch(const GdnLogprobArgs& a, const Pieces& p, cudaStream_t stream) {
@@ -493,8 +546,8 @@ cudaError_t launch(const GdnLogprobArgs& a, const Pieces& p, cudaStream_t stream
   gdn_token_logprobs_kernel<T, kTop, kEntropy><<<grid, kThreads, 0, stream>>>(a, p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // a row's pieces: about parts / rows
-  if (grid > a.N)
+  // few rows: a CTA's warps share one
+  if (a.N <= 152 * 8)
     return launch_pdl(true, gdn_token_logprobs_join_kernel<T, kTop, kWarps>, dim3((unsigned)a.N),
                       dim3(kThreads), 0, stream, a, p);
   return launch_pdl(true, gdn_token_logprobs_join_kernel<T, kTop, 1>,
@@ -511,9 +564,7 @@ cudaError_t launch(const GdnLogprobArgs& a, const Pieces& p, cudaStream_t stream
 }  // namespace
 
 size_t gdn_token_logprobs_bytes(int N, int V, int bf16, int top_k) {
-  (void)V;
-  (void)bf16;
-  return stats_bytes(N) + sizeof(Key) * top_k * slots(N);
+  return stats_bytes(N) + (top_k ? sizeof(uint32_t) * (size_t)N * granules_of(V, bf16) : 0);
 }
 
 cudaError_t gdn_launch_token_logprobs(const GdnLogprobArgs& a, cudaStream_t stream) {
@@ -524,6 +575,6 @@ cudaError_t gdn_launch_token_logprobs(const GdnLogprobArgs& a, cudaStream_t stre
   p.c = a.scale * kLog2e;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.stats = reinterpret_cast<float4*>(ws);
-  p.keys = reinterpret_cast<Key*>(ws + stats_bytes(a.N));
+  p.tops = reinterpret_cast<uint32_t*>(ws + stats_bytes(a.N));
   return a.bf16 ? launch<__nv_bfloat16>(a, p, stream) : launch<float>(a, p, stream);
 }
