@@ -73,73 +73,68 @@ __device__ __forceinline__ int scale_exponent(float top) {
   return min(max(e, kMinExp), kMaxExp);
 }
 
-// Vector index -> (token, keys or values, head): heads fastest, then keys / values, then tokens.
-struct Where {
-  int token, head, which;
-};
-__device__ __forceinline__ Where where(long long vec, int H) {
-  const long long r = vec / H;
-  return Where{(int)(r >> 1), (int)(vec - r * H), (int)(r & 1)};
-}
-
-// Element offset of a cache vector, or -1: skipped (negative slot) or out of range (recorded).
-__device__ __forceinline__ long long row_of(int slot, int head, int H, int page_shift,
-                                            int num_pages) {
+// Row of a token's slot in the cache (of H * page rows a page), or -1: skipped (negative slot) or
+// out of range (recorded).
+__device__ __forceinline__ long long row_of(const GdnKvCacheArgs& c, int slot, int head) {
   if (slot < 0) return -1;
-  const int page = slot >> page_shift, off = slot & ((1 << page_shift) - 1);
-  if (page >= num_pages) {
+  const int page = slot >> c.page_shift, off = slot & ((1 << c.page_shift) - 1);
+  if (page >= c.num_pages) {
     atomicOr(&g_err_kv, kErrIndex);
     return -1;
   }
-  return ((((long long)page * H + head) << page_shift) + off);
+  return (((long long)page * c.H + head) << c.page_shift) + off;
 }
+
+// Grid: x tokens, y = keys of head 0 .. H - 1, then values.  d / 8 lanes a vector; a thread has
+// kTokens tokens, kThreads 8 / d apart, their loads issued before any use.
+constexpr int kTokens = 4;
 
 template <typename Tin, int D, bool kF8>
 __global__ void __launch_bounds__(kThreads) gdn_kv_append_kernel(
     GdnKvCacheArgs c, int n, const Tin* k, long long k_stride, const Tin* v, long long v_stride,
     const int32_t* slots) {
-  constexpr int L = D / 8;                             // lanes a vector
+  constexpr int L = D / 8, kStep = kThreads / L;
   const int lane = threadIdx.x % L;
-  const long long vecs = 2ll * n * c.H;
-  const long long step = (long long)gridDim.x * (kThreads / L);
-  // whole warps stay in the loop for the shuffles: past the end, the last vector once more
-  const long long first = (long long)blockIdx.x * (kThreads / L) + threadIdx.x / L;
-  for (long long v0 = first; __any_sync(0xffffffffu, v0 < vecs); v0 += step) {
-    const long long vec = v0 < vecs ? v0 : vecs - 1;
-    const Where w = where(vec, c.H);
-    const long long row =
-        v0 < vecs ? row_of(slots[w.token], w.head, c.H, c.page_shift, c.num_pages) : -1;
-    const Tin* src = (w.which ? v + w.token * v_stride : k + w.token * k_stride) +
-                     (long long)w.head * D + lane * 8;
-    const Vec8 x = load8(src);
+  const bool values = (int)blockIdx.y >= c.H;
+  const int head = values ? blockIdx.y - c.H : blockIdx.y;
+  const long long stride = values ? v_stride : k_stride;
+  const Tin* src = (values ? v : k) + (long long)head * D + lane * 8;
+  const int t0 = blockIdx.x * (kStep * kTokens) + threadIdx.x / L;
+  int slot[kTokens];
+  Vec8 x[kTokens];
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i) {
+    const int t = t0 + i * kStep;
+    slot[i] = t < n ? slots[t] : -1;
+    x[i] = load8(src + min(t, n - 1) * stride);       // (whole warps stay for the shuffles)
+  }
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i) {
+    const long long row = row_of(c, slot[i], head);
     if constexpr (!kF8) {
-      if (row >= 0)
-        store8(static_cast<__nv_bfloat16*>(w.which ? c.v : c.k) + row * D + lane * 8, x);
+      if (row >= 0) store8(static_cast<__nv_bfloat16*>(values ? c.v : c.k) + row * D + lane * 8, x[i]);
     } else {
       float top = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float m = fabsf(x.x[i]);
+      for (int e = 0; e < 8; ++e) {
+        const float m = fabsf(x[i].x[e]);
         top = m < INFINITY ? fmaxf(top, m) : top;      // false for NaN too
       }
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       const int e = scale_exponent(top);
       const float f = pow2i(-e);
-      uint32_t lo = 0, hi = 0;
+      uint32_t w[2] = {};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        lo |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x.x[2 * i] * f, x.x[2 * i + 1] * f),
-                                                 __NV_SATFINITE, __NV_E4M3)
-              << (16 * i);
-        hi |= (uint32_t)__nv_cvt_float2_to_fp8x2(
-                  make_float2(x.x[4 + 2 * i] * f, x.x[5 + 2 * i] * f), __NV_SATFINITE, __NV_E4M3)
-              << (16 * i);
-      }
+      for (int q = 0; q < 4; ++q)
+        w[q >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(
+                         make_float2(x[i].x[2 * q] * f, x[i].x[2 * q + 1] * f), __NV_SATFINITE,
+                         __NV_E4M3)
+                     << (16 * (q & 1));
       if (row >= 0) {
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(w.which ? c.v : c.k) + row * D +
-                                  lane * 8) = make_uint2(lo, hi);
-        if (lane == 0) (w.which ? c.v_exp : c.k_exp)[row] = (uint8_t)(e + 127);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(values ? c.v : c.k) + row * D + lane * 8) =
+            make_uint2(w[0], w[1]);
+        if (lane == 0) (values ? c.v_exp : c.k_exp)[row] = (uint8_t)(e + 127);
       }
     }
   }
@@ -149,44 +144,60 @@ template <typename Tout, int D, bool kF8>
 __global__ void __launch_bounds__(kThreads) gdn_kv_read_kernel(GdnKvCacheArgs c, int n,
                                                                const int32_t* slots, Tout* k_out,
                                                                Tout* v_out) {
-  constexpr int L = D / 8;
+  constexpr int L = D / 8, kStep = kThreads / L;
   const int lane = threadIdx.x % L;
-  const long long vecs = 2ll * n * c.H;
-  const long long step = (long long)gridDim.x * (kThreads / L);
-  for (long long vec = (long long)blockIdx.x * (kThreads / L) + threadIdx.x / L; vec < vecs;
-       vec += step) {
-    const Where w = where(vec, c.H);
-    const long long row = row_of(slots[w.token], w.head, c.H, c.page_shift, c.num_pages);
-    Vec8 x = {};
-    if (row >= 0) {
-      if constexpr (!kF8) {
-        x = load8(static_cast<const __nv_bfloat16*>(w.which ? c.v : c.k) + row * D + lane * 8);
-      } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(
-            static_cast<const uint8_t*>(w.which ? c.v : c.k) + row * D + lane * 8);
-        const float f = pow2i((int)(w.which ? c.v_exp : c.k_exp)[row] - 127);
+  const bool values = (int)blockIdx.y >= c.H;
+  const int head = values ? blockIdx.y - c.H : blockIdx.y;
+  const int t0 = blockIdx.x * (kStep * kTokens) + threadIdx.x / L;
+  long long row[kTokens];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t two = ((i < 2 ? u.x : u.y) >> (16 * (i & 1))) & 0xffffu;
-          const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3));
-          x.x[2 * i] = __low2float(h) * f;
-          x.x[2 * i + 1] = __high2float(h) * f;
-        }
+  for (int i = 0; i < kTokens; ++i) {
+    const int t = t0 + i * kStep;
+    row[i] = row_of(c, t < n ? slots[t] : -1, head);
+  }
+  Vec8 x[kTokens];
+  if constexpr (!kF8) {
+    const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(values ? c.v : c.k) + lane * 8;
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) x[i] = row[i] >= 0 ? load8(base + row[i] * D) : Vec8{};
+  } else {
+    const uint8_t* base = static_cast<const uint8_t*>(values ? c.v : c.k) + lane * 8;
+    const uint8_t* exps = values ? c.v_exp : c.k_exp;
+    uint2 u[kTokens];
+    int e[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      u[i] = row[i] >= 0 ? *reinterpret_cast<const uint2*>(base + row[i] * D) : make_uint2(0, 0);
+      e[i] = row[i] >= 0 ? exps[row[i]] : 127;
+    }
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      const float f = __uint_as_float((uint32_t)e[i] << 23);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t two = ((q < 2 ? u[i].x : u[i].y) >> (16 * (q & 1))) & 0xffffu;
+        const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3));
+        x[i].x[2 * q] = __low2float(h) * f;
+        x[i].x[2 * q + 1] = __high2float(h) * f;
       }
     }
-    store8((w.which ? v_out : k_out) + ((long long)w.token * c.H + w.head) * D + lane * 8, x);
+  }
+#pragma unroll
+  for (int i = 0; i < kTokens; ++i) {
+    const int t = t0 + i * kStep;
+    if (t < n) store8((values ? v_out : k_out) + ((long long)t * c.H + head) * D + lane * 8, x[i]);
   }
 }
 
-int grid_for(long long vecs, int D) {
-  const long long blocks = (vecs * (D / 8) + kThreads - 1) / kThreads;
-  return (int)(blocks < 152 * 8 ? blocks : 152 * 8);
+dim3 grid_for(int n, int H, int D) {
+  const int tokens = kThreads / (D / 8) * kTokens;
+  return dim3((unsigned)((n + (long long)tokens - 1) / tokens), (unsigned)(2 * H));
 }
 
 template <typename Tin, int D>
 void launch_append(const GdnKvCacheArgs& c, int n, const void* k, long long ks, const void* v,
                    long long vs, const int32_t* slots, cudaStream_t stream) {
-  const int grid = grid_for(2ll * n * c.H, D);
+  const dim3 grid = grid_for(n, c.H, D);
   if (c.f8)
     gdn_kv_append_kernel<Tin, D, true><<<grid, kThreads, 0, stream>>>(
         c, n, (const Tin*)k, ks, (const Tin*)v, vs, slots);
@@ -198,7 +209,7 @@ void launch_append(const GdnKvCacheArgs& c, int n, const void* k, long long ks, 
 template <typename Tout, int D>
 void launch_read(const GdnKvCacheArgs& c, int n, const int32_t* slots, void* k, void* v,
                  cudaStream_t stream) {
-  const int grid = grid_for(2ll * n * c.H, D);
+  const dim3 grid = grid_for(n, c.H, D);
   if (c.f8)
     gdn_kv_read_kernel<Tout, D, true><<<grid, kThreads, 0, stream>>>(c, n, slots, (Tout*)k, (Tout*)v);
   else

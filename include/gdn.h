@@ -420,7 +420,7 @@ typedef enum { GDN_KV_BF16 = 0, GDN_KV_E4M3 = 1 } gdn_kv_format;
 typedef struct {
   int32_t num_pages;     /* >= 0 */
   int32_t page_size;     /* 16, 32, 64 or 128 tokens */
-  int32_t num_kv_heads;  /* H >= 1; num_pages * page_size * H < 2^31 */
+  int32_t num_kv_heads;  /* 1 <= H <= 1024; num_pages * page_size * H < 2^31 */
   int32_t head_dim;      /* D: 128 or 256 */
   gdn_kv_format format;
   void* k;               /* [num_pages, H, page_size, D] bf16 or e4m3 codes, 16-byte aligned */

@@ -29,7 +29,7 @@ def _cache(**kw):
 BAD_CACHES = [
     (dict(num_pages=-1), 1), (dict(num_kv_heads=0), 1), (dict(head_dim=0), 1),
     (dict(page_size=0), 1), (dict(format=2), 1), (dict(head_dim=64), 2), (dict(page_size=8), 2),
-    (dict(page_size=48), 2), (dict(page_size=256), 2), (dict(num_pages=1 << 24, page_size=128), 2),
+    (dict(page_size=48), 2), (dict(page_size=256), 2), (dict(num_kv_heads=1025), 2), (dict(num_pages=1 << 24, page_size=128), 2),
     (dict(k=None), 1), (dict(v=None), 1), (dict(k=A + 8), 1), (dict(v=A + 2), 1),
     (dict(format=1), 1), (dict(format=1, k_exp=A), 1),
 ]
