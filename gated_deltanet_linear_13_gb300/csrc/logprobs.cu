@@ -28,6 +28,11 @@
 #include "sm100_ptx.cuh"
 
 using namespace gdn;
+using ptx::add2;
+using ptx::fma2;
+using ptx::mul2;
+using ptx::pair;
+using ptx::unpair;
 
 static __device__ unsigned int g_err_lp;
 
@@ -181,30 +186,6 @@ struct Pieces {                            // how the line is cut
   uint32_t* tops;                          // [row][granule]: the largest logit's order bits
 };
 
-__device__ __forceinline__ unsigned long long pair(float a, float b) {
-  unsigned long long r;
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpair(unsigned long long p, float* a, float* b) {
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(*a), "=f"(*b) : "l"(p));
-}
-__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
-  unsigned long long r;
-  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b,
-                                                   unsigned long long c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));

@@ -726,6 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!live) lim = 0;
       any_live = __any_sync(0xffffffffu, live);
       const float rc = kF8 ? coef * sQFac[r] : coef;
+      const unsigned long long rc2 = pair(rc, rc);
       m = -INFINITY;
       l = 0.0f;
       for (int j = it.j0; j < it.j1; ++j, ++g) {
@@ -742,10 +743,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float4 k4 = ks[i], v4 = ks[32 + i];
-              s[4 * i] = fmaf(s[4 * i] * k4.x, rc, v4.x);
-              s[4 * i + 1] = fmaf(s[4 * i + 1] * k4.y, rc, v4.y);
-              s[4 * i + 2] = fmaf(s[4 * i + 2] * k4.z, rc, v4.z);
-              s[4 * i + 3] = fmaf(s[4 * i + 3] * k4.w, rc, v4.w);
+              unpair(fma2(mul2(pair(s[4 * i], s[4 * i + 1]), pair(k4.x, k4.y)), rc2,
+                          pair(v4.x, v4.y)), &s[4 * i], &s[4 * i + 1]);
+              unpair(fma2(mul2(pair(s[4 * i + 2], s[4 * i + 3]), pair(k4.z, k4.w)), rc2,
+                          pair(v4.z, v4.w)), &s[4 * i + 2], &s[4 * i + 3]);
             }
           }
           const int seen = lim - j * kKeys - 64 * half;  // this half's keys that the row sees
@@ -792,19 +793,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
           }
           const float base = m == -INFINITY ? 0.0f : m;
-          float sum4[4] = {};
+          const unsigned long long minus_base = pair(-base, -base);
+          unsigned long long sum2[2] = {};            // pairs
           if constexpr (kF8) {
             uint32_t t0[16], t1[16], t2[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const float4 iv = ks[64 + i];
               float e[4];
+              unpair(add2(pair(s[4 * i], s[4 * i + 1]), minus_base), &e[0], &e[1]);
+              unpair(add2(pair(s[4 * i + 2], s[4 * i + 3]), minus_base), &e[2], &e[3]);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) e[q] = ex2_approx(s[4 * i + q] - base);
-              sum4[0] = fmaf(e[0], iv.x, sum4[0]);
-              sum4[1] = fmaf(e[1], iv.y, sum4[1]);
-              sum4[2] = fmaf(e[2], iv.z, sum4[2]);
-              sum4[3] = fmaf(e[3], iv.w, sum4[3]);
+              for (int q = 0; q < 4; ++q) e[q] = ex2_approx(e[q]);
+              sum2[0] = fma2(pair(e[0], e[1]), pair(iv.x, iv.y), sum2[0]);
+              sum2[1] = fma2(pair(e[2], e[3]), pair(iv.z, iv.w), sum2[1]);
               split_e5m2(e, &t0[i], &t1[i], &t2[i]);
             }
             tmem_st16(ts + 16 * half, t0);
@@ -814,19 +816,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             float hi[32], lo[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float e0 = ex2_approx(fmaf(s[2 * i], rc, -base));
-              const float e1 = ex2_approx(fmaf(s[2 * i + 1], rc, -base));
-              sum4[(2 * i) & 3] += e0;
-              sum4[(2 * i + 1) & 3] += e1;
-              const uint32_t h = pack_bf16(e0, e1);
-              hi[i] = __uint_as_float(h);
-              lo[i] = __uint_as_float(pack_bf16(e0 - __uint_as_float(h << 16),
-                                                e1 - __uint_as_float(h & 0xffff0000u)));
+              float e0, e1;
+              unpair(fma2(pair(s[2 * i], s[2 * i + 1]), rc2, minus_base), &e0, &e1);
+              e0 = ex2_approx(e0);
+              e1 = ex2_approx(e1);
+              const unsigned long long e2 = pair(e0, e1);
+              sum2[i & 1] = add2(sum2[i & 1], e2);
+              // the leading bits by truncation, the exact rest rounded
+              const float h0 = __uint_as_float(__float_as_uint(e0) & 0xffff0000u);
+              const float h1 = __uint_as_float(__float_as_uint(e1) & 0xffff0000u);
+              hi[i] = __uint_as_float(__byte_perm(__float_as_uint(e0), __float_as_uint(e1), 0x7632));
+              float l0, l1;
+              unpair(add2(e2, pair(-h0, -h1)), &l0, &l1);
+              lo[i] = __uint_as_float(pack_bf16(l0, l1));
             }
             tmem_st32(ts + 32 * half, hi);
             tmem_st32(ts + 64 + 32 * half, lo);
           }
-          l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+          float l4[4];
+          unpair(sum2[0], &l4[0], &l4[1]);
+          unpair(sum2[1], &l4[2], &l4[3]);
+          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
           tmem_wait_st();
           tc_fence_before();
         }
