@@ -649,6 +649,15 @@ def _kv_cache(k_cache, v_cache, k_exp, v_exp):
     """(C struct, device) of a paged cache [num_pages, H, page_size, D]: bf16, or float8_e4m3fn
     codes with uint8 exponents [num_pages, H, page_size]."""
     dev, shape, dtype = k_cache.device, k_cache.shape, k_cache.dtype
+    if (dtype is torch.float8_e4m3fn and len(shape) == 4 and k_exp is not None and
+            v_exp is not None and v_cache.dtype is dtype and v_cache.shape == shape and
+            k_exp.dtype is torch.uint8 and v_exp.dtype is torch.uint8 and
+            k_exp.shape == v_exp.shape == shape[:3] and
+            dev == v_cache.device == k_exp.device == v_exp.device and dev.type == "cuda" and
+            k_cache.is_contiguous() and v_cache.is_contiguous() and k_exp.is_contiguous() and
+            v_exp.is_contiguous()):                  # the usual case at once
+        return GdnKvCache(shape[0], shape[2], shape[1], shape[3], GDN_KV_E4M3, k_cache.data_ptr(),
+                          v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr()), dev
     if dev.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
     if len(shape) != 4:
@@ -674,8 +683,12 @@ def _token_stride(t: torch.Tensor, name: str, shape, dtype, device) -> int:
     """The token stride (elements) of t [..., H, D], whose heads are dense and whose leading
     dimensions lie one token after the other."""
     H, D = shape[-2:]
-    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
-        return H * D
+    if t.shape == shape and t.dtype is dtype and t.device == device:
+        if t.is_contiguous():
+            return H * D
+        strides = t.stride()
+        if len(shape) == 3 and strides[2] == 1 and strides[1] == D and shape[0] > 1:
+            return strides[0]                        # slices of wider rows
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
