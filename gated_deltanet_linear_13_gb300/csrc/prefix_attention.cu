@@ -88,7 +88,7 @@ struct Params {
   int rows_p, rows_s;              // rows stored a part (<= 128)
   float *o_p, *o_s;                // parts: [slot][D / 4][rows][4]
   float2 *ml_p, *ml_s;             // [slot][rows]: m (base 2), l
-  long long* line;                 // [B + 1]: where each sequence's units start; the line's end
+  int2 *span_p, *span_s;           // [unit]: the CTAs that have its first and its last tile
 };
 
 __device__ __forceinline__ int own_len(const GdnAttnArgs& a, int b) {
@@ -129,7 +129,7 @@ __device__ __forceinline__ long long head_len(const Params& p) {
 
 // One CTA's piece of a unit.
 struct Item {
-  bool prefix;
+  bool prefix, first, last; // the prefix's or a sequence's; has the unit's first, last tile
   int h, b, rt, n;          // head, sequence, row tile, the sequence's own tokens
   int keys, j0, j1;         // keys some row sees; key tiles [j0, j1)
   long long unit;           // index among the prefix's / the sequences' units
@@ -187,6 +187,8 @@ struct Walk {
       const long long j1 = end > first ? end - first : 0;
       it->j0 = base + (int)(j0 < tiles ? j0 : tiles);
       it->j1 = base + (int)(j1 < tiles ? j1 : tiles);
+      it->first = it->j0 == base;
+      it->last = it->j1 == base + tiles;
       at += unit_len(p, tiles);
       if (prefix) {
         if (++rt == p.row_tiles_p) {
@@ -355,14 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         *sB0 = b;
         *sAt0 = at;
       }
-      if (c == 0 && b < p.a.B) {
-        p.line[b] = at;
-        const int n = p.a.kv_len[b];
-        if (n > (p.a.max_pages << p.a.cache.page_shift)) atomicOr(&g_err_attn, kErrIndex);
-      }
+      if (c == 0 && b < p.a.B && p.a.kv_len[b] > (p.a.max_pages << p.a.cache.page_shift))
+        atomicOr(&g_err_attn, kErrIndex);
       if (c != 0 && carry > lo) break;                // uniform
     }
-    if (c == 0 && tid == 0) p.line[p.a.B] = W;
   }
   pdl_trigger();                                      // the merge may be set up
   tc_fence_before();
@@ -615,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       asm volatile("cp.async.wait_all;\n" ::: "memory");
       if (kF8 || p.a.scale <= 0.0f) {
-        constexpr int kAt = 2;                        // passes side by side
+        constexpr int kAt = 4;                        // passes side by side
 #pragma unroll 1
         for (int r0 = sw * kPer; r0 < n; r0 += kAt * 8 * kPer) {
           uint32_t w[kAt][4];
@@ -692,6 +690,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (more) load_q(it);
       // ---- the part: O, m, l of the item's rows
       if (begun) wait(bar_pv + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, sAbort);
+      if (begun && r == 0 && half == 0) {
+        // where the merge finds the unit's parts
+        int2* span = (done.prefix ? p.span_p : p.span_s) + done.unit;
+        if (done.first) span->x = c;
+        if (done.last) span->y = c;
+      }
       if (begun && any_live) {
         tc_fence_after();
         if (half == 1) sSum[r] = l;
@@ -856,12 +860,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------------------- the merge
 //
 // A warp takes eight rows of one head (the parts lie with consecutive rows side by side) and 64
-// columns, and joins the rows' parts, found from the line's layout.  Few rows are cut into many
+// columns, and joins the rows' parts: the CTAs of a unit's span, one slot each.  Few rows are cut into many
 // parts: then (kGroups = 8) the eight warps of a block share out the parts of the same rows, so
 // that they are read at the same time, and join what they have in shared memory.
-template <int D, typename Tout, int kGroups>
+template <int D, typename Tout, int kGroups, int kAhead>
 __global__ void __launch_bounds__(256) gdn_prefix_merge_kernel(const Params p) {
-  constexpr int kAhead = 2, kVec = 4;                 // parts in flight, 16-byte vectors a lane
+  constexpr int kVec = 4;                             // 16-byte vectors a lane
   __shared__ float4 s_acc[kGroups][16][8];            // [warp][vector of the 64 columns][row]
   __shared__ float2 s_ml[kGroups][8];
   const unsigned rows = (unsigned)p.a.B * p.a.T * p.G;   // of a head
@@ -872,29 +876,25 @@ __global__ void __launch_bounds__(256) gdn_prefix_merge_kernel(const Params p) {
   const int token = (int)(R / (unsigned)p.G), gh = (int)(R - (unsigned)token * p.G);
   const int b = token / p.a.T, t = token - b * p.a.T;
   const int raw = p.a.kv_len[b], n = own_len(p.a, b);
+  const int rs = t * p.G + gh, rt_s = rs / kRows, rt_p = (int)(R / kRows);
+  const bool own = n > 0 && tile_keys(p, n, rt_s) > 0;
+  const long long unit_s = ((long long)b * p.row_tiles_s + rt_s) * H + h;
   pdl_wait();
-  const long long W = p.line[p.a.B];
-  const long long at_b = p.line[b];
-  const int parts = (int)(W < kCtas ? W : kCtas);
   float acc[4 * kVec] = {}, m = -INFINITY, l = 0.0f;
-  // the parts c0 + skip, + step, ... of a unit
-  auto join = [&](long long at, int tiles, long long unit, const float* o, const float2* ml,
-                  int stored, int r, int skip, int step) {
-    // the CTAs that hold the first and the last of the unit's tiles
-    const long long x0 = at + p.unit_cost, x1 = x0 + tiles - 1;
-    const int c0 = (int)quotient((x0 + 1) * parts - 1, W);
-    const int c1 = (int)quotient((x1 + 1) * parts - 1, W);
-    for (int c = c0 + skip; c <= c1; c += kAhead * step) {
+  // the parts span.x + skip, + step, ... of a unit
+  auto join = [&](int2 span, long long unit, const float* o, const float2* ml, int stored, int r,
+                  int skip, int step) {
+    for (int c = span.x + skip; c <= span.y; c += kAhead * step) {
       float2 v[kAhead];
       float4 x[kAhead][kVec];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const long long slot = unit + min(c + i * step, c1);
+        const long long slot = unit + min(c + i * step, span.y);
         const float4* src = reinterpret_cast<const float4*>(o) + (slot * (D / 4) + cg) * stored + r;
         v[i] = ml[slot * stored + r];
 #pragma unroll
         for (int q = 0; q < kVec; ++q) x[i][q] = src[(long long)(4 * q) * stored];
-        if (c + i * step > c1) v[i] = make_float2(-INFINITY, 0.0f);
+        if (c + i * step > span.y) v[i] = make_float2(-INFINITY, 0.0f);
       }
       float mn = m;
 #pragma unroll
@@ -920,27 +920,19 @@ __global__ void __launch_bounds__(256) gdn_prefix_merge_kernel(const Params p) {
       }
     }
   };
-  if (raw >= 0 && W > 0) {
+  if (raw >= 0) {
+    const int2 span_s = own ? p.span_s[unit_s] : make_int2(0, -1);
     if (p.prefix_tiles > 0) {
-      const int rt = R / kRows;
-      const long long hl = head_len(p), bl = (long long)p.row_tiles_p * unit_len(p, p.block_tiles);
       // a warp takes whole blocks, or parts of each
       const bool whole = p.blocks >= kGroups;
-      for (int blk = whole ? group : 0; blk < p.blocks; blk += whole ? kGroups : 1)
-        join(h * hl + blk * bl + (long long)rt * block_len(p, blk),
-             min(p.block_tiles, p.prefix_tiles - blk * p.block_tiles),
-             ((long long)h * p.blocks + blk) * p.row_tiles_p + rt, p.o_p, p.ml_p, p.rows_p,
-             R % kRows, whole ? 0 : (group + blk) % kGroups, whole ? 1 : kGroups);
+      for (int blk = whole ? group : 0; blk < p.blocks; blk += whole ? kGroups : 1) {
+        const long long unit = ((long long)h * p.blocks + blk) * p.row_tiles_p + rt_p;
+        join(p.span_p[unit], unit, p.o_p, p.ml_p, p.rows_p, R % kRows,
+             whole ? 0 : (group + blk) % kGroups, whole ? 1 : kGroups);
+      }
     }
-    const int r = t * p.G + gh, rt = r / kRows;
-    const int tiles = n > 0 ? key_tiles(tile_keys(p, n, rt)) : 0;
-    if (tiles > 0) {
-      long long at = at_b;
-      for (int i = 0; i < rt; ++i) at += (long long)H * unit_len(p, key_tiles(tile_keys(p, n, i)));
-      at += (long long)h * unit_len(p, tiles);
-      join(at, tiles, ((long long)b * p.row_tiles_s + rt) * H + h, p.o_s, p.ml_s, p.rows_s,
-           r % kRows, (group + kGroups / 2) % kGroups, kGroups);
-    }
+    join(span_s, unit_s, p.o_s, p.ml_s, p.rows_s, rs % kRows, (group + kGroups / 2) % kGroups,
+         kGroups);
   }
   const long long row = (long long)token * p.a.Hq + h * p.G + gh;
   Tout* out = static_cast<Tout*>(p.a.out) + row * D + blockIdx.z * 64;
@@ -995,19 +987,25 @@ __global__ void __launch_bounds__(256) gdn_prefix_merge_kernel(const Params p) {
 template <int D, typename Tout>
 cudaError_t launch_merge(const Params& p, cudaStream_t stream) {
   const long long eights = ((long long)p.a.B * p.a.T * p.G + 7) / 8;
-  const unsigned H = (unsigned)p.a.cache.H;
-  if (eights * H > kFewRows / 8)
-    return launch_pdl(true, gdn_prefix_merge_kernel<D, Tout, 1>,
-                      dim3((unsigned)((eights + 7) / 8), H, D / 64), dim3(256), 0, stream, p);
-  return launch_pdl(true, gdn_prefix_merge_kernel<D, Tout, 8>, dim3((unsigned)eights, H, D / 64),
-                    dim3(256), 0, stream, p);
+  const unsigned H = (unsigned)p.a.cache.H, Z = D / 64;
+  // kAhead parts in flight a warp: four where all blocks are resident at 128 registers a thread
+  // (32 sequences, 16384 shared tokens, 384 blocks: 43.2 us with four, 41.5 with two; 16
+  // sequences, 192 blocks: 29.3 and 30.5)
+  if (eights * H * Z <= 2 * kCtas)
+    return launch_pdl(true, gdn_prefix_merge_kernel<D, Tout, 8, 4>, dim3((unsigned)eights, H, Z),
+                      dim3(256), 0, stream, p);
+  if (eights * H <= kFewRows / 8)
+    return launch_pdl(true, gdn_prefix_merge_kernel<D, Tout, 8, 2>, dim3((unsigned)eights, H, Z),
+                      dim3(256), 0, stream, p);
+  return launch_pdl(true, gdn_prefix_merge_kernel<D, Tout, 1, 2>,
+                    dim3((unsigned)((eights + 7) / 8), H, Z), dim3(256), 0, stream, p);
 }
 
 // ------------------------------------------------------------------------------- host side
 
 struct Layout {
   int row_tiles_p, row_tiles_s, rows_p, rows_s;
-  size_t line, ml_p, ml_s, o_p, o_s, total;
+  size_t span_p, span_s, ml_p, ml_s, o_p, o_s, total;
 };
 
 Layout layout_of(int B, int T, int Hq, int H, int D) {
@@ -1024,7 +1022,8 @@ Layout layout_of(int B, int T, int Hq, int H, int D) {
   const size_t np = (up_units + kCtas) * y.rows_p;
   const size_t ns = ((size_t)B * y.row_tiles_s * H + kCtas) * y.rows_s;
   size_t off = 0;
-  y.line = off; off += up(8 * ((size_t)B + 1));
+  y.span_p = off; off += up(8 * up_units);
+  y.span_s = off; off += up(8 * (size_t)B * y.row_tiles_s * H);
   y.ml_p = off; off += up(8 * np);
   y.ml_s = off; off += up(8 * ns);
   y.o_p = off; off += up(4 * np * D);
@@ -1087,7 +1086,8 @@ cudaError_t gdn_launch_prefix_attention(const GdnAttnArgs& a, cudaStream_t strea
   p.unit_cost = a.cache.D == 256 && !a.cache.f8 ? 1 : 2;
   p.rows_p = y.rows_p;
   p.rows_s = y.rows_s;
-  p.line = reinterpret_cast<long long*>(ws + y.line);
+  p.span_p = reinterpret_cast<int2*>(ws + y.span_p);
+  p.span_s = reinterpret_cast<int2*>(ws + y.span_s);
   p.ml_p = reinterpret_cast<float2*>(ws + y.ml_p);
   p.ml_s = reinterpret_cast<float2*>(ws + y.ml_s);
   p.o_p = reinterpret_cast<float*>(ws + y.o_p);
