@@ -759,34 +759,43 @@ def gdn_prefix_attention(q, k_cache, v_cache, out, *, pages, kv_len, prefix_page
     [B, T, Hq] fp32 or None; scale defaults to 1 / sqrt(D).  Returns ``out``."""
     L = load_library()
     c, dev = _kv_cache(k_cache, v_cache, k_exp, v_exp)
-    if q.dim() != 4:
-        raise ValueError(f"q: shape {tuple(q.shape)}, expected 4 dimensions")
-    B, T, Hq, D = q.shape
-    qs = _token_stride(q, "q", (B, T, Hq, c.head_dim), torch.bfloat16, dev)
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError(f"q: shape {tuple(shape)}, expected 4 dimensions")
+    B, T, Hq, D = shape
+    if D == c.head_dim and q.dtype is torch.bfloat16 and q.device == dev and q.is_contiguous():
+        qs = Hq * D
+    else:
+        qs = _token_stride(q, "q", (B, T, Hq, c.head_dim), torch.bfloat16, dev)
     dt = _dt(out)
-    _need(out, "out", (B, T, Hq, D), out.dtype, dev)
+    _need(out, "out", shape, out.dtype, dev)
+    i32 = torch.int32
     if pages.dim() != 2:
         raise ValueError(f"pages: shape {tuple(pages.shape)}, expected (B, max_pages)")
-    _need(pages, "pages", (B, pages.shape[1]), torch.int32, dev)
-    _need(kv_len, "kv_len", (B,), torch.int32, dev)
-    if prefix_len < 0:
-        raise ValueError("prefix_len must not be negative")
+    max_pages = pages.shape[1]
+    _need(pages, "pages", (B, max_pages), i32, dev)
+    _need(kv_len, "kv_len", (B,), i32, dev)
+    pp = None
     if prefix_len:
+        if prefix_len < 0:
+            raise ValueError("prefix_len must not be negative")
         if prefix_pages is None:
             raise ValueError("prefix_pages is required")
-        _need(prefix_pages, "prefix_pages", (prefix_pages.numel(),), torch.int32, dev)
-        if prefix_pages.numel() * c.page_size < prefix_len:
+        n = prefix_pages.numel()
+        _need(prefix_pages, "prefix_pages", (n,), i32, dev)
+        if n * c.page_size < prefix_len:
             raise ValueError("prefix_pages holds fewer tokens than prefix_len")
+        pp = prefix_pages.data_ptr()
     if lse is not None:
-        _need(lse, "lse", (B, T, Hq), torch.float32, dev)
+        _need(lse, "lse", shape[:3], torch.float32, dev)
     if workspace is None:
         need = int(L.gdn_prefix_attention_workspace_size(B, T, Hq, c.num_kv_heads, D))
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_bytes = workspace.numel() * workspace.element_size()
-    st = L.gdn_prefix_attention(ctypes.byref(c), B, T, Hq, _ptr(q), qs, _ptr(prefix_pages),
-                                int(prefix_len), _ptr(pages), pages.shape[1], _ptr(kv_len),
-                                float(D ** -0.5 if scale is None else scale), dt, _ptr(out),
-                                _ptr(lse), _ptr(workspace), ws_bytes, _stream_of(stream, dev))
+    st = L.gdn_prefix_attention(ctypes.byref(c), B, T, Hq, q.data_ptr(), qs, pp, prefix_len,
+                                pages.data_ptr(), max_pages, kv_len.data_ptr(),
+                                D ** -0.5 if scale is None else scale, dt, out.data_ptr(),
+                                _ptr(lse), workspace.data_ptr(), workspace.nbytes,
+                                _stream_of(stream, dev))
     _check(st, "gdn_prefix_attention")
     return out
 
