@@ -97,7 +97,8 @@ __device__ __forceinline__ int own_len(const GdnAttnArgs& a, int b) {
 }
 // keys that some row of row tile rt of a sequence of n tokens sees (the last row's)
 __device__ __forceinline__ int tile_keys(const Params& p, int n, int rt) {
-  const int t = min(p.a.T - 1, ((rt + 1) * kRows - 1) / p.G);
+  const int last = (rt + 1) * kRows - 1;              // (of the last tile: no division)
+  const int t = rt + 1 == p.row_tiles_s ? p.a.T - 1 : last / p.G;
   return max(0, min(n, n - p.a.T + 1 + t));
 }
 __device__ __forceinline__ int key_tiles(int keys) { return (keys + kKeys - 1) / kKeys; }
@@ -140,14 +141,27 @@ struct Walk {
   long long pos, end, at;   // at: where the current unit starts
   bool prefix;
   int b, blk, rt, h;
-  int len_b, len;           // the last sequence whose length was read, and it
+  int n, keys, tiles;       // the current unit's sequence length, keys and key tiles
+
+  // for the unit at (b, rt), which changed
+  __device__ __forceinline__ void measure(const Params& p, bool other_sequence) {
+    if (prefix) {
+      n = 0;
+      keys = p.a.prefix_len;
+      tiles = min(p.block_tiles, p.prefix_tiles - blk * p.block_tiles);
+      return;
+    }
+    if (b >= p.a.B) return;
+    if (other_sequence) n = own_len(p.a, b);
+    keys = n > 0 ? tile_keys(p, n, rt) : 0;
+    tiles = key_tiles(keys);
+  }
 
   __device__ void start(const Params& p, long long lo, long long hi, int b0, long long at0) {
     pos = lo; end = hi;
     const long long hl = head_len(p);
     prefix = lo < hl * p.a.cache.H;
     b = prefix ? 0 : b0; blk = 0; rt = 0; h = 0;
-    len_b = -1;
     at = at0;
     if (prefix) {
       h = (int)quotient(lo, hl);
@@ -158,25 +172,27 @@ struct Walk {
       rt = (int)quotient(rest, block_len(p, blk));
       at = h * hl + blk * bl + (long long)rt * block_len(p, blk);
     }
+    measure(p, true);
+    if (!prefix && b < p.a.B && lo < hi) {
+      // the units of the sequence before lo
+      while (lo - at >= (long long)p.a.cache.H * unit_len(p, tiles) && rt + 1 < p.row_tiles_s) {
+        at += (long long)p.a.cache.H * unit_len(p, tiles);
+        ++rt;
+        measure(p, false);
+      }
+      if (tiles > 0) h = (int)quotient(lo - at, unit_len(p, tiles));
+      at += (long long)h * unit_len(p, tiles);
+    }
   }
   __device__ bool next(const Params& p, Item* it) {
     const int H = p.a.cache.H;
     while (at < end) {
-      int keys, tiles, base = 0, n = 0;
+      int base = 0;
       if (prefix) {
-        keys = p.a.prefix_len;
         base = blk * p.block_tiles;
-        tiles = min(p.block_tiles, p.prefix_tiles - base);
         it->unit = ((long long)h * p.blocks + blk) * p.row_tiles_p + rt;
       } else {
         if (b >= p.a.B) return false;
-        if (b != len_b) {
-          len_b = b;
-          len = own_len(p.a, b);
-        }
-        n = len;
-        keys = n > 0 ? tile_keys(p, n, rt) : 0;
-        tiles = key_tiles(keys);
         it->unit = ((long long)b * p.row_tiles_s + rt) * H + h;
       }
       it->prefix = prefix;
@@ -197,12 +213,13 @@ struct Walk {
             blk = 0;
             if (++h == H) { h = 0; prefix = false; }
           }
+          measure(p, true);
         }
-      } else if (n <= 0) {
-        ++b; rt = 0; h = 0;
-      } else if (++h == H) {
+      } else if (n <= 0 || ++h == H) {
         h = 0;
-        if (++rt == p.row_tiles_s) { rt = 0; ++b; }
+        const bool other = n <= 0 || ++rt == p.row_tiles_s;
+        if (other) { rt = 0; ++b; }
+        measure(p, other);
       }
       if (it->j1 > it->j0) return true;
     }
