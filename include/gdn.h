@@ -473,9 +473,11 @@ gdn_status gdn_kv_cache_read(const gdn_kv_cache* cache, int32_t n, const int32_t
  * A page entry outside the cache is recorded as GDN_ERR_DEVICE_INDEX (its tokens read as zero
  * codes).  Cache entries at and past a sequence's length may hold anything, NaN included.
  * The lengths stay on the device, so a captured graph can be replayed as they grow.
- * Accuracy: exact products of bf16 (or e4m3) operands, fp32 scores and softmax statistics; the
- * probabilities enter the second product with 16 significant bits (bf16 cache: two bf16 terms)
- * or 11 (e4m3 cache: three e5m2 terms), down to 2^-24 of their row's first tile's largest there.
+ * Accuracy: exact products of bf16 (or e4m3) operands, fp32 sums, scores and softmax statistics;
+ * the probabilities enter the second product with 16 significant bits (bf16 cache: two bf16
+ * terms) or 11 (e4m3 cache: three e5m2 terms, and no finer than 2^-25 of the row's largest, each
+ * weighted with its value's scale).  A query with an infinity or a NaN makes its row NaN, and so
+ * does a visible key or value with one.
  */
 size_t gdn_prefix_attention_workspace_size(int32_t batch, int32_t seqlen, int32_t num_heads,
                                            int32_t num_kv_heads, int32_t head_dim);
