@@ -148,17 +148,17 @@ struct Best {
     }
     set_floor(k);
   }
-  // N keys of each lane.  The first time, the lanes' largest come first (32 distinct keys): the
+  // N keys of each lane.  Without a floor, the lanes' largest come first (32 distinct keys): the
   // floor is then near its place, and few of the others pass it.
   template <int N>
   __device__ __forceinline__ void offer_all(Key (&key)[N], int k) {
-    if (__shfl_sync(0xffffffffu, mine, 0) == 0) {
+    if (floor == 0 && __shfl_sync(0xffffffffu, mine, 0) == 0) {
       Key top = key[0];
 #pragma unroll
       for (int i = 1; i < N; ++i) top = key_max(top, key[i]);
 #pragma unroll
       for (int i = 0; i < N; ++i) key[i] = key[i] == top ? 0 : key[i];
-      mine = sorted(top > floor ? top : 0);
+      mine = sorted(top);
       set_floor(k);
     }
     uint32_t any = 0;                      // (one copy of the code for all N)
@@ -415,18 +415,22 @@ __global__ void __launch_bounds__(kThreads) gdn_token_logprobs_join_kernel(GdnLo
   const int id = a.logprobs && sub == 0 ? a.targets[row] : -1;
   pdl_wait();
   Stats st{-INFINITY, 0.0f, 0.0f};
-  for (int i = sub * 32 + lane; i < pieces; i += kRowWarps * 32) {
-    const float4 v = p.stats[row + c0 + i];
-    st = merge(st, Stats{v.x, v.y, v.z}, p.c);
-  }
+  auto statistics = [&]() {
+    for (int i = sub * 32 + lane; i < pieces; i += kRowWarps * 32) {
+      const float4 v = p.stats[row + c0 + i];
+      st = merge(st, Stats{v.x, v.y, v.z}, p.c);
+    }
+    st = warp_merge(st, p.c);
+  };
+  if (!kTop) statistics();
   Best best;
   best.start();
   if constexpr (kTop) {
-    // the best k granules (every warp of the row finds them), then of each warp's share of those
+    // the best k granules (the row's first warp finds them), then of each warp's share of those
     // the vectors that may be among the best k
     const int n = min(a.top_k, p.granules);
     Key granules = (uint32_t)~lane;                   // all of them, where there are at most k
-    if (p.granules > a.top_k) {
+    if (p.granules > a.top_k && sub == 0) {
       const uint32_t* tops = p.tops + row * p.granules;
       for (int q0 = 0; q0 < p.granules; q0 += 32 * kTopsAhead) {
         Key key[kTopsAhead];
@@ -438,10 +442,19 @@ __global__ void __launch_bounds__(kThreads) gdn_token_logprobs_join_kernel(GdnLo
         best.offer_all(key, a.top_k);
       }
       granules = best.mine;
+    }
+    statistics();                                     // (the other warps while the first selects)
+    if (p.granules > a.top_k) {
+      if constexpr (kRowWarps > 1) {
+        if (warp == 0) s_best[0][lane] = granules;
+        __syncthreads();
+        granules = s_best[0][lane];
+        __syncthreads();
+      }
       // k logits reach the k-th granule's largest
-      const Key least = (best.floor >> 32) << 32;
+      const Key least = __shfl_sync(0xffffffffu, granules, a.top_k - 1);
       best.start();
-      best.floor = least - 1;
+      best.floor = ((least >> 32) << 32) - 1;
     }
     for (int i0 = sub; i0 < n; i0 += kRowWarps * kGranulesAhead) {
       Key key[2 * kGranulesAhead];
@@ -460,16 +473,22 @@ __global__ void __launch_bounds__(kThreads) gdn_token_logprobs_join_kernel(GdnLo
       best.offer_all(key, a.top_k);
     }
   }
-  st = warp_merge(st, p.c);
   if constexpr (kRowWarps > 1) {
     if (lane == 0) s_stats[warp] = st;
     if (kTop) s_best[warp][lane] = best.mine;
     __syncthreads();
     if (warp > 0) return;
     st = warp_merge(lane < kWarps ? s_stats[lane] : Stats{-INFINITY, 0.0f, 0.0f}, p.c);
-    if constexpr (kTop)
-      for (int i = 1; i < kWarps; ++i)
-        if (__any_sync(0xffffffffu, s_best[i][lane] > best.floor)) best.join(s_best[i][lane], a.top_k);
+    if constexpr (kTop) {
+      // the lists' first four at once, then what else of them is good enough
+      best.start();
+      best.mine = Best::sorted(s_best[lane & (kWarps - 1)][lane / kWarps]);
+      best.set_floor(a.top_k);
+      for (int i = 0; i < kWarps; ++i) {
+        const Key rest = lane >= 32 / kWarps ? s_best[i][lane] : 0;
+        if (__any_sync(0xffffffffu, rest > best.floor)) best.offer(rest, a.top_k);
+      }
+    }
   }
   if constexpr (kTop) {
     // the logits of the best k vectors, a lane one at a time

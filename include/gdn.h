@@ -476,8 +476,9 @@ gdn_status gdn_kv_cache_read(const gdn_kv_cache* cache, int32_t n, const int32_t
  * Accuracy: exact products of bf16 (or e4m3) operands, fp32 sums, scores and softmax statistics;
  * the probabilities enter the second product with 16 significant bits (bf16 cache: two bf16
  * terms) or 11 (e4m3 cache: three e5m2 terms, and no finer than 2^-25 of the row's largest, each
- * weighted with its value's scale).  A query with an infinity or a NaN makes its row NaN, and so
- * does a visible key or value with one.
+ * weighted with its value's scale).  A query with an infinity or a NaN makes its row NaN, a
+ * key with one the rows that see it, a value with one (of a token that some row sees) every row
+ * that shares its products: the sequence's rows, or the batch's for the prefix.
  */
 size_t gdn_prefix_attention_workspace_size(int32_t batch, int32_t seqlen, int32_t num_heads,
                                            int32_t num_kv_heads, int32_t head_dim);
