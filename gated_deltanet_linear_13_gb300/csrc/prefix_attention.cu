@@ -48,7 +48,7 @@ namespace {
 constexpr int kCtas = 152;                 // one CTA an SM
 constexpr int kRows = 128, kKeys = 128;
 constexpr int kFewRows = 2048;             // the merge's warps share out a row's parts up to here
-constexpr long long kBlockBytes = 32ll << 20;
+constexpr long long kBlockBytes = 256ll << 20;
 constexpr int KB = 1024;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -1086,8 +1086,10 @@ cudaError_t gdn_launch_prefix_attention(const GdnAttnArgs& a, cudaStream_t strea
   p.row_tiles_p = y.row_tiles_p;
   p.row_tiles_s = y.row_tiles_s;
   p.prefix_tiles = (a.prefix_len + kKeys - 1) / kKeys;
-  // several row tiles of a prefix that L2 does not hold beside everything else: blocks of keys
-  // of about one CTA's part
+  // Several row tiles of a prefix far larger than L2: blocks of keys of about one CTA's part, so
+  // that the row tiles read the same keys at the same time.  Smaller ones stay in L2 long enough,
+  // and blocks cost more parts to join (16 x 4 tokens, bf16, 134 MB of prefix: 75 us with, 71
+  // without; 40 x 4: 183, 157; 12 x 4 tokens, 537 MB: 223, 250; 40 x 4, 410 MB: 459, 478).
   const long long prefix_bytes = 2ll * a.prefix_len * a.cache.H * a.cache.D * (a.cache.f8 ? 1 : 2);
   p.blocks = 1;
   if (y.row_tiles_p > 1 && prefix_bytes > kBlockBytes) {

@@ -449,6 +449,21 @@ def test_attention_nan_stays_in_its_rows(gdn, fmt):
     assert torch.equal(out[~bad], good[~bad])
 
 
+def test_attention_many_sequences(gdn):
+    """More sequences than the kernel's threads lay out at a time, with and without a prefix."""
+    for prefix in (0, 200):
+        case = _attention_case(500, 1, 4, 2, 128, prefix, [(i * 11) % 150 - (i % 7 == 3) * 200
+                                                           for i in range(500)], 16, "f8", seed=71)
+        case["lens"] = [max(n, -1) for n in case["lens"]]
+        _check_attention(gdn, case)
+
+
+@pytest.mark.parametrize("fmt,prefix", [("bf16", 140001), ("f8", 270000)])
+def test_attention_very_long_prefix(gdn, fmt, prefix):
+    """Several row tiles on a prefix so long that its keys are worked on in blocks."""
+    _check_attention(gdn, _attention_case(2, 33, 4, 2, 256, prefix, [33, 200], 128, fmt, seed=72))
+
+
 def test_attention_no_tokens(gdn):
     case = _attention_case(1, 1, 4, 1, 128, 16, [1], 16, "bf16", seed=51)
     q = case["q"][:, :0]
