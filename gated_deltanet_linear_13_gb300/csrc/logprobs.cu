@@ -9,13 +9,15 @@
 // The alternatives cost the pass one maximum a granule (the kilobyte that a warp takes at a time).
 // The k granules with the largest maxima hold the k best logits: a logit of another granule is
 // beaten by the largest of each of the k.  (Granules are consecutive, so this holds for equal
-// values too, which go by the lower index.)  The joining kernel finds them among the row's maxima,
-// reads them again (k kilobytes of a row of hundreds), narrows them down to k vectors of 16 bytes
-// in the same way, and takes the best k of those vectors' logits.  Each time a warp keeps the best
-// 32 in order, one a lane: a single better one is inserted (a ballot gives its place, a shuffle
-// moves the rest up), many at once are sorted and merged.  A value and an index make one 64-bit
-// key, ordered by value (NaN first, -0 equal to 0) and then by lower index; keys are distinct, so
-// the result depends on no order of execution.
+// values too, which go by the lower index.)  The joining kernel finds the k-th largest of the
+// row's maxima by counting, reads those granules again (k kilobytes of a row of hundreds), and
+// gathers what reaches that maximum: vectors of 16 bytes, then their logits, a few more than k of
+// them.  A logit's place is the number of better ones.  Where more pass than there is room for
+// (rows of equal logits, rising rows) a warp keeps the best 32 vectors in order instead, one a lane, and the best
+// 32 of their logits: a single better one is inserted (a ballot gives its place, a shuffle moves
+// the rest up), many at once are sorted and merged.  A value and an index make one 64-bit key,
+// ordered by value (NaN first, -0 equal to 0) and then by lower index; keys are distinct, so the
+// result depends on no order of execution.
 //
 // All rows lie on one line of granules (the last of a row shorter), cut into equal parts, a warp's
 // each, so that one long row fills the GPU as well as twenty thousand short ones; no warp waits for
@@ -49,8 +51,8 @@ typedef unsigned long long Key;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 4, kParts = 152 * kCtasPerSm * kWarps;
-// loads ahead of a lane in the joining kernel: granules' maxima, granules, logits
-constexpr int kTopsAhead = 8, kGranulesAhead = 4, kLogitsAhead = 8;
+// of a lane in the joining kernel: granules' maxima held, loads ahead of granules and of logits
+constexpr int kHeld = 16, kGranulesAhead = 4, kLogitsAhead = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <typename T>
@@ -76,11 +78,13 @@ __device__ __forceinline__ Stats merge(const Stats& a, const Stats& b, float c) 
   if (fb != 0.0f) r.z += fb * b.z, r.w += fb * (b.w + db * b.z);
   return r;
 }
+__device__ __forceinline__ Stats other_lane(const Stats& a, int o) {
+  return Stats{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.z, o),
+               __shfl_xor_sync(0xffffffffu, a.w, o)};
+}
 __device__ __forceinline__ Stats warp_merge(Stats a, float c) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    a = merge(a, Stats{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.z, o),
-                       __shfl_xor_sync(0xffffffffu, a.w, o)}, c);
+  for (int o = 16; o > 0; o >>= 1) a = merge(a, other_lane(a, o), c);
   return a;
 }
 
@@ -398,88 +402,216 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   }
 }
 
+// The best k of a row's granules by their largest logit, equal ones by the lower index, in
+// ascending order into list; returns order bits that each of them reaches.  The k-th largest is
+// found bit by bit, counting what reaches a number (a warp's sum is one instruction), and as soon
+// as exactly k do, those are the ones.  A bf16 number's order bits differ in the upper half only.
+template <typename T>
+__device__ __forceinline__ uint32_t best_granules(const uint32_t* tops, int granules, int k,
+                                                  const uint32_t (&held)[kHeld], int* list) {
+  constexpr int kLow = sizeof(T) == 2 ? 16 : 0;
+  const int lane = threadIdx.x & 31;
+  auto each = [&](auto&& f) {              // the row's maxima, 32 at a time; 0 past the end
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i * 32 < granules) f(i * 32 + lane, held[i]);
+#pragma unroll 4
+    for (int q = kHeld * 32 + lane; q - lane < granules; q += 32)
+      f(q, q < granules ? tops[q] : 0u);
+  };
+  uint32_t most = 0, least = 0xffffffffu;
+  each([&](int q, uint32_t v) {
+    most = max(most, v);
+    if (q < granules) least = min(least, v);
+  });
+  most = __reduce_max_sync(0xffffffffu, most);
+  least = __reduce_min_sync(0xffffffffu, least);
+  auto reach = [&](uint32_t y) {
+    int n = 0;
+    each([&](int, uint32_t v) { n += v >= y ? 1 : 0; });
+    return (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+  };
+  // their common leading bits, then the others
+  uint32_t x = most;
+  int b = 31 - __clz(most ^ least);
+  if (b >= kLow) x &= ~((2u << b) - 1u);
+#pragma unroll 1
+  for (; b >= kLow; --b) {
+    const uint32_t y = x | 1u << b;
+    const int n = reach(y);
+    if (n >= k) x = y;
+    if (n == k) break;
+  }
+  x &= ~((1u << kLow) - 1u);
+  const uint32_t over = x + (1u << kLow);  // (0: nothing is)
+  int ties = k - (over ? reach(over) : 0), taken = 0;
+  const uint32_t before = (1u << lane) - 1u;
+  each([&](int q, uint32_t v) {
+    if (taken >= k) return;
+    const bool more = over && v >= over, tie = v >= x && !more;
+    const uint32_t tied = __ballot_sync(0xffffffffu, tie);
+    const bool take = more || (tie && __popc(tied & before) < ties);
+    const uint32_t took = __ballot_sync(0xffffffffu, take);
+    if (take) list[taken + __popc(took & before)] = q;
+    ties -= min(ties, __popc(tied));
+    taken += __popc(took);
+  });
+  return x;
+}
+
 // Joins a row's pieces: kRowWarps warps a row (1: a few pieces; 8: many, which the warps share).
 template <typename T, bool kTop, int kRowWarps>
 __global__ void __launch_bounds__(kThreads) gdn_token_logprobs_join_kernel(GdnLogprobArgs a, Pieces p) {
+  constexpr int kVec = Granule<T>::kVec;
+  // a row's candidates: vectors, then logits
+  constexpr int kVectors = kTop ? 64 : 1, kMost = kTop ? 64 : 1, kSlots = kTop ? kWarps / kRowWarps : 1;
   __shared__ Stats s_stats[kWarps];
-  __shared__ Key s_best[kWarps][32];
+  __shared__ Key s_best[kTop ? kWarps : 1][32];
+  __shared__ uint4 s_vector[kSlots][kVectors];
+  __shared__ int s_index[kSlots][kVectors];
+  __shared__ __align__(16) Key s_candidate[kSlots][kMost];
+  __shared__ int s_granule[kSlots][32];
+  __shared__ uint32_t s_floor[kSlots];
+  __shared__ int s_vectors[kSlots], s_candidates[kSlots];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = kRowWarps == 1 ? 0 : warp;
+  const int sub = kRowWarps == 1 ? 0 : warp, slot = kRowWarps == 1 ? warp : 0;
   const long long row = kRowWarps == 1 ? (long long)blockIdx.x * kWarps + warp : blockIdx.x;
   if (row >= a.N) return;                             // (whole blocks where warps share a row)
+  auto sync = [&]() {                                 // the row's warps
+    if constexpr (kRowWarps == 1) __syncwarp();
+    else __syncthreads();
+  };
   const T* x = static_cast<const T*>(a.logits) + row * a.row_stride;
   const long long x0 = row * p.granules, x1 = x0 + p.granules - 1;
   // the parts that hold the row's first and last granule
   const int c0 = (int)(((x0 + 1) * p.parts - 1) / p.total);
   const int pieces = (int)(((x1 + 1) * p.parts - 1) / p.total) - c0 + 1;
   const int id = a.logprobs && sub == 0 ? a.targets[row] : -1;
+  const float target = id >= 0 && id < a.V ? ld_elem(x + id) : 0.0f;
+  if (kTop && lane == 0 && sub == 0) s_vectors[slot] = s_candidates[slot] = 0;
   pdl_wait();
-  Stats st{-INFINITY, 0.0f, 0.0f};
-  auto statistics = [&]() {
-    for (int i = sub * 32 + lane; i < pieces; i += kRowWarps * 32) {
-      const float4 v = p.stats[row + c0 + i];
-      st = merge(st, Stats{v.x, v.y, v.z}, p.c);
-    }
-    st = warp_merge(st, p.c);
-  };
-  if (!kTop) statistics();
-  Best best;
-  best.start();
+  const int shift = shift_of(x), n = min(a.top_k, p.granules);
+  int granule = lane;                                 // lane i the i-th of the best (or of all)
+  uint32_t floor = 0;                                 // k logits reach it
+  // the first warp finds the granules, the others join the statistics
+  const bool selects = kTop && sub == 0 && p.granules > a.top_k;
   if constexpr (kTop) {
-    // the best k granules (the row's first warp finds them), then of each warp's share of those
-    // the vectors that may be among the best k
-    const int n = min(a.top_k, p.granules);
-    Key granules = (uint32_t)~lane;                   // all of them, where there are at most k
-    if (p.granules > a.top_k && sub == 0) {
+    if (selects) {
       const uint32_t* tops = p.tops + row * p.granules;
-      for (int q0 = 0; q0 < p.granules; q0 += 32 * kTopsAhead) {
-        Key key[kTopsAhead];
+      uint32_t held[kHeld];
 #pragma unroll
-        for (int i = 0; i < kTopsAhead; ++i) {
-          const int q = q0 + i * 32 + lane;
-          key[i] = q < p.granules ? ((Key)tops[q] << 32) | (uint32_t)~q : 0;
+      for (int i = 0; i < kHeld; ++i) {
+        const int q = i * 32 + lane;
+        held[i] = q < p.granules ? tops[q] : 0u;
+      }
+      floor = best_granules<T>(tops, p.granules, a.top_k, held, s_granule[slot]);
+      if (lane == 0) s_floor[slot] = floor;
+    }
+  }
+  Stats st{-INFINITY, 0.0f, 0.0f};
+  constexpr int kOthers = kTop && kRowWarps > 1 ? kRowWarps - 1 : kRowWarps;
+  for (int i = (sub - (kRowWarps - kOthers)) * 32 + lane; i >= 0 && i < pieces; i += kOthers * 32) {
+    const float4 v = p.stats[row + c0 + i];
+    st = merge(st, Stats{v.x, v.y, v.z}, p.c);
+  }
+  if (kRowWarps == 1 || kOthers == kRowWarps || sub > 0) st = warp_merge(st, p.c);
+  if (kRowWarps > 1 && lane == 0) s_stats[warp] = st;
+  if constexpr (kTop) {
+    sync();
+    if (p.granules > a.top_k) granule = s_granule[slot][lane], floor = s_floor[slot];
+    // their vectors that reach it
+    for (int i0 = sub; i0 < n; i0 += kRowWarps * kGranulesAhead) {
+      uint4 u[2 * kGranulesAhead];
+      int vec[2 * kGranulesAhead];
+#pragma unroll
+      for (int i = 0; i < kGranulesAhead; ++i) {
+        const int at = i0 + i * kRowWarps, q = __shfl_sync(0xffffffffu, granule, at & 31);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          vec[2 * i + v] = at < n ? q * 64 + v * 32 + lane : -1;
+          u[2 * i + v] = at < n ? load_vec(x, (long long)vec[2 * i + v] * kVec - shift, a.V)
+                                : make_uint4(0, 0, 0, 0);
         }
-        best.offer_all(key, a.top_k);
       }
-      granules = best.mine;
-    }
-    statistics();                                     // (the other warps while the first selects)
-    if (p.granules > a.top_k) {
-      if constexpr (kRowWarps > 1) {
-        if (warp == 0) s_best[0][lane] = granules;
-        __syncthreads();
-        granules = s_best[0][lane];
-        __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 2 * kGranulesAhead; ++j) {
+        if (vec[j] < 0 || order_bits(vector_top(u[j], x)) < floor) continue;
+        const int to = atomicAdd(&s_vectors[slot], 1);
+        if (to >= kVectors) continue;
+        s_vector[slot][to] = u[j];
+        s_index[slot][to] = vec[j];
       }
-      // k logits reach the k-th granule's largest
-      const Key least = __shfl_sync(0xffffffffu, granules, a.top_k - 1);
-      best.start();
-      best.floor = ((least >> 32) << 32) - 1;
     }
+    sync();
+    // and those vectors' logits
+    const int logits = min(s_vectors[slot], kVectors) * kVec;
+    for (int i = sub * 32 + lane; i < logits; i += kRowWarps * 32) {
+      const int e = i % kVec;
+      const T* words = reinterpret_cast<const T*>(&s_vector[slot][i / kVec]);
+      const float f = ld_elem(words + e);
+      const long long at = (long long)s_index[slot][i / kVec] * kVec + e - shift;
+      if (order_bits(f) < floor || at < 0 || at >= a.V) continue;
+      const int to = atomicAdd(&s_candidates[slot], 1);
+      if (to < kMost) s_candidate[slot][to] = order_key(f, (int)at);
+    }
+  }
+  if (kTop || kRowWarps > 1) sync();
+  if constexpr (kRowWarps > 1) {
+    st = s_stats[lane & (kWarps - 1)];                // every eight lanes hold all of them
+    for (int o = kWarps / 2; o > 0; o >>= 1) st = merge(st, other_lane(st, o), p.c);
+  }
+  const bool dead = st.m == -INFINITY && st.z == 0.0f;  // every logit -inf
+  // (a merge rounds its two sides differently, so lanes may differ in the last bit)
+  const float log2z = __shfl_sync(0xffffffffu, log2f(st.z), 0);
+  auto logp = [&](float v) { return dead ? -INFINITY : (v - st.m) * a.scale - kLn2 * log2z; };
+  auto store_top = [&](int rank, Key key) {
+    a.top_ids[row * a.top_k + rank] = (int)~(uint32_t)key;
+    a.top_logprobs[row * a.top_k + rank] = logp(bits_value((uint32_t)(key >> 32)));
+  };
+  if (lane == 0 && sub == 0) {
+    if (a.logprobs) {
+      if (id >= a.V) atomicOr(&g_err_lp, kErrIndex);
+      a.logprobs[row] = id >= a.V ? NAN : id >= 0 ? logp(target) : 0.0f;
+    }
+    if (a.entropy) a.entropy[row] = dead ? 0.0f : kLn2 * (log2z - st.w / st.z);
+  }
+  if constexpr (kTop) {
+    const int candidates = s_candidates[slot];
+    if (s_vectors[slot] <= kVectors && candidates <= kMost) {
+      // a candidate's place: how many are better
+      for (int i = sub * 32 + lane; i < candidates; i += kRowWarps * 32) {
+        const Key key = s_candidate[slot][i];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < candidates; ++j) rank += s_candidate[slot][j] > key ? 1 : 0;
+        if (rank < a.top_k) store_top(rank, key);
+      }
+      return;
+    }
+    // Too many (equal logits, or rising ones): of each warp's granules the vectors that may be
+    // among the best k, then the best k of those vectors' logits.
+    Best best;
+    best.start();
+    if (floor != 0) best.floor = ((Key)floor << 32) - 1;
     for (int i0 = sub; i0 < n; i0 += kRowWarps * kGranulesAhead) {
       Key key[2 * kGranulesAhead];
 #pragma unroll
       for (int i = 0; i < kGranulesAhead; ++i) {
-        const int at = i0 + i * kRowWarps;
-        const int q = (int)~(uint32_t)__shfl_sync(0xffffffffu, granules, at & 31);
+        const int at = i0 + i * kRowWarps, q = __shfl_sync(0xffffffffu, granule, at & 31);
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           const int vec = q * 64 + v * 32 + lane;
-          const uint4 u = at < n ? load_vec(x, (long long)vec * Granule<T>::kVec - shift_of(x), a.V)
+          const uint4 u = at < n ? load_vec(x, (long long)vec * kVec - shift, a.V)
                                  : make_uint4(0, 0, 0, 0);
           key[2 * i + v] = at < n ? order_key(vector_top(u, x), vec) : 0;
         }
       }
       best.offer_all(key, a.top_k);
     }
-  }
-  if constexpr (kRowWarps > 1) {
-    if (lane == 0) s_stats[warp] = st;
-    if (kTop) s_best[warp][lane] = best.mine;
-    __syncthreads();
-    if (warp > 0) return;
-    st = warp_merge(lane < kWarps ? s_stats[lane] : Stats{-INFINITY, 0.0f, 0.0f}, p.c);
-    if constexpr (kTop) {
+    if constexpr (kRowWarps > 1) {
+      s_best[warp][lane] = best.mine;
+      __syncthreads();
+      if (warp > 0) return;
       // the lists' first four at once, then what else of them is good enough
       best.start();
       best.mine = Best::sorted(s_best[lane & (kWarps - 1)][lane / kWarps]);
@@ -489,44 +621,22 @@ __global__ void __launch_bounds__(kThreads) gdn_token_logprobs_join_kernel(GdnLo
         if (__any_sync(0xffffffffu, rest > best.floor)) best.offer(rest, a.top_k);
       }
     }
-  }
-  if constexpr (kTop) {
     // the logits of the best k vectors, a lane one at a time
-    constexpr int kVec = Granule<T>::kVec;
-    const int shift = shift_of(x), n = a.top_k * kVec;
+    const int logits = a.top_k * kVec;
     const Key vector = best.mine;
     best.start();
-    for (int i0 = 0; i0 < n; i0 += 32 * kLogitsAhead) {
+    for (int i0 = 0; i0 < logits; i0 += 32 * kLogitsAhead) {
       Key key[kLogitsAhead];
 #pragma unroll
       for (int j = 0; j < kLogitsAhead; ++j) {
         const int i = i0 + j * 32 + lane;
         const Key v = __shfl_sync(0xffffffffu, vector, (i / kVec) & 31);
         const long long at = (long long)(uint32_t)~(uint32_t)v * kVec + i % kVec - shift;
-        key[j] = i < n && v != 0 && at >= 0 && at < a.V ? order_key(ld_elem(x + at), (int)at) : 0;
+        key[j] = i < logits && v != 0 && at >= 0 && at < a.V ? order_key(ld_elem(x + at), (int)at) : 0;
       }
       best.offer_all(key, a.top_k);
     }
-  }
-  const bool dead = st.m == -INFINITY && st.z == 0.0f;  // every logit -inf
-  const float log2z = log2f(st.z);
-  auto logp = [&](float v) { return dead ? -INFINITY : (v - st.m) * a.scale - kLn2 * log2z; };
-  if (lane == 0) {
-    if (a.logprobs) {
-      float lp = 0.0f;
-      if (id >= a.V) {
-        atomicOr(&g_err_lp, kErrIndex);
-        lp = NAN;
-      } else if (id >= 0) {
-        lp = logp(ld_elem(x + id));
-      }
-      a.logprobs[row] = lp;
-    }
-    if (a.entropy) a.entropy[row] = dead ? 0.0f : kLn2 * (log2z - st.w / st.z);
-  }
-  if (kTop && lane < a.top_k) {
-    a.top_ids[row * a.top_k + lane] = (int)~(uint32_t)best.mine;
-    a.top_logprobs[row * a.top_k + lane] = logp(bits_value((uint32_t)(best.mine >> 32)));
+    if (lane < a.top_k) store_top(lane, best.mine);
   }
 }
 
