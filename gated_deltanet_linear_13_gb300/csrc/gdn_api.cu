@@ -537,8 +537,8 @@ static gdn_status check_kv_cache(const gdn_kv_cache* c, GdnKvCacheArgs* out) {
   if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
     return GDN_ERR_UNSUPPORTED;
   if (c->num_kv_heads > 1024) return GDN_ERR_UNSUPPORTED;
-  // rows of one head's tokens are counted in 32 bits
-  if ((long long)c->num_pages * c->page_size * c->num_kv_heads > 0x7fffffffLL)
+  // rows of a head's tokens are counted in 32 bits, a page past the last among them
+  if ((long long)c->num_pages * c->page_size * c->num_kv_heads > 0x7fffff00LL)
     return GDN_ERR_UNSUPPORTED;
   const bool f8 = c->format == GDN_KV_E4M3;
   if (c->num_pages > 0 &&

@@ -9,8 +9,10 @@
 // exact, and every stored value c 2^e is exact in bf16, so reading back rounds nothing.  From
 // max|x| = f 2^x, 1 <= f < 2: e = x - 8 when f <= 1.75 (448 = 1.75 2^8), else x - 7.
 //
-// Both kernels move 16 bytes of the 16-bit side a lane, d / 8 lanes a vector, and are bound by
-// memory.
+// Both kernels move eight elements a lane, d / 8 lanes a vector, four tokens of a lane on the way
+// at a time (one: 29.4 and 51.9 us below), and are bound by memory: 16384 bf16 tokens of 4 x 256
+// into an 8-bit cache 19.4 us (5.2 TB/s read and written), 40001 tokens of 8 x 128 out of one
+// 42.7 us (5.8 TB/s); a few tokens cost one launch, 2.4 us.
 #include <cuda_fp8.h>
 
 #include "common.cuh"

@@ -13,11 +13,11 @@
 // row's maxima by counting, reads those granules again (k kilobytes of a row of hundreds), and
 // gathers what reaches that maximum: vectors of 16 bytes, then their logits, a few more than k of
 // them.  A logit's place is the number of better ones.  Where more pass than there is room for
-// (rows of equal logits, rising rows) a warp keeps the best 32 vectors in order instead, one a lane, and the best
-// 32 of their logits: a single better one is inserted (a ballot gives its place, a shuffle moves
-// the rest up), many at once are sorted and merged.  A value and an index make one 64-bit key,
-// ordered by value (NaN first, -0 equal to 0) and then by lower index; keys are distinct, so the
-// result depends on no order of execution.
+// (rows of equal logits, rising rows) a warp keeps the best 32 vectors in order instead, one a
+// lane, and the best 32 of their logits: a single better one is inserted (a ballot gives its
+// place, a shuffle moves the rest up), many at once are sorted and merged.  A value and an index
+// make one 64-bit key, ordered by value (NaN first, -0 equal to 0) and then by lower index; keys
+// are distinct, so the result depends on no order of execution.
 //
 // All rows lie on one line of granules (the last of a row shorter), cut into equal parts, a warp's
 // each, so that one long row fills the GPU as well as twenty thousand short ones; no warp waits for
@@ -25,7 +25,9 @@
 //
 // Bound by memory: each logit is read once.  At the copy rate an SM gets 12 bf16 logits a cycle,
 // for which it can issue 128 lane operations; a logit takes about nine (packed fp32 pairs where
-// there are such instructions) and one of 16 exponentials a cycle.
+// there are such instructions) and one of 16 exponentials a cycle.  Measured: 1000 rows of 151669
+// in fp32 100 us (6.1 TB/s); 64 rows of 248320 in bf16 with 20 alternatives 17.7 us, of which the
+// pass takes 11 and the join 6; one row 9.1 us, two launches.
 #include "common.cuh"
 #include "sm100_ptx.cuh"
 
@@ -51,7 +53,9 @@ typedef unsigned long long Key;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 4, kParts = 152 * kCtasPerSm * kWarps;
-// of a lane in the joining kernel: granules' maxima held, loads ahead of granules and of logits
+// of a lane in the joining kernel: granules' maxima held, loads ahead of granules (two: 1400 rows
+// of 32000 with 20 alternatives 44.6 us, four: 39.8, eight: 38.0, but 3000 rows 70.6 for 60.2) and
+// of logits
 constexpr int kHeld = 16, kGranulesAhead = 4, kLogitsAhead = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -215,7 +219,8 @@ __device__ __forceinline__ float max_half(uint32_t w) {
 __device__ __forceinline__ void range(const uint4& u, const uint4& v, const __nv_bfloat16*,
                                       const float*, float* top, float* least) {
   *top = max_half(max2_nan(max_word(u), max_word(v)));
-  const uint32_t lo = min2(min2(min2(u.x, u.y), min2(u.z, u.w)), min2(min2(v.x, v.y), min2(v.z, v.w)));
+  const uint32_t lo =
+      min2(min2(min2(u.x, u.y), min2(u.z, u.w)), min2(min2(v.x, v.y), min2(v.z, v.w)));
   *least = fminf(__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u));
 }
 __device__ __forceinline__ void range(const uint4&, const uint4&, const float*, const float* f,
@@ -282,7 +287,7 @@ __device__ __forceinline__ uint4 load_vec(const T* row, long long i, int V) {
 }
 
 template <typename T>
-__device__ __forceinline__ int shift_of(const T* row) {   // logits from its 16-byte boundary to a row
+__device__ __forceinline__ int shift_of(const T* row) {   // logits from a 16-byte boundary to a row
   return (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
 }
 
@@ -461,10 +466,12 @@ __device__ __forceinline__ uint32_t best_granules(const uint32_t* tops, int gran
 
 // Joins a row's pieces: kRowWarps warps a row (1: a few pieces; 8: many, which the warps share).
 template <typename T, bool kTop, int kRowWarps>
-__global__ void __launch_bounds__(kThreads) gdn_token_logprobs_join_kernel(GdnLogprobArgs a, Pieces p) {
+__global__ void __launch_bounds__(kThreads)
+    gdn_token_logprobs_join_kernel(GdnLogprobArgs a, Pieces p) {
   constexpr int kVec = Granule<T>::kVec;
   // a row's candidates: vectors, then logits
-  constexpr int kVectors = kTop ? 64 : 1, kMost = kTop ? 64 : 1, kSlots = kTop ? kWarps / kRowWarps : 1;
+  constexpr int kVectors = kTop ? 64 : 1, kMost = kTop ? 64 : 1;
+  constexpr int kSlots = kTop ? kWarps / kRowWarps : 1;               // rows of a block
   __shared__ Stats s_stats[kWarps];
   __shared__ Key s_best[kTop ? kWarps : 1][32];
   __shared__ uint4 s_vector[kSlots][kVectors];
@@ -632,7 +639,8 @@ __global__ void __launch_bounds__(kThreads) gdn_token_logprobs_join_kernel(GdnLo
         const int i = i0 + j * 32 + lane;
         const Key v = __shfl_sync(0xffffffffu, vector, (i / kVec) & 31);
         const long long at = (long long)(uint32_t)~(uint32_t)v * kVec + i % kVec - shift;
-        key[j] = i < logits && v != 0 && at >= 0 && at < a.V ? order_key(ld_elem(x + at), (int)at) : 0;
+        key[j] = i < logits && v != 0 && at >= 0 && at < a.V ? order_key(ld_elem(x + at), (int)at)
+                                                             : 0;
       }
       best.offer_all(key, a.top_k);
     }
@@ -656,7 +664,8 @@ cudaError_t launch(const GdnLogprobArgs& a, const Pieces& p, cudaStream_t stream
   gdn_token_logprobs_kernel<T, kTop, kEntropy><<<grid, kThreads, 0, stream>>>(a, p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // few rows: a CTA's warps share one
+  // Few rows: a CTA's warps share one (20 of 32000 logits, with eight warps a row and with one:
+  // 300 rows 14.5 / 24.8 us, 1000 rows 30.1 / 34.4, 1400 rows 41.3 / 39.6).
   if (a.N <= 152 * 8)
     return launch_pdl(true, gdn_token_logprobs_join_kernel<T, kTop, kWarps>, dim3((unsigned)a.N),
                       dim3(kThreads), 0, stream, a, p);

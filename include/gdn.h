@@ -420,7 +420,7 @@ typedef enum { GDN_KV_BF16 = 0, GDN_KV_E4M3 = 1 } gdn_kv_format;
 typedef struct {
   int32_t num_pages;     /* >= 0 */
   int32_t page_size;     /* 16, 32, 64 or 128 tokens */
-  int32_t num_kv_heads;  /* 1 <= H <= 1024; num_pages * page_size * H < 2^31 */
+  int32_t num_kv_heads;  /* 1 <= H <= 1024; num_pages * page_size * H <= 2^31 - 256 */
   int32_t head_dim;      /* D: 128 or 256 */
   gdn_kv_format format;
   void* k;               /* [num_pages, H, page_size, D] bf16 or e4m3 codes, 16-byte aligned */
@@ -476,9 +476,10 @@ gdn_status gdn_kv_cache_read(const gdn_kv_cache* cache, int32_t n, const int32_t
  * Accuracy: exact products of bf16 (or e4m3) operands, fp32 sums, scores and softmax statistics;
  * the probabilities enter the second product with 16 significant bits (bf16 cache: two bf16
  * terms) or 11 (e4m3 cache: three e5m2 terms, and no finer than 2^-25 of the row's largest, each
- * weighted with its value's scale).  A query with an infinity or a NaN makes its row NaN, a
- * key with one the rows that see it, a value with one (of a token that some row sees) every row
- * that shares its products: the sequence's rows, or the batch's for the prefix.
+ * weighted with its value's scale).  bf16 values above 2^64 may overflow the sums.
+ * A query with an infinity or a NaN makes its row NaN, a key with one the rows that see it, a
+ * value with one (of a token that some row sees) every row that shares its products: the
+ * sequence's rows, or the batch's for the prefix.
  */
 size_t gdn_prefix_attention_workspace_size(int32_t batch, int32_t seqlen, int32_t num_heads,
                                            int32_t num_kv_heads, int32_t head_dim);
