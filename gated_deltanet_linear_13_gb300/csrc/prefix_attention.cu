@@ -78,8 +78,8 @@ struct Shape {
   static constexpr int kRing = kQBytes;
   static constexpr int kMax = kRing + kSlots * kSlotBytes;           // [2][2][128] float
   static constexpr int kSum = kMax + 2048;                           // [128] float
-  static constexpr int kQFac = kSum + 512;                           // [128] float (8-bit)
-  static constexpr int kScales = kQFac + (kF8 ? 512 : 0);            // [2][3][128] float (8-bit)
+  static constexpr int kQFac = kSum + 512;                           // [2][128] float (8-bit)
+  static constexpr int kScales = kQFac + (kF8 ? 1024 : 0);            // [2][3][128] float (8-bit)
   static constexpr int kBars = kScales + (kF8 ? 3072 : 0);
   static constexpr int kMisc = kBars + 8 * (2 * kSlots + 12 + 1);
   static constexpr int kBytes = kMisc + 64;
@@ -608,7 +608,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // from overflow and a raise to rows whose first tile says little; e5m2 ends at 57344, so the
     // reference lies kLift below the maximum and P starts at 2^kLift
     constexpr float kSlack = kF8 ? 7.0f : 32.0f, kLift = kF8 ? 8.0f : 0.0f;
-    uint32_t g = 0;
+    // turn: counts the items (a warp may load the next one's Q while another has yet to read its
+    // own row's factor of this one)
+    uint32_t g = 0, turn = 0;
     // Q: an item's rows, dealt to the warps and gathered into the swizzled K-major layout (small
     // loops: this code runs once an item and its instructions come from L2).  8-bit: a row's
     // bf16 elements land where its two terms will lie, 4 x 128 bytes, and are split in place.
@@ -696,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint2*>(to) = make_uint2(hw[0] | hw[1] << 16, hw[2] | hw[3] << 16);
                 *reinterpret_cast<uint2*>(to + kRows * D) =
                     make_uint2(lw[0] | lw[1] << 16, lw[2] | lw[3] << 16);
-                if (ql == 0) sQFac[row] = __uint_as_float((uint32_t)(127 + e) << 23);
+                if (ql == 0) sQFac[128 * (turn & 1) + row] = __uint_as_float((uint32_t)(127 + e) << 23);
               }
             }
           }
@@ -712,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // thread, so O stays until then.
     bool live = false, any_live = false;
     float m = -INFINITY, l = 0.0f;                    // reference, this half's sum
-    for (bool begun = false;; begun = true) {
+    for (bool begun = false;; begun = true, ++turn) {
       const Item done = it;
       const bool more = walk.next(p, &it);
       if (more) load_q(it);
@@ -757,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       live = item_row(p, it, r, &token, &gh, &lim);
       if (!live) lim = 0;
       any_live = __any_sync(0xffffffffu, live);
-      const float rc = kF8 ? coef * sQFac[r] : coef;
+      const float rc = kF8 ? coef * sQFac[128 * (turn & 1) + r] : coef;
       const unsigned long long rc2 = pair(rc, rc);
       m = -INFINITY;
       l = 0.0f;
