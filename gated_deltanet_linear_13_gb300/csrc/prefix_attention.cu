@@ -698,7 +698,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint2*>(to) = make_uint2(hw[0] | hw[1] << 16, hw[2] | hw[3] << 16);
                 *reinterpret_cast<uint2*>(to + kRows * D) =
                     make_uint2(lw[0] | lw[1] << 16, lw[2] | lw[3] << 16);
-                if (ql == 0) sQFac[128 * (turn & 1) + row] = __uint_as_float((uint32_t)(127 + e) << 23);
+                if (ql == 0)
+                  sQFac[128 * (turn & 1) + row] = __uint_as_float((uint32_t)(127 + e) << 23);
               }
             }
           }
