@@ -542,7 +542,8 @@ static gdn_status check_kv_cache(const gdn_kv_cache* c, GdnKvCacheArgs* out) {
     return GDN_ERR_UNSUPPORTED;
   const bool f8 = c->format == GDN_KV_E4M3;
   if (c->num_pages > 0 &&
-      (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v) || (f8 && (!c->k_exp || !c->v_exp))))
+      (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v) ||
+       (f8 && (!c->k_exp || !c->v_exp || !aligned4(c->k_exp) || !aligned4(c->v_exp)))))
     return GDN_ERR_INVALID_ARGUMENT;
   out->num_pages = c->num_pages;
   out->page_shift = __builtin_ctz((unsigned)c->page_size);

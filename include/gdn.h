@@ -425,7 +425,8 @@ typedef struct {
   gdn_kv_format format;
   void* k;               /* [num_pages, H, page_size, D] bf16 or e4m3 codes, 16-byte aligned */
   void* v;
-  uint8_t* k_exp;        /* GDN_KV_E4M3: [num_pages, H, page_size], e + 127; else ignored */
+  uint8_t* k_exp;        /* GDN_KV_E4M3: [num_pages, H, page_size], e + 127, 4-byte aligned;
+                            else ignored */
   uint8_t* v_exp;
 } gdn_kv_cache;
 

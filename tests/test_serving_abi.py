@@ -44,6 +44,16 @@ def test_bad_caches_are_refused(L, bad, status):
                                   None, A, 1 << 40, None) == status
 
 
+@pytest.mark.parametrize("bad", [dict(k_exp=A + 1), dict(v_exp=A + 2), dict(k_exp=A + 3, v_exp=A + 3)])
+def test_unaligned_exponents_are_refused(L, bad):
+    """The attention reads four exponents at a time."""
+    c = ctypes.byref(_cache(**{**dict(format=1, k_exp=A, v_exp=A), **bad}))
+    assert L.gdn_kv_cache_append(c, 4, gdn.GDN_BF16, A, 1024, A, 1024, A, None) == 1
+    assert L.gdn_kv_cache_read(c, 4, A, gdn.GDN_BF16, A, A, None) == 1
+    assert L.gdn_prefix_attention(c, 1, 1, 24, A, 24 * 256, A, 64, A, 1, A, 1.0, gdn.GDN_BF16, A,
+                                  None, A, 1 << 40, None) == 1
+
+
 def test_kv_cache_arguments(L):
     c = ctypes.byref(_cache())
 
