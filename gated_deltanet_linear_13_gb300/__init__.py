@@ -193,6 +193,17 @@ def _stream_of(stream, device: torch.device) -> int:
     return _stream(stream)
 
 
+def _workspace(need: int, device: torch.device, stream) -> torch.Tensor:
+    """A call's own workspace, from the pool of the stream that it runs on, so that the memory
+    goes to nobody else before the call is through."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        raw = _stream(stream)
+        stream = (torch.cuda.ExternalStream(raw, device=device) if raw
+                  else torch.cuda.default_stream(device))
+    with torch.cuda.stream(stream):                  # (None: the current one)
+        return torch.empty(need, dtype=torch.uint8, device=device)
+
+
 def _check(status: int, where: str):
     if status != GDN_OK:
         raise GDNError(status, where)
@@ -790,7 +801,7 @@ def gdn_prefix_attention(q, k_cache, v_cache, out, *, pages, kv_len, prefix_page
         _need(lse, "lse", shape[:3], torch.float32, dev)
     if workspace is None:
         need = int(L.gdn_prefix_attention_workspace_size(B, T, Hq, c.num_kv_heads, D))
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _workspace(need, dev, stream)
     st = L.gdn_prefix_attention(ctypes.byref(c), B, T, Hq, q.data_ptr(), qs, pp, prefix_len,
                                 pages.data_ptr(), max_pages, kv_len.data_ptr(),
                                 D ** -0.5 if scale is None else scale, dt, out.data_ptr(),
@@ -840,7 +851,7 @@ def gdn_token_logprobs(logits, targets, logprobs, entropy=None, *, top_ids=None,
     if workspace is None:
         need = int(L.gdn_token_logprobs_workspace_size(N, V, dt, k))
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = _workspace(need, dev, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = L.gdn_token_logprobs(N, V, dt, _ptr(logits), logits.stride(0) if N > 1 else V,
                               _ptr(targets), float(scale), _ptr(logprobs), _ptr(entropy), k,

@@ -589,6 +589,32 @@ def test_logprobs_hard_rows(gdn, v, dtype):
     _check_logprobs(gdn, x, t, 0)
 
 
+def test_own_workspace_belongs_to_the_stream(gdn, monkeypatch):
+    """A workspace that a call allocates comes from the stream it runs on (a Stream, a raw one)."""
+    x = torch.zeros(2, 5000, dtype=torch.bfloat16, device="cuda")
+    ent = torch.empty(2, device="cuda")
+    q = torch.zeros(1, 1, 2, 128, dtype=torch.bfloat16, device="cuda")
+    kv = torch.zeros(1, 1, 16, 128, dtype=torch.bfloat16, device="cuda")
+    one = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    seen, empty = [], torch.empty
+
+    def recorded(*a, **kw):
+        seen.append(torch.cuda.current_stream().cuda_stream)
+        return empty(*a, **kw)
+
+    monkeypatch.setattr(torch, "empty", recorded)
+    for stream in (side, side.cuda_stream):
+        gdn.gdn_token_logprobs(x, None, None, ent, stream=stream)
+        gdn.gdn_prefix_attention(q, kv, kv, out, pages=one, kv_len=one[0], stream=stream)
+    monkeypatch.undo()
+    side.synchronize()
+    _clean(gdn)
+    assert seen == [side.cuda_stream] * 4
+
+
 def test_logprobs_parts_and_streams(gdn):
     """Without targets or without entropy; on another stream; bit for bit the same again."""
     g = _gen(9)
