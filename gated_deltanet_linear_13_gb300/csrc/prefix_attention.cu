@@ -29,11 +29,12 @@
 // again, l = sum_j P'_j 2^(-e_j).
 //
 // Bound: many keys a row tile by the products (D = 256: 2.25 us a tile of 128 keys in bf16, 1.6 in
-// 8 bits, 87 and 100% of the measured rate over the three and five products; D = 128: 1.2 us, the
-// chain score, softmax, product); many short sequences by memory (128 sequences of up to 2048
-// tokens of their own on 4096: 103 us, 5.1 TB/s); a few keys by latency (one request on 512 + 37
-// keys: 12 us with the merge).  Measured in whole: 32 sequences on 16384, 8-bit, 42 us; 16 x 4
-// tokens on 32771, bf16, 71; 666 tokens on 20000, D = 128, 125.
+// 8 bits: over the three and the five products 87% of the bf16 rate of a library matrix product
+// and about twice that rate; D = 128: 1.2 us, the chain score, softmax, product); many short
+// sequences by memory (128 sequences of up to 2048 tokens of their own on 4096: 104 us, 5.0 TB/s);
+// a few keys by latency (one request on 512 + 37 keys: 12 us with the merge).  Measured in whole:
+// 32 sequences on 16384, 8-bit, 42 us; 16 x 4 tokens on 32771, bf16, 72; 666 tokens on 20000,
+// D = 128, 126.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
