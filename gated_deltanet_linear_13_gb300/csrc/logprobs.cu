@@ -349,7 +349,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       load(ahead[kDepth - 1]);
       nan = nan || top != top;
       if (top > m) {                                  // seldom after the first granules
-        const float d = (m - top) * p.c - off, s = ptx::ex2_approx(d);
+        const float to_mc = top * p.c;
+        const float to_off = fabsf(top) < 1e30f ? fmaf(top, p.c, -to_mc) : 0.0f;
+        // from 2^-mc to 2^-to_mc: both roundings, or the sums so far lose their weight
+        const float d = (m - top) * p.c - off + to_off, s = ptx::ex2_approx(d);
         const unsigned long long s2 = pair(s, s);
         if (s != 0.0f) {
           w2 = mul2(fma2(z2, pair(d, d), w2), s2);
@@ -358,12 +361,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           w2 = z2 = 0;
         }
         m = top;
-        mc = m * p.c;
-        off = fabsf(m) < 1e30f ? fmaf(m, p.c, -mc) : 0.0f;   // m c - mc, exactly
+        mc = to_mc;
+        off = to_off;                                 // m c - mc, exactly
       }
       if (least > -1e30f && m < 1e30f) {              // nothing below is infinite
-        // t = x c - mc in one rounding; t - off is meant, which the sums make up for when m
-        // changes and at the end
+        // t = x c - mc in one rounding; t - off is meant, which the sums make up for at the end
         const unsigned long long minus_mc = pair(-mc, -mc);
 #pragma unroll
         for (int e = 0; e < G::kPer; e += 2) {
