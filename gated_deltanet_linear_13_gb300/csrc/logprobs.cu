@@ -4,7 +4,8 @@
 // Per set of logits x: the maximum m, z = sum 2^t and w = sum 2^t t with t = (x - m) scale log2 e;
 // two sets join by rescaling to the larger maximum.  Then logp(i) = (x_i - m) scale - ln z and the
 // entropy is ln 2 (log2 z - w / z): centred on m, so that nothing cancels and nothing overflows
-// however large the logits are.
+// however large the logits are.  t is x c - m c in one rounding where m c is small enough for its
+// own rounding to be made up for afterwards, and (x - m) c elsewhere.
 //
 // The alternatives cost the pass one maximum a granule (the kilobyte that a warp takes at a time).
 // The k granules with the largest maxima hold the k best logits: a logit of another granule is
@@ -28,6 +29,8 @@
 // there are such instructions) and one of 16 exponentials a cycle.  Measured: 1000 rows of 151669
 // in fp32 100 us (6.1 TB/s); 64 rows of 248320 in bf16 with 20 alternatives 17.7 us, of which the
 // pass takes 11 and the join 6; one row 9.1 us, two launches.
+#include <float.h>
+
 #include "common.cuh"
 #include "sm100_ptx.cuh"
 
@@ -58,6 +61,8 @@ constexpr int kCtasPerSm = 4, kParts = 152 * kCtasPerSm * kWarps;
 // of logits
 constexpr int kHeld = 16, kGranulesAhead = 4, kLogitsAhead = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// a reference m c up to here rounds by at most a quarter, which 2^x takes without loss
+constexpr float kNear = 4194304.0f;
 
 template <typename T>
 struct Granule {
@@ -71,10 +76,21 @@ struct Stats {
   float m, z, w;
 };
 
+// (a - b) s, whose difference alone may overflow where s is tiny
+__device__ __forceinline__ float scaled_difference(float a, float b, float s) {
+  return (0.5f * a - 0.5f * b) * s * 2.0f;
+}
+
+// m c minus its rounding, exactly, where that is small enough to be used (else (x - m) c is)
+__device__ __forceinline__ float rounding(float m, float c) {
+  const float mc = m * c;
+  return fabsf(mc) <= kNear ? fmaf(m, c, -mc) : 0.0f;
+}
+
 __device__ __forceinline__ Stats merge(const Stats& a, const Stats& b, float c) {
   const float m = fmaxf(a.m, b.m);
   if (m == -INFINITY || a.z != a.z || b.z != b.z) return Stats{m, a.z + b.z, a.w + b.w};
-  const float da = (a.m - m) * c, db = (b.m - m) * c;
+  const float da = scaled_difference(a.m, m, c), db = scaled_difference(b.m, m, c);
   const float fa = ptx::ex2_approx(da), fb = ptx::ex2_approx(db);
   Stats r{m, 0.0f, 0.0f};
   // a side that underflows adds nothing (its da may be infinite)
@@ -190,6 +206,7 @@ struct Pieces {                            // how the line is cut
   int granules;                            // of a row
   int parts;                               // equal parts of the line, a warp's each
   float c;                                 // scale log2 e
+  float least;                             // logits above this stay finite when scaled by c
   float4* stats;                           // [row + part]: m, z, w
   uint32_t* tops;                          // [row][granule]: the largest logit's order bits
 };
@@ -331,9 +348,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const unsigned long long c2 = pair(p.c, p.c);
   while (left > 0) {
     // ---- this warp's granules of a row
-    float m = -INFINITY, mc = 0.0f, off = 0.0f;
+    float m = -INFINITY, above = INFINITY;            // (see below)
     unsigned long long z2 = 0, w2 = 0;                // pairs of sums
-    bool nan = false;
     const int q0 = q, q1 = q + left < p.granules ? q + left : p.granules;
 #pragma unroll kDepth
     for (; q < q1; ++q) {
@@ -347,25 +363,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         ahead[i][1] = ahead[i + 1][1];
       }
       load(ahead[kDepth - 1]);
-      nan = nan || top != top;
       if (top > m) {                                  // seldom after the first granules
-        const float to_mc = top * p.c;
-        const float to_off = fabsf(top) < 1e30f ? fmaf(top, p.c, -to_mc) : 0.0f;
-        // from 2^-mc to 2^-to_mc: both roundings, or the sums so far lose their weight
-        const float d = (m - top) * p.c - off + to_off, s = ptx::ex2_approx(d);
+        // The sums' reference is m c as it rounds where that is near, else m c itself.  They go
+        // from one to the next by both roundings, or what is summed so far loses its weight.
+        const float d = scaled_difference(m, top, p.c) - rounding(m, p.c) + rounding(top, p.c);
+        const float s = ptx::ex2_approx(d);
         const unsigned long long s2 = pair(s, s);
-        if (s != 0.0f) {
-          w2 = mul2(fma2(z2, pair(d, d), w2), s2);
-          z2 = mul2(z2, s2);
-        } else {
-          w2 = z2 = 0;
-        }
+        w2 = s != 0.0f ? mul2(fma2(z2, pair(d, d), w2), s2) : 0;
+        z2 = mul2(z2, s2);                            // (a NaN stays)
         m = top;
-        mc = to_mc;
-        off = to_off;                                 // m c - mc, exactly
+        above = fabsf(m * p.c) <= kNear ? p.least : INFINITY;
       }
-      if (least > -1e30f && m < 1e30f) {              // nothing below is infinite
-        // t = x c - mc in one rounding; t - off is meant, which the sums make up for at the end
+      const float mc = m * p.c;
+      if (least > above) {
+        // t = x c - mc in one rounding; that mc is rounded the sums make up for at the end
         const unsigned long long minus_mc = pair(-mc, -mc);
 #pragma unroll
         for (int e = 0; e < G::kPer; e += 2) {
@@ -376,12 +387,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           z2 = add2(z2, e2);
           if (kEntropy) w2 = fma2(e2, t2, w2);
         }
-      } else if (m != -INFINITY) {
-        const unsigned long long minus_m = pair(-m, -m);
+      } else if (m != -INFINITY || top != top) {
+        // infinite logits among them, or a reference too large to be taken off after scaling:
+        // then t = (x - m) c
+        const bool near = fabsf(mc) <= kNear;
+        const float sub = near ? 0.0f : m, base = near ? mc : 0.0f;
+        const unsigned long long minus_sub = pair(-sub, -sub), minus_base = pair(-base, -base);
 #pragma unroll
         for (int e = 0; e < G::kPer; e += 2) {
           float t0, t1;
-          unpair(fma2(add2(pair(f[e], f[e + 1]), minus_m), c2, pair(off, off)), &t0, &t1);
+          unpair(fma2(add2(pair(f[e], f[e + 1]), minus_sub), c2, minus_base), &t0, &t1);
           const unsigned long long e2 = pair(ptx::ex2_approx(t0), ptx::ex2_approx(t1));
           z2 = add2(z2, e2);
           // 0 * -inf is no part of the sum
@@ -398,8 +413,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     float z0, z1, w0, w1;
     unpair(z2, &z0, &z1);
     unpair(w2, &w0, &w1);
-    const float z = z0 + z1, up = ptx::ex2_approx(-off);
-    const Stats st = warp_merge(Stats{m, nan ? NAN : z * up, (w0 + w1 - off * z) * up}, p.c);
+    const float z = z0 + z1, off = rounding(m, p.c), up = ptx::ex2_approx(-off);
+    const Stats st = warp_merge(Stats{m, z * up, (w0 + w1 - off * z) * up}, p.c);
     if (lane == 0) p.stats[(long long)row + part] = make_float4(st.m, st.z, st.w, 0.0f);
     if (q == p.granules) {
       q = 0;
@@ -572,7 +587,9 @@ __global__ void __launch_bounds__(kThreads)
   const bool dead = st.m == -INFINITY && st.z == 0.0f;  // every logit -inf
   // (a merge rounds its two sides differently, so lanes may differ in the last bit)
   const float log2z = __shfl_sync(0xffffffffu, log2f(st.z), 0);
-  auto logp = [&](float v) { return dead ? -INFINITY : (v - st.m) * a.scale - kLn2 * log2z; };
+  auto logp = [&](float v) {
+    return dead ? -INFINITY : scaled_difference(v, st.m, a.scale) - kLn2 * log2z;
+  };
   auto store_top = [&](int rank, Key key) {
     a.top_ids[row * a.top_k + rank] = (int)~(uint32_t)key;
     a.top_logprobs[row * a.top_k + rank] = logp(bits_value((uint32_t)(key >> 32)));
@@ -693,7 +710,9 @@ cudaError_t gdn_launch_token_logprobs(const GdnLogprobArgs& a, cudaStream_t stre
   p.granules = granules_of(a.V, a.bf16);
   p.total = (long long)p.granules * a.N;
   p.parts = (int)(p.total < kParts ? p.total : kParts);
-  p.c = a.scale * kLog2e;
+  // twice it is finite too (a scale past 1e38 is cut short: differences below 1e-36 could tell)
+  p.c = fminf(a.scale * kLog2e, 0.5f * FLT_MAX);
+  p.least = -1e30f / p.c;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.stats = reinterpret_cast<float4*>(ws);
   p.tops = reinterpret_cast<uint32_t*>(ws + stats_bytes(a.N));

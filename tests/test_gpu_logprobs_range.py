@@ -87,3 +87,54 @@ def test_rising_rows_at_low_temperature(gdn, scale):
     x = torch.arange(v, device="cuda") * (0.75 / 256) - 0.75 * v / 256
     x = (x + torch.randn(n, v, generator=_gen(2), device="cuda")) / scale + 100.0
     _check(gdn, x, scale=scale)
+
+
+MASKS = [-1e9, -1e10, -1e12, -1e20, -1e29, -3e38]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale", [0.5, 1.0, 1 / 0.3, 10.0, 100.0])
+def test_large_finite_masks(gdn, scale, dtype):
+    """Tokens masked with a large finite number, whole stretches of the vocabulary and single ones,
+    -inf among them; rows that hold nothing else; rows of one or many huge logits."""
+    v, g = 100003, _gen(3)
+    rows = []
+    for mask in MASKS:
+        x = 2 * torch.randn(v, generator=g, device="cuda")
+        x[1000:] = mask                                     # a stretch
+        rows.append(x)
+        x = torch.full((v,), mask, device="cuda")           # a few live ones
+        x[[17, 50000, v - 1]] = torch.tensor([1.0, -2.0, 0.5], device="cuda")
+        rows.append(x)
+        x = 2 * torch.randn(v, generator=g, device="cuda")
+        x[torch.rand(v, generator=g, device="cuda") < 0.5] = mask
+        x[v // 2:v // 2 + 5000] = -math.inf
+        rows.append(x)
+        rows.append(torch.full((v,), mask, device="cuda"))  # nothing live
+        x = torch.full((v,), mask, device="cuda")
+        x[::3] = -math.inf
+        rows.append(x)
+    for top in (1e10, 1e20, 3e38):
+        x = 2 * torch.randn(v, generator=g, device="cuda")
+        x[40000] = top                                      # one huge logit
+        rows.append(x)
+        rows.append(torch.full((v,), top, device="cuda"))
+    _check(gdn, torch.stack(rows).to(dtype), scale=scale)
+
+
+@pytest.mark.parametrize("base", [2.9e6, 2.91e6, 1e7, 1e8])
+@pytest.mark.parametrize("v", [7001, 248320])
+def test_both_sides_of_the_centred_sums(gdn, base, v):
+    """Logits around and past the size from which a thread centres each logit before scaling it."""
+    x = base * (1 + 2e-6 * torch.rand(40, v, generator=_gen(4), device="cuda"))
+    x[:, ::7] = 2.5e6
+    _check(gdn, x)
+
+
+@pytest.mark.parametrize("scale,size", [(1e-38, 3e38), (1e-20, 1e21), (1e20, 1e-19), (1e20, 1e15),
+                                        (2e37, 1e-36), (1e-45, 1.0)])
+def test_scales_of_any_size(gdn, scale, size):
+    x = size * (2 * torch.rand(40, 30011, generator=_gen(5), device="cuda") - 1)
+    x[:10, 100:] = torch.finfo(torch.float32).min
+    x[5:15, ::5] = -math.inf
+    _check(gdn, x, scale=scale)
