@@ -87,6 +87,26 @@ inline cudaError_t set_carveout_once(K kernel, int percent, unsigned* done_mask)
   return e;
 }
 
+// ----------------------------------------------------------------- exponents of scaled differences
+// Sums of 2^((x - m) c) are taken as 2^(x c - mc), mc = m c as it rounds, in one rounding a term;
+// so each carries 2^rounding(m, c), which is made up for afterwards.  Up to kNear that is at most a
+// quarter of a binary order.  A larger reference would round by whole ones: (x - m) c then.
+constexpr float kNear = 4194304.0f;
+
+// m c minus its rounding, exactly; 0 where m c itself is the reference
+__device__ __forceinline__ float rounding(float m, float c) {
+  const float mc = m * c;
+  return fabsf(mc) <= kNear ? fmaf(m, c, -mc) : 0.0f;
+}
+// (a - b) c, whose difference alone may overflow where c is tiny
+__device__ __forceinline__ float scaled_difference(float a, float b, float c) {
+  return (0.5f * a - 0.5f * b) * c * 2.0f;
+}
+// the exponent from sums under one reference to sums under another
+__device__ __forceinline__ float reference_difference(float from, float to, float c) {
+  return scaled_difference(from, to, c) - rounding(from, c) + rounding(to, c);
+}
+
 // ----------------------------------------------------------------- programmatic dependent launch
 // A kernel launched with launch_pdl may start while the kernel before it in the stream is
 // still running: it does its set-up, then pdl_wait() (every thread) blocks until that kernel

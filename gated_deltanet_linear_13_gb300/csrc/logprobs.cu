@@ -61,8 +61,6 @@ constexpr int kCtasPerSm = 4, kParts = 152 * kCtasPerSm * kWarps;
 // of logits
 constexpr int kHeld = 16, kGranulesAhead = 4, kLogitsAhead = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// a reference m c up to here rounds by at most a quarter, which 2^x takes without loss
-constexpr float kNear = 4194304.0f;
 
 template <typename T>
 struct Granule {
@@ -75,17 +73,6 @@ struct Granule {
 struct Stats {
   float m, z, w;
 };
-
-// (a - b) s, whose difference alone may overflow where s is tiny
-__device__ __forceinline__ float scaled_difference(float a, float b, float s) {
-  return (0.5f * a - 0.5f * b) * s * 2.0f;
-}
-
-// m c minus its rounding, exactly, where that is small enough to be used (else (x - m) c is)
-__device__ __forceinline__ float rounding(float m, float c) {
-  const float mc = m * c;
-  return fabsf(mc) <= kNear ? fmaf(m, c, -mc) : 0.0f;
-}
 
 __device__ __forceinline__ Stats merge(const Stats& a, const Stats& b, float c) {
   const float m = fmaxf(a.m, b.m);
@@ -366,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       if (top > m) {                                  // seldom after the first granules
         // The sums' reference is m c as it rounds where that is near, else m c itself.  They go
         // from one to the next by both roundings, or what is summed so far loses its weight.
-        const float d = scaled_difference(m, top, p.c) - rounding(m, p.c) + rounding(top, p.c);
+        const float d = reference_difference(m, top, p.c);
         const float s = ptx::ex2_approx(d);
         const unsigned long long s2 = pair(s, s);
         w2 = s != 0.0f ? mul2(fma2(z2, pair(d, d), w2), s2) : 0;

@@ -35,6 +35,8 @@
 // a few keys by latency (one request on 512 + 37 keys: 12 us with the merge).  Measured in whole:
 // 32 sequences on 16384, 8-bit, 42 us; 16 x 4 tokens on 32771, bf16, 72; 666 tokens on 20000,
 // D = 128, 126.
+#include <float.h>
+
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -61,6 +63,8 @@ constexpr int kRows = 128, kKeys = 128;
 // 32 sequences of 24 heads 39.5 / 43.9 us, 64: 61.6 / 62.6, 100: 92.5 / 91.1, 128: 107.8 / 103.6).
 constexpr int kFewRows = 2048;
 constexpr long long kBlockBytes = 256ll << 20;
+// parts whose reference m lies past it leave the score that m is of as well
+constexpr float kFar = 0.25f * kNear;
 constexpr int KB = 1024;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -96,10 +100,12 @@ struct Params {
   GdnAttnArgs a;
   int G, row_tiles_p, row_tiles_s, prefix_tiles;
   int unit_cost;                   // tiles that a unit's start and end are worth
+  float coef;                      // see score_unit
   int blocks, block_tiles;         // the prefix's key tiles, cut into blocks (the last shorter)
   int rows_p, rows_s;              // rows stored a part (<= 128)
   float *o_p, *o_s;                // parts: [slot][D / 4][rows][4]
   float2 *ml_p, *ml_s;             // [slot][rows]: m (base 2), l
+  float *far_p, *far_s;            // [slot][rows]: where |m| > kFar, the score m is of (bf16 cache)
   int2 *span_p, *span_s;           // [unit]: the CTAs that have its first and its last tile
 };
 
@@ -261,6 +267,11 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
   if (!*abort) atomicOr(&g_err_attn, kErrTimeout);
   *abort = 1;
   return false;
+}
+
+// What a score is multiplied with, in binary orders (a scale of zero goes into Q).
+__host__ __device__ __forceinline__ float score_unit(float scale) {
+  return scale == 0.0f ? 1.0f : fminf(fabsf(scale) * kLog2e, FLT_MAX);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -602,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* sSum = reinterpret_cast<float*>(smem + Z::kSum);
     float* sQFac = reinterpret_cast<float*>(smem + Z::kQFac);
     // the scale's sign goes into Q, and so does a scale of zero
-    const float coef = p.a.scale == 0.0f ? 1.0f : fabsf(p.a.scale) * kLog2e;
+    const float coef = score_unit(p.a.scale);
     const uint32_t flip = p.a.scale < 0.0f ? 0x80008000u : 0u;
     const uint32_t keep = p.a.scale == 0.0f ? 0u : ~0u;
     // P may reach 2^kSlack over the reference: bf16 has fp32's range, so 32 leaves O and l far
@@ -716,6 +727,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // thread, so O stays until then.
     bool live = false, any_live = false;
     float m = -INFINITY, l = 0.0f;                    // reference, this half's sum
+    // bf16: the score whose product with rc m is, and whether m is large in a row of the warp: an
+    // m past kNear rounds by more than 2^x takes, and the reference is the product itself
+    float from = -INFINITY;
+    bool any_far = false;
     for (bool begun = false;; begun = true, ++turn) {
       const Item done = it;
       const bool more = walk.next(p, &it);
@@ -751,8 +766,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // m = -inf says that the row saw nothing; a row of NaN scores did
-        if (live && half == 0)
-          (done.prefix ? p.ml_p : p.ml_s)[slot * stored + r] = make_float2(l == l ? m : 0.0f, l);
+        if (live && half == 0) {
+          // (a score beyond what fp32 holds is still one)
+          const float ref = kF8 || from == -INFINITY ? m : fminf(fmaxf(m, -FLT_MAX), FLT_MAX);
+          (done.prefix ? p.ml_p : p.ml_s)[slot * stored + r] = make_float2(l == l ? ref : 0.0f, l);
+          if (!kF8 && fabsf(ref) > kFar) (done.prefix ? p.far_p : p.far_s)[slot * stored + r] = from;
+        }
         tc_fence_before();
       }
       if (!more) break;
@@ -804,15 +823,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           sm[half * 128 + r] = top;
           named_bar_sync(1 + quarter, 64);
           top = fmaxf(top, sm[(1 - half) * 128 + r]);
+          const float score = top;
           if constexpr (!kF8) top *= rc;
           // the reference: the first maximum; later only when it is passed by more than kSlack
-          const bool raise = top - kLift > m + kSlack;
+          bool raise = top - kLift > m + kSlack;
+          if (!kF8 && any_far && fabsf(m) > kNear)
+            raise = scaled_difference(score, from, rc) > kSlack;
           if (j == it.j0) {
             m = top - kLift;
+            if constexpr (!kF8) {
+              from = score;
+              any_far = __any_sync(0xffffffffu, fabsf(m) > kNear && score != -INFINITY);
+            }
           } else if (__any_sync(0xffffffffu, raise)) {
             const float mn = raise ? top - kLift : m;
-            const float f = raise ? ex2_approx(m - mn) : 1.0f;
+            float f = raise ? ex2_approx(m - mn) : 1.0f;
             m = mn;
+            if constexpr (!kF8) {
+              if (raise) {
+                if (any_far || fabsf(m) > kNear) f = ex2_approx(reference_difference(from, score, rc));
+                from = score;
+              }
+              any_far = __any_sync(0xffffffffu, fabsf(m) > kNear && from != -INFINITY);
+            }
             l *= f;
             wait(bar_pv + 8 * (buf ^ 1), ((g - 1) >> 1) & 1, sAbort);  // O of the tiles before
             tc_fence_after();
@@ -828,7 +861,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_wait_st();
           }
-          const float base = m == -INFINITY ? 0.0f : m;
+          float base = (kF8 ? m : from) == -INFINITY ? 0.0f : m;
+          if constexpr (!kF8) {
+            // s rc - m in one rounding; in the rows of a large m (s - from) rc
+            if (any_far) {
+              const bool far = fabsf(base) > kNear;
+              const float sub = far ? -from : 0.0f;
+              const unsigned long long minus_from = pair(sub, sub);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                unpair(add2(pair(s[2 * i], s[2 * i + 1]), minus_from), &s[2 * i], &s[2 * i + 1]);
+              if (far) base = 0.0f;
+            }
+          }
           const unsigned long long minus_base = pair(-base, -base);
           unsigned long long sum2[2] = {};            // pairs
           if constexpr (kF8) {
@@ -890,14 +935,59 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------------------- the merge
-//
+
+// A row whose references are so large that their rounding shows: its parts joined by the scores
+// that these are of, one after the other.  One 16-byte vector (cg) of row R of head h.
+template <int D>
+__device__ __noinline__ void join_far(const Params& p, int b, int h, unsigned R, int rs, bool own,
+                                      int cg, float4* acc, float* m, float* l) {
+  const int rt_p = (int)(R / kRows), rt_s = rs / kRows;
+  float top = -INFINITY;
+  for (int pass = 0; pass < 2; ++pass) {
+    auto unit = [&](int2 span, long long u, const float* o, const float2* ml, const float* far,
+                    int stored, int r) {
+      span.y = min(span.y, kCtas - 1);
+      for (int c = max(span.x, 0); c <= span.y; ++c) {
+        const long long at = (u + c) * stored + r;
+        const float2 v = ml[at];
+        if (v.x == -INFINITY) continue;
+        const bool counts = fabsf(v.x) > kFar;        // the others weigh nothing (NaN stays)
+        if (pass == 0) {
+          if (counts) top = fmaxf(top, far[at]);
+          continue;
+        }
+        const float w = counts ? ex2_approx(reference_difference(far[at], top, p.coef)) : 0.0f;
+        const float4 x =
+            reinterpret_cast<const float4*>(o)[((u + c) * (D / 4) + cg) * stored + r];
+        *l += v.y * w;
+        acc->x += x.x * w; acc->y += x.y * w; acc->z += x.z * w; acc->w += x.w * w;
+      }
+    };
+    if (pass == 1) {
+      *acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      *l = 0.0f;
+    }
+    for (int blk = 0; p.prefix_tiles > 0 && blk < p.blocks; ++blk) {
+      const long long u = ((long long)h * p.blocks + blk) * p.row_tiles_p + rt_p;
+      unit(p.span_p[u], u, p.o_p, p.ml_p, p.far_p, p.rows_p, R % kRows);
+    }
+    const long long u = ((long long)b * p.row_tiles_s + rt_s) * p.a.cache.H + h;
+    if (own) unit(p.span_s[u], u, p.o_s, p.ml_s, p.far_s, p.rows_s, rs % kRows);
+  }
+  *m = top * p.coef;
+}
+
 // A warp takes eight rows of one head (the parts lie with consecutive rows side by side) and 64
 // columns, and joins the rows' parts: the CTAs of a unit's span, one slot each.  Few rows are cut
 // into many parts: then (kGroups = 8) the eight warps of a block share out the parts of the same
 // rows, so that they are read at the same time, and join what they have in shared memory.  Bound
 // by the latency of the parts' loads, out of L2: 5 to 8 us of the whole.
-template <int D, typename Tout, int kGroups, int kAhead>
-__global__ void __launch_bounds__(256) gdn_prefix_merge_kernel(const Params p) {
+//
+// The bounds keep the bf16 cache's code at 80 registers, three blocks an SM (128 sequences, D = 128:
+// 48.3 us; with 64 registers 51.0).
+template <int D, typename Tout, int kGroups, int kAhead, bool kF8>
+__global__ void __launch_bounds__(256, kF8 ? 0 : kAhead == 4 ? 2 : 3)
+    gdn_prefix_merge_kernel(const Params p) {
   constexpr int kVec = 4;                             // 16-byte vectors a lane
   __shared__ float4 s_acc[kGroups][16][8];            // [warp][vector of the 64 columns][row]
   __shared__ float2 s_ml[kGroups][8];
@@ -971,6 +1061,8 @@ __global__ void __launch_bounds__(256) gdn_prefix_merge_kernel(const Params p) {
   const long long row = (long long)token * p.a.Hq + h * p.G + gh;
   Tout* out = static_cast<Tout*>(p.a.out) + row * D + blockIdx.z * 64;
   const bool lead = blockIdx.z == 0;
+  // (twice kFar: what lies below kFar then weighs nothing)
+  auto far = [&]() { return !kF8 && fabsf(m) > 2.0f * kFar && m != -INFINITY; };
   auto store = [&](int vec, const float* y) {
     // l is NaN where a score is, 0 where no key is seen
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -985,6 +1077,18 @@ __global__ void __launch_bounds__(256) gdn_prefix_merge_kernel(const Params p) {
   };
   if constexpr (kGroups == 1) {
     if (R0 >= rows) return;
+    if (far()) {
+      float4 x;
+      float m1, l1;
+#pragma unroll 1
+      for (int q = 0; q < kVec; ++q) {
+        join_far<D>(p, b, h, R, rs, own, cg + 4 * q, &x, &m1, &l1);
+        m = m1, l = l1;
+        const float y[4] = {x.x, x.y, x.z, x.w};
+        store(4 * q + (lane >> 3), y);
+      }
+      return;
+    }
 #pragma unroll
     for (int q = 0; q < kVec; ++q) store(4 * q + (lane >> 3), acc + 4 * q);
   } else {
@@ -1014,11 +1118,18 @@ __global__ void __launch_bounds__(256) gdn_prefix_merge_kernel(const Params p) {
       l += v[i].y * w;
       y[0] += x.x * w; y[1] += x.y * w; y[2] += x.z * w; y[3] += x.w * w;
     }
+    if (far()) {
+      float4 x;
+      float m1, l1;
+      join_far<D>(p, b, h, R, rs, own, blockIdx.z * 16 + vec, &x, &m1, &l1);
+      m = m1, l = l1;
+      y[0] = x.x, y[1] = x.y, y[2] = x.z, y[3] = x.w;
+    }
     store(vec, y);
   }
 }
 
-template <int D, typename Tout>
+template <int D, typename Tout, bool kF8>
 cudaError_t launch_merge(const Params& p, cudaStream_t stream) {
   const long long eights = ((long long)p.a.B * p.a.T * p.G + 7) / 8;
   const unsigned H = (unsigned)p.a.cache.H, Z = D / 64;
@@ -1026,12 +1137,12 @@ cudaError_t launch_merge(const Params& p, cudaStream_t stream) {
   // (32 sequences, 16384 shared tokens, 384 blocks: 43.2 us with four, 41.5 with two; 16
   // sequences, 192 blocks: 29.3 and 30.5)
   if (eights * H * Z <= 2 * kCtas)
-    return launch_pdl(true, gdn_prefix_merge_kernel<D, Tout, 8, 4>, dim3((unsigned)eights, H, Z),
+    return launch_pdl(true, gdn_prefix_merge_kernel<D, Tout, 8, 4, kF8>, dim3((unsigned)eights, H, Z),
                       dim3(256), 0, stream, p);
   if (eights * H <= kFewRows / 8)
-    return launch_pdl(true, gdn_prefix_merge_kernel<D, Tout, 8, 2>, dim3((unsigned)eights, H, Z),
+    return launch_pdl(true, gdn_prefix_merge_kernel<D, Tout, 8, 2, kF8>, dim3((unsigned)eights, H, Z),
                       dim3(256), 0, stream, p);
-  return launch_pdl(true, gdn_prefix_merge_kernel<D, Tout, 1, 2>,
+  return launch_pdl(true, gdn_prefix_merge_kernel<D, Tout, 1, 2, kF8>,
                     dim3((unsigned)((eights + 7) / 8), H, Z), dim3(256), 0, stream, p);
 }
 
@@ -1039,7 +1150,7 @@ cudaError_t launch_merge(const Params& p, cudaStream_t stream) {
 
 struct Layout {
   int row_tiles_p, row_tiles_s, rows_p, rows_s;
-  size_t span_p, span_s, ml_p, ml_s, o_p, o_s, total;
+  size_t span_p, span_s, ml_p, ml_s, far_p, far_s, o_p, o_s, total;
 };
 
 Layout layout_of(int B, int T, int Hq, int H, int D) {
@@ -1060,6 +1171,8 @@ Layout layout_of(int B, int T, int Hq, int H, int D) {
   y.span_s = off; off += up(8 * (size_t)B * y.row_tiles_s * H);
   y.ml_p = off; off += up(8 * np);
   y.ml_s = off; off += up(8 * ns);
+  y.far_p = off; off += up(4 * np);
+  y.far_s = off; off += up(4 * ns);
   y.o_p = off; off += up(4 * np * D);
   y.o_s = off; off += up(4 * ns * D);
   y.total = off;
@@ -1085,7 +1198,8 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
   e = launch_pdl(false, gdn_prefix_attention_kernel<D, kF8>, dim3(kCtas), dim3(kThreads), Z::kBytes,
                  stream, p, mk, mv);
   if (e != cudaSuccess) return e;
-  return p.a.out_bf16 ? launch_merge<D, __nv_bfloat16>(p, stream) : launch_merge<D, float>(p, stream);
+  return p.a.out_bf16 ? launch_merge<D, __nv_bfloat16, kF8>(p, stream)
+                       : launch_merge<D, float, kF8>(p, stream);
 }
 
 }  // namespace
@@ -1120,12 +1234,15 @@ cudaError_t gdn_launch_prefix_attention(const GdnAttnArgs& a, cudaStream_t strea
   // 1000 tokens, bf16, D = 256: 110 / 117 us; the same at D = 128: 70 / 67; prompt of 666 tokens
   // on 20000, D = 128: 162 / 143; 32 sequences on 16384, 8-bit, D = 256: 44 / 43)
   p.unit_cost = a.cache.D == 256 && !a.cache.f8 ? 1 : 2;
+  p.coef = score_unit(a.scale);
   p.rows_p = y.rows_p;
   p.rows_s = y.rows_s;
   p.span_p = reinterpret_cast<int2*>(ws + y.span_p);
   p.span_s = reinterpret_cast<int2*>(ws + y.span_s);
   p.ml_p = reinterpret_cast<float2*>(ws + y.ml_p);
   p.ml_s = reinterpret_cast<float2*>(ws + y.ml_s);
+  p.far_p = a.cache.f8 ? nullptr : reinterpret_cast<float*>(ws + y.far_p);
+  p.far_s = a.cache.f8 ? nullptr : reinterpret_cast<float*>(ws + y.far_s);
   p.o_p = reinterpret_cast<float*>(ws + y.o_p);
   p.o_s = reinterpret_cast<float*>(ws + y.o_s);
   if (a.cache.D == 128)

@@ -66,24 +66,26 @@ def _check(gdn, c, q, scale):
 
 
 @pytest.mark.parametrize("prefix,own", [(0, 1), (0, 90), (4000, 1), (5000, 200)])
-@pytest.mark.parametrize("power,sign", [(20, 1), (22, -1), (24, 1), (27, -1), (27, 1), (33, 1),
-                                        (40, -1), (60, 1)])
+@pytest.mark.parametrize("power,lead", [(20, 1.0), (22, -1.0), (24, 1.0), (27, -1.0), (27, 1.0),
+                                        (33, 1.0), (40, -1.0), (60, 1.0), (33, 1.5), (34, -1.5)])
 @pytest.mark.parametrize("unit", ["nat", "raw"])
-def test_scores_of_any_size(gdn, unit, power, sign, prefix, own):
-    """Scores of 2^power units and a few units of their last place more, at a scale that makes such
-    a unit one (nat), or at scale 1 (raw): far past what 2^score, or a rounding of it, could hold."""
-    last = 2 ** (power - 22)                 # at least a unit of the last place of all scores
+def test_scores_of_any_size(gdn, unit, power, lead, prefix, own):
+    """Scores of lead 2^power and a few units of their last place more, at a scale that makes such
+    a unit one (nat), or at scale 1 (raw): far past what 2^score, or a rounding of it, could hold.
+    (With a lead of 1.5 scores that differ by a unit are the same once scaled by log2 e.)"""
+    # at least a unit of the last place of all scores
+    last = 2.0 ** (power - (22 if abs(lead) == 1.0 else 23))
 
     def rows(g, n):
         k = torch.zeros(n, H, D, device="cuda")
-        k[..., 5] = sign * 2.0 ** (power // 2)
+        k[..., 5] = lead * 2.0 ** (power // 2)
         k[..., 77] = torch.randint(-3, 4, (n, H), generator=g, device="cuda").float()
         return k.to(torch.bfloat16)
 
     c = _case(rows, prefix, own, power + prefix)
     q = torch.zeros(2, 1, H * GROUP, D, device="cuda")
     q[..., 5] = 2.0 ** (power - power // 2)
-    q[..., 77] = float(last)
+    q[..., 77] = last
     _check(gdn, c, q.to(torch.bfloat16), 1.0 / last if unit == "nat" else 1.0)
 
 
