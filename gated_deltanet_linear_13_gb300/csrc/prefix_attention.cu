@@ -615,7 +615,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the scale's sign goes into Q, and so does a scale of zero
     const float coef = score_unit(p.a.scale);
     const uint32_t flip = p.a.scale < 0.0f ? 0x80008000u : 0u;
-    const uint32_t keep = p.a.scale == 0.0f ? 0u : ~0u;
     // P may reach 2^kSlack over the reference: bf16 has fp32's range, so 32 leaves O and l far
     // from overflow and a raise to rows whose first tile says little; e5m2 ends at 57344, so the
     // reference lies kLift below the maximum and P starts at 2^kLift
@@ -654,7 +653,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       asm volatile("cp.async.wait_all;\n" ::: "memory");
-      if (kF8 || p.a.scale <= 0.0f) {
+      if (p.a.scale == 0.0f) {
+        // zero times Q: NaN is left where an element is not finite
+        auto times0 = [](uint32_t w) -> uint32_t {
+          return ((w & 0x7f80u) == 0x7f80u ? 0x7fc0u : 0u) |
+                 ((w & 0x7f800000u) == 0x7f800000u ? 0x7fc00000u : 0u);
+        };
+#pragma unroll 1
+        for (int row = sw * kPer + lane / L; row < n; row += 8 * kPer) {
+          uint4* u = reinterpret_cast<uint4*>(smem + at(row));
+          *u = make_uint4(times0(u->x), times0(u->y), times0(u->z), times0(u->w));
+        }
+      }
+      if (kF8 || p.a.scale < 0.0f) {
         constexpr int kAt = 4;                        // passes side by side
 #pragma unroll 1
         for (int r0 = sw * kPer; r0 < n; r0 += kAt * 8 * kPer) {
@@ -665,8 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = r0 + i * 8 * kPer + lane / L;
             const uint4 u = row < n ? *reinterpret_cast<const uint4*>(smem + at(row))
                                     : make_uint4(0, 0, 0, 0);
-            w[i][0] = (u.x & keep) ^ flip; w[i][1] = (u.y & keep) ^ flip;
-            w[i][2] = (u.z & keep) ^ flip; w[i][3] = (u.w & keep) ^ flip;
+            w[i][0] = u.x ^ flip; w[i][1] = u.y ^ flip;
+            w[i][2] = u.z ^ flip; w[i][3] = u.w ^ flip;
             if (!kF8 && row < n)
               *reinterpret_cast<uint4*>(smem + at(row)) =
                   make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);

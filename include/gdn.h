@@ -478,9 +478,12 @@ gdn_status gdn_kv_cache_read(const gdn_kv_cache* cache, int32_t n, const int32_t
  * the probabilities enter the second product with 16 significant bits (bf16 cache: two bf16
  * terms) or 11 (e4m3 cache: three e5m2 terms, and no finer than 2^-25 of the row's largest, each
  * weighted with its value's scale).  bf16 values above 2^64 may overflow the sums.
- * A query with an infinity or a NaN makes its row NaN, a key with one the rows that see it, a
- * value with one (of a token that some row sees) every row that shares its products: the
- * sequence's rows, or the batch's for the prefix.
+ * A NaN in a query makes its row NaN, one in a key the rows that see it (at a scale of zero too).
+ * An infinity in a query does the same with an e4m3 cache, and in any query at a scale of zero;
+ * else it counts, as one in a key of a bf16 cache does, by the scores that it makes: +inf or NaN
+ * makes the row NaN, -inf leaves the key no weight.  A NaN or an infinity in a value (of a token
+ * that some row sees) does so to every row that shares its products: the sequence's rows, or the
+ * batch's for the prefix.
  */
 size_t gdn_prefix_attention_workspace_size(int32_t batch, int32_t seqlen, int32_t num_heads,
                                            int32_t num_kv_heads, int32_t head_dim);
