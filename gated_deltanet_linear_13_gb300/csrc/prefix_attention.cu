@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_addr(sTmem), 512);
     tmem_relinquish();
   }
-  if (warp == 0 && lane == 0) {
+  if (warp == 0 && lane == 0 && p.a.cache.num_pages > 0) {   // (an empty cache has no maps)
     tma_prefetch_desc(&map_k);
     tma_prefetch_desc(&map_v);
   }
