@@ -204,6 +204,15 @@ def _workspace(need: int, device: torch.device, stream) -> torch.Tensor:
         return torch.empty(need, dtype=torch.uint8, device=device)
 
 
+def _workspace_bytes(workspace: torch.Tensor, device: torch.device) -> int:
+    """The bytes of a caller's workspace, which the kernels take as one piece of the device's."""
+    if workspace.device != device:
+        raise ValueError(f"workspace: on {workspace.device}, expected {device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.nbytes
+
+
 def _check(status: int, where: str):
     if status != GDN_OK:
         raise GDNError(status, where)
@@ -805,8 +814,8 @@ def gdn_prefix_attention(q, k_cache, v_cache, out, *, pages, kv_len, prefix_page
     st = L.gdn_prefix_attention(ctypes.byref(c), B, T, Hq, q.data_ptr(), qs, pp, prefix_len,
                                 pages.data_ptr(), max_pages, kv_len.data_ptr(),
                                 D ** -0.5 if scale is None else scale, dt, out.data_ptr(),
-                                _ptr(lse), workspace.data_ptr(), workspace.nbytes,
-                                _stream_of(stream, dev))
+                                _ptr(lse), workspace.data_ptr(),
+                                _workspace_bytes(workspace, dev), _stream_of(stream, dev))
     _check(st, "gdn_prefix_attention")
     return out
 
@@ -852,7 +861,7 @@ def gdn_token_logprobs(logits, targets, logprobs, entropy=None, *, top_ids=None,
         need = int(L.gdn_token_logprobs_workspace_size(N, V, dt, k))
         if need:
             workspace = _workspace(need, dev, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_bytes = 0 if workspace is None else _workspace_bytes(workspace, dev)
     st = L.gdn_token_logprobs(N, V, dt, _ptr(logits), logits.stride(0) if N > 1 else V,
                               _ptr(targets), float(scale), _ptr(logprobs), _ptr(entropy), k,
                               _ptr(top_ids), _ptr(top_logprobs), _ptr(workspace), ws_bytes,
