@@ -8,12 +8,7 @@ using namespace gdn;
 
 static __device__ unsigned int g_err_ckpt;
 
-unsigned gdn_take_error_checkpoint() {
-  unsigned v = 0, z = 0;
-  cudaMemcpyFromSymbol(&v, g_err_ckpt, sizeof(v));
-  cudaMemcpyToSymbol(g_err_ckpt, &z, sizeof(z));
-  return v;
-}
+unsigned gdn_take_error_checkpoint() { return gdn::take_error(g_err_ckpt); }
 
 __global__ void __launch_bounds__(256) gdn_checkpoint_kernel(
     int op, long long state_v4, long long conv_v4, float4* state, uint4* conv_state,

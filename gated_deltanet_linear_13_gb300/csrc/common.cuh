@@ -30,6 +30,17 @@ __device__ __forceinline__ bool in_bounds(unsigned int* word, bool ok) {
 __device__ __forceinline__ constexpr bool in_bounds(unsigned int*, bool) { return true; }
 #endif
 
+// A translation unit's error word, read and cleared on the host.  A word that nothing was recorded
+// in is not written: the copies are the query's time (ten words: 94 us, with the writes 129).
+template <typename Word>
+inline unsigned take_error(const Word& word) {
+  unsigned v = 0;
+  const unsigned zero = 0;
+  cudaMemcpyFromSymbol(&v, word, sizeof(v));
+  if (v) cudaMemcpyToSymbol(word, &zero, sizeof(zero));
+  return v;
+}
+
 // ----------------------------------------------------------------- element access
 
 __device__ __forceinline__ float ld_elem(const float* p) { return *p; }

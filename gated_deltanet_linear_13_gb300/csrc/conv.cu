@@ -22,12 +22,7 @@ using namespace gdn::ptx;
 
 static __device__ unsigned int g_err_conv;
 
-unsigned gdn_take_error_conv() {
-  unsigned v = 0, z = 0;
-  cudaMemcpyFromSymbol(&v, g_err_conv, sizeof(v));
-  cudaMemcpyToSymbol(g_err_conv, &z, sizeof(z));
-  return v;
-}
+unsigned gdn_take_error_conv() { return gdn::take_error(g_err_conv); }
 
 constexpr int TT = 64;             // tokens per CTA tile
 constexpr int TG = 16;             // tokens per thread (a CTA has TT / TG token groups)

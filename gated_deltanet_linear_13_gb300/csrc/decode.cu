@@ -29,12 +29,7 @@ using namespace gdn::ptx;
 
 static __device__ unsigned int g_err_decode;
 
-unsigned gdn_take_error_decode() {
-  unsigned v = 0, z = 0;
-  cudaMemcpyFromSymbol(&v, g_err_decode, sizeof(v));
-  cudaMemcpyToSymbol(g_err_decode, &z, sizeof(z));
-  return v;
-}
+unsigned gdn_take_error_decode() { return gdn::take_error(g_err_decode); }
 
 // Conv of one channel: window = [old state (W-1 values, oldest first), new input]; the new
 // state (the last W-1 inputs) is written back by the caller through conv_store_state.

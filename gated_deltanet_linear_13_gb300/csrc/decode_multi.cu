@@ -54,12 +54,7 @@ using namespace gdn;
 
 static __device__ unsigned int g_err_multi;
 
-unsigned gdn_take_error_decode_multi() {
-  unsigned v = 0, z = 0;
-  cudaMemcpyFromSymbol(&v, g_err_multi, sizeof(v));
-  cudaMemcpyToSymbol(g_err_multi, &z, sizeof(z));
-  return v;
-}
+unsigned gdn_take_error_decode_multi() { return gdn::take_error(g_err_multi); }
 
 namespace {
 

@@ -21,12 +21,7 @@ using namespace gdn;
 
 static __device__ unsigned int g_err_kv;
 
-unsigned gdn_take_error_kv_cache() {
-  unsigned v = 0, z = 0;
-  cudaMemcpyFromSymbol(&v, g_err_kv, sizeof(v));
-  cudaMemcpyToSymbol(g_err_kv, &z, sizeof(z));
-  return v;
-}
+unsigned gdn_take_error_kv_cache() { return gdn::take_error(g_err_kv); }
 
 namespace {
 

@@ -43,12 +43,7 @@ using ptx::unpair;
 
 static __device__ unsigned int g_err_lp;
 
-unsigned gdn_take_error_logprobs() {
-  unsigned v = 0, z = 0;
-  cudaMemcpyFromSymbol(&v, g_err_lp, sizeof(v));
-  cudaMemcpyToSymbol(g_err_lp, &z, sizeof(z));
-  return v;
-}
+unsigned gdn_take_error_logprobs() { return gdn::take_error(g_err_lp); }
 
 namespace {
 

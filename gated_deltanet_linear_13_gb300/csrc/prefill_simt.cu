@@ -23,12 +23,7 @@ using namespace gdn;
 
 static __device__ unsigned int g_err_simt;
 
-unsigned gdn_take_error_prefill_simt() {
-  unsigned v = 0, z = 0;
-  cudaMemcpyFromSymbol(&v, g_err_simt, sizeof(v));
-  cudaMemcpyToSymbol(g_err_simt, &z, sizeof(z));
-  return v;
-}
+unsigned gdn_take_error_prefill_simt() { return gdn::take_error(g_err_simt); }
 
 namespace {
 constexpr int C = kChunk, D = kHeadDim, R = 32, NSPLIT = D / R;

@@ -54,12 +54,7 @@ using namespace gdn::ptx;
 
 static __device__ unsigned int g_err_tc;
 
-unsigned gdn_take_error_prefill_tc() {
-  unsigned v = 0, z = 0;
-  cudaMemcpyFromSymbol(&v, g_err_tc, sizeof(v));
-  cudaMemcpyToSymbol(g_err_tc, &z, sizeof(z));
-  return v;
-}
+unsigned gdn_take_error_prefill_tc() { return gdn::take_error(g_err_tc); }
 
 namespace {
 

@@ -48,12 +48,7 @@ using namespace gdn::ptx;
 
 static __device__ unsigned int g_err_attn;
 
-unsigned gdn_take_error_prefix_attention() {
-  unsigned v = 0, z = 0;
-  cudaMemcpyFromSymbol(&v, g_err_attn, sizeof(v));
-  cudaMemcpyToSymbol(g_err_attn, &z, sizeof(z));
-  return v;
-}
+unsigned gdn_take_error_prefix_attention() { return gdn::take_error(g_err_attn); }
 
 namespace {
 

@@ -16,12 +16,7 @@ using namespace gdn;
 
 static __device__ unsigned int g_err_varlen;
 
-unsigned gdn_take_error_varlen() {
-  unsigned v = 0, z = 0;
-  cudaMemcpyFromSymbol(&v, g_err_varlen, sizeof(v));
-  cudaMemcpyToSymbol(g_err_varlen, &z, sizeof(z));
-  return v;
-}
+unsigned gdn_take_error_varlen() { return gdn::take_error(g_err_varlen); }
 
 constexpr int PREP_THREADS = 1024;
 
