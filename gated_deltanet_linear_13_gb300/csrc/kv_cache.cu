@@ -79,7 +79,10 @@ __device__ __forceinline__ long long row_of(const GdnKvCacheArgs& c, int slot, i
     atomicOr(&g_err_kv, kErrIndex);
     return -1;
   }
-  return (((long long)page * c.H + head) << c.page_shift) + off;
+  const long long row = (((long long)page * c.H + head) << c.page_shift) + off;
+  return in_bounds(&g_err_kv, head < c.H && row < ((long long)c.num_pages * c.H << c.page_shift))
+             ? row
+             : -1;
 }
 
 // Grid: x tokens, y = keys of head 0 .. H - 1, then values.  d / 8 lanes a vector; a thread has
@@ -102,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_append_kernel(
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
     const int t = t0 + i * kStep;
-    slot[i] = t < n ? slots[t] : -1;
+    slot[i] = t < n && in_bounds(&g_err_kv, t >= 0) ? slots[t] : -1;
     x[i] = load8(src + min(t, n - 1) * stride);       // (whole warps stay for the shuffles)
   }
 #pragma unroll
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_read_kernel(GdnKvCacheArgs c,
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
     const int t = t0 + i * kStep;
-    row[i] = row_of(c, t < n ? slots[t] : -1, head);
+    row[i] = row_of(c, t < n && in_bounds(&g_err_kv, t >= 0) ? slots[t] : -1, head);
   }
   Vec8 x[kTokens];
   if constexpr (!kF8) {
@@ -182,7 +185,8 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_read_kernel(GdnKvCacheArgs c,
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
     const int t = t0 + i * kStep;
-    if (t < n) store8((values ? v_out : k_out) + ((long long)t * c.H + head) * D + lane * 8, x[i]);
+    if (t < n && in_bounds(&g_err_kv, t >= 0 && head < c.H && lane * 8 + 8 <= D))
+      store8((values ? v_out : k_out) + ((long long)t * c.H + head) * D + lane * 8, x[i]);
   }
 }
 

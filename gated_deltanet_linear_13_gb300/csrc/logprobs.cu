@@ -312,7 +312,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (aleft <= 0) return;
     if (aq > 0 && aq + 2 < p.granules) {              // all of it the row's
 #pragma unroll
-      for (int v = 0; v < 2; ++v) to[v] = load_inner(ap + v * 32 * G::kVec);
+      for (int v = 0; v < 2; ++v) {
+        const T* at = ap + v * 32 * G::kVec;
+        if (in_bounds(&g_err_lp, at >= ax && at + G::kVec <= ax + a.V)) to[v] = load_inner(at);
+      }
     } else {
 #pragma unroll
       for (int v = 0; v < 2; ++v) to[v] = load_vec(ax, ap - ax + v * 32 * G::kVec, a.V);
@@ -387,7 +390,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
       if constexpr (kTop) {
         const uint32_t bits = __reduce_max_sync(0xffffffffu, order_bits(top));
-        if (lane == 0) p.tops[(long long)row * p.granules + q] = bits;
+        if (lane == 0 && in_bounds(&g_err_lp, row < a.N && q < p.granules))
+          p.tops[(long long)row * p.granules + q] = bits;
       }
     }
     left -= q1 - q0;
@@ -397,7 +401,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     unpair(w2, &w0, &w1);
     const float z = z0 + z1, off = rounding(m, p.c), up = ptx::ex2_approx(-off);
     const Stats st = warp_merge(Stats{m, z * up, (w0 + w1 - off * z) * up}, p.c);
-    if (lane == 0) p.stats[(long long)row + part] = make_float4(st.m, st.z, st.w, 0.0f);
+    if (lane == 0 && in_bounds(&g_err_lp, row < a.N && part < kParts))
+      p.stats[(long long)row + part] = make_float4(st.m, st.z, st.w, 0.0f);
     if (q == p.granules) {
       q = 0;
       ++row;
@@ -517,6 +522,7 @@ __global__ void __launch_bounds__(kThreads)
   Stats st{-INFINITY, 0.0f, 0.0f};
   constexpr int kOthers = kTop && kRowWarps > 1 ? kRowWarps - 1 : kRowWarps;
   for (int i = (sub - (kRowWarps - kOthers)) * 32 + lane; i >= 0 && i < pieces; i += kOthers * 32) {
+    if (!in_bounds(&g_err_lp, c0 >= 0 && c0 + i < kParts)) break;
     const float4 v = p.stats[row + c0 + i];
     st = merge(st, Stats{v.x, v.y, v.z}, p.c);
   }
@@ -525,6 +531,7 @@ __global__ void __launch_bounds__(kThreads)
   if constexpr (kTop) {
     sync();
     if (p.granules > a.top_k) granule = s_granule[slot][lane], floor = s_floor[slot];
+    if (lane < n && !in_bounds(&g_err_lp, granule >= 0 && granule < p.granules)) granule = 0;
     // their vectors that reach it
     for (int i0 = sub; i0 < n; i0 += kRowWarps * kGranulesAhead) {
       uint4 u[2 * kGranulesAhead];
@@ -573,6 +580,7 @@ __global__ void __launch_bounds__(kThreads)
     return dead ? -INFINITY : scaled_difference(v, st.m, a.scale) - kLn2 * log2z;
   };
   auto store_top = [&](int rank, Key key) {
+    if (!in_bounds(&g_err_lp, rank >= 0 && rank < a.top_k && ~(uint32_t)key < (uint32_t)a.V)) return;
     a.top_ids[row * a.top_k + rank] = (int)~(uint32_t)key;
     a.top_logprobs[row * a.top_k + rank] = logp(bits_value((uint32_t)(key >> 32)));
   };

@@ -141,6 +141,17 @@ __device__ __forceinline__ long long head_len(const Params& p) {
          ((long long)(p.blocks - 1) * unit_len(p, p.block_tiles) + block_len(p, p.blocks - 1));
 }
 
+// What the workspace has room for (index checks): units, and parts' slots.
+__device__ __forceinline__ long long unit_room(const Params& p, bool prefix) {
+  return prefix ? max((long long)p.a.cache.H * p.row_tiles_p, (long long)kCtas)
+                : (long long)p.a.B * p.row_tiles_s * p.a.cache.H;
+}
+__device__ __forceinline__ bool in_workspace(const Params& p, bool prefix, long long unit, int c,
+                                             int r) {
+  return in_bounds(&g_err_attn, unit >= 0 && unit < unit_room(p, prefix) && c >= 0 && c < kCtas &&
+                                    r >= 0 && r < (prefix ? p.rows_p : p.rows_s));
+}
+
 // One CTA's piece of a unit.
 struct Item {
   bool prefix, first, last; // the prefix's or a sequence's; has the unit's first, last tile
@@ -418,13 +429,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto row_of = [&](int j) -> int {                 // of this lane's page of key tile j
       const int i = j * per + lane;
       if (lane >= per || (long long)i * page >= it.keys) return outside;
+      if (!in_bounds(&g_err_attn, it.prefix ? (long long)i * page < p.a.prefix_len
+                                            : it.b < p.a.B && i < p.a.max_pages))
+        return outside;
       const int id = it.prefix ? p.a.prefix_pages[i]
                                : p.a.pages[(long long)it.b * p.a.max_pages + i];
       if ((unsigned)id >= (unsigned)p.a.cache.num_pages) {
         atomicOr(&g_err_attn, kErrIndex);
         return outside;
       }
-      return id * head_rows + (it.h << shift);
+      const int row = id * head_rows + (it.h << shift);
+      return in_bounds(&g_err_attn, row >= 0 && row < outside) ? row : outside;
     };
     uint32_t last = 0;                                // ring position after this warp's last fill
     auto fill = [&](uint32_t ring, int row) {
@@ -574,8 +589,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      : p.a.pages[(long long)it.b * p.a.max_pages + i];
             if ((unsigned)id < (unsigned)p.a.cache.num_pages) {
               const long long r = (((long long)id * p.a.cache.H + it.h) << shift) + (key & pm);
-              ke = *reinterpret_cast<const uint32_t*>(p.a.cache.k_exp + r);
-              ve = *reinterpret_cast<const uint32_t*>(p.a.cache.v_exp + r);
+              if (in_bounds(&g_err_attn,
+                            r + 4 <= ((long long)p.a.cache.num_pages * p.a.cache.H << shift))) {
+                ke = *reinterpret_cast<const uint32_t*>(p.a.cache.k_exp + r);
+                ve = *reinterpret_cast<const uint32_t*>(p.a.cache.v_exp + r);
+              }
             }
           }
           float ks[4], ev[4], iv[4];
@@ -639,9 +657,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   (long long)it.h * p.G * D + ql * 8;
 #pragma unroll 2
         for (; row < n; row += 8 * kPer) {
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(sb + at(row)),
-                       "l"(q0 + t * p.a.q_stride + gh * D)
-                       : "memory");
+          if (in_bounds(&g_err_attn, (it.prefix ? 0 : it.b) * p.a.T + (int)t < p.a.B * p.a.T &&
+                                         it.h * p.G + (int)gh < p.a.Hq && row < kRows))
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(sb + at(row)),
+                         "l"(q0 + t * p.a.q_stride + gh * D)
+                         : "memory");
           gh += dg;
           t += dt;
           if (gh >= (unsigned)p.G) gh -= p.G, ++t;
@@ -743,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (more) load_q(it);
       // ---- the part: O, m, l of the item's rows
       if (begun) wait(bar_pv + 8 * ((g - 1) & 1), ((g - 1) >> 1) & 1, sAbort);
-      if (begun && r == 0 && half == 0) {
+      if (begun && r == 0 && half == 0 && in_workspace(p, done.prefix, done.unit, c, 0)) {
         // where the merge finds the unit's parts
         int2* span = (done.prefix ? p.span_p : p.span_s) + done.unit;
         if (done.first) span->x = c;
@@ -764,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float o[32];
           tmem_ld32(tmem + TM_O + lane_base + half * (D / 2) + 4 * i, o);
           tmem_wait_ld();
-          if (live) {
+          if (live && in_workspace(p, done.prefix, done.unit, c, r)) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               op[(long long)(i + e) * stored] =
@@ -772,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // m = -inf says that the row saw nothing; a row of NaN scores did
-        if (live && half == 0) {
+        if (live && half == 0 && in_workspace(p, done.prefix, done.unit, c, r)) {
           // (a score beyond what fp32 holds is still one)
           const float ref = kF8 || from == -INFINITY ? m : fminf(fmaxf(m, -FLT_MAX), FLT_MAX);
           (done.prefix ? p.ml_p : p.ml_s)[slot * stored + r] = make_float2(l == l ? ref : 0.0f, l);
@@ -950,10 +970,11 @@ __device__ __noinline__ void join_far(const Params& p, int b, int h, unsigned R,
   const int rt_p = (int)(R / kRows), rt_s = rs / kRows;
   float top = -INFINITY;
   for (int pass = 0; pass < 2; ++pass) {
-    auto unit = [&](int2 span, long long u, const float* o, const float2* ml, const float* far,
-                    int stored, int r) {
+    auto unit = [&](bool prefix, int2 span, long long u, const float* o, const float2* ml,
+                    const float* far, int stored, int r) {
       span.y = min(span.y, kCtas - 1);
       for (int c = max(span.x, 0); c <= span.y; ++c) {
+        if (!in_workspace(p, prefix, u, c, r)) break;
         const long long at = (u + c) * stored + r;
         const float2 v = ml[at];
         if (v.x == -INFINITY) continue;
@@ -975,10 +996,10 @@ __device__ __noinline__ void join_far(const Params& p, int b, int h, unsigned R,
     }
     for (int blk = 0; p.prefix_tiles > 0 && blk < p.blocks; ++blk) {
       const long long u = ((long long)h * p.blocks + blk) * p.row_tiles_p + rt_p;
-      unit(p.span_p[u], u, p.o_p, p.ml_p, p.far_p, p.rows_p, R % kRows);
+      unit(true, p.span_p[u], u, p.o_p, p.ml_p, p.far_p, p.rows_p, R % kRows);
     }
     const long long u = ((long long)b * p.row_tiles_s + rt_s) * p.a.cache.H + h;
-    if (own) unit(p.span_s[u], u, p.o_s, p.ml_s, p.far_s, p.rows_s, rs % kRows);
+    if (own) unit(false, p.span_s[u], u, p.o_s, p.ml_s, p.far_s, p.rows_s, rs % kRows);
   }
   *m = top * p.coef;
 }
@@ -1011,9 +1032,10 @@ __global__ void __launch_bounds__(256, kF8 ? 0 : kAhead == 4 ? 2 : 3)
   pdl_wait();
   float acc[4 * kVec] = {}, m = -INFINITY, l = 0.0f;
   // the parts span.x + skip, + step, ... of a unit
-  auto join = [&](int2 span, long long unit, const float* o, const float2* ml, int stored, int r,
-                  int skip, int step) {
+  auto join = [&](bool prefix, int2 span, long long unit, const float* o, const float2* ml,
+                  int stored, int r, int skip, int step) {
     span.y = min(span.y, kCtas - 1);                  // (whatever a spoilt workspace says)
+    if (!in_workspace(p, prefix, unit, 0, r)) return;
     for (int c = max(span.x, 0) + skip; c <= span.y; c += kAhead * step) {
       float2 v[kAhead];
       float4 x[kAhead][kVec];
@@ -1051,17 +1073,19 @@ __global__ void __launch_bounds__(256, kF8 ? 0 : kAhead == 4 ? 2 : 3)
     }
   };
   if (raw >= 0) {
-    const int2 span_s = own ? p.span_s[unit_s] : make_int2(0, -1);
+    const int2 span_s =
+        own && in_workspace(p, false, unit_s, 0, 0) ? p.span_s[unit_s] : make_int2(0, -1);
     if (p.prefix_tiles > 0) {
       // a warp takes whole blocks, or parts of each
       const bool whole = p.blocks >= kGroups;
       for (int blk = whole ? group : 0; blk < p.blocks; blk += whole ? kGroups : 1) {
         const long long unit = ((long long)h * p.blocks + blk) * p.row_tiles_p + rt_p;
-        join(p.span_p[unit], unit, p.o_p, p.ml_p, p.rows_p, R % kRows,
+        if (!in_workspace(p, true, unit, 0, 0)) break;
+        join(true, p.span_p[unit], unit, p.o_p, p.ml_p, p.rows_p, R % kRows,
              whole ? 0 : (group + blk) % kGroups, whole ? 1 : kGroups);
       }
     }
-    join(span_s, unit_s, p.o_s, p.ml_s, p.rows_s, rs % kRows, (group + kGroups / 2) % kGroups,
+    join(false, span_s, unit_s, p.o_s, p.ml_s, p.rows_s, rs % kRows, (group + kGroups / 2) % kGroups,
          kGroups);
   }
   const long long row = (long long)token * p.a.Hq + h * p.G + gh;
@@ -1070,6 +1094,9 @@ __global__ void __launch_bounds__(256, kF8 ? 0 : kAhead == 4 ? 2 : 3)
   // (twice kFar: what lies below kFar then weighs nothing)
   auto far = [&]() { return !kF8 && fabsf(m) > 2.0f * kFar && m != -INFINITY; };
   auto store = [&](int vec, const float* y) {
+    if (!in_bounds(&g_err_attn, row < (long long)p.a.B * p.a.T * p.a.Hq &&
+                                    (int)blockIdx.z * 64 + 4 * vec + 4 <= D))
+      return;
     // l is NaN where a score is, 0 where no key is seen
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     if constexpr (sizeof(Tout) == 2)
