@@ -852,17 +852,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float score = top;
           if constexpr (!kF8) top *= rc;
           // the reference: the first maximum; later only when it is passed by more than kSlack
-          bool raise = top - kLift > m + kSlack;
+          bool raise = kF8 ? top - m > kLift + kSlack : top > m + kSlack;
           if (!kF8 && any_far && fabsf(m) > kNear)
             raise = scaled_difference(score, from, rc) > kSlack;
+          auto lifted = [&]() {                       // (a large maximum less kLift would round)
+            return !kF8 ? top : fabsf(top) > kNear ? top : top - kLift;
+          };
           if (j == it.j0) {
-            m = top - kLift;
+            m = lifted();
             if constexpr (!kF8) {
               from = score;
               any_far = __any_sync(0xffffffffu, fabsf(m) > kNear && score != -INFINITY);
             }
           } else if (__any_sync(0xffffffffu, raise)) {
-            const float mn = raise ? top - kLift : m;
+            const float mn = raise ? lifted() : m;
             float f = raise ? ex2_approx(m - mn) : 1.0f;
             m = mn;
             if constexpr (!kF8) {

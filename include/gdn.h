@@ -474,13 +474,15 @@ gdn_status gdn_kv_cache_read(const gdn_kv_cache* cache, int32_t n, const int32_t
  * A page entry outside the cache is recorded as GDN_ERR_DEVICE_INDEX (its tokens read as zero
  * codes).  Cache entries at and past a sequence's length may hold anything, NaN included.
  * The lengths stay on the device, so a captured graph can be replayed as they grow.
- * Accuracy: exact products of bf16 (or e4m3) operands, fp32 sums, scores and softmax statistics
- * (whatever the scores' size; past fp32's range they are infinite).  With an e4m3 cache a query
- * enters as the sum of two e4m3 numbers, exact but for elements below 2^-10 of its row's largest,
- * which are held to 2^-17 of that.
- * The probabilities enter the second product with 16 significant bits (bf16 cache: two bf16
- * terms) or 11 (e4m3 cache: three e5m2 terms, and no finer than 2^-25 of the row's largest, each
- * weighted with its value's scale).  bf16 values above 2^64 may overflow the sums.
+ * Accuracy: exact products of bf16 (or e4m3) operands, fp32 sums, scores and softmax statistics;
+ * scores past fp32's range are infinite.  The probabilities enter the second product with 16
+ * significant bits (bf16 cache: two bf16 terms) or 11 (e4m3 cache: three e5m2 terms, and no finer
+ * than 2^-25 of the row's largest, each weighted with its value's scale; 2^-17 where the scores
+ * pass 2^21).  With an e4m3 cache a query enters as the sum of two e4m3 numbers, exact but for
+ * elements below 2^-10 of its row's largest, which are held to 2^-17 of that, and a score is rounded
+ * together with its value's exponent, to 2^-24 of its size; with a bf16 cache the differences
+ * of a row's scores are taken as they are, whatever their size.  bf16 values above 2^64 may
+ * overflow the sums.
  * A NaN in a query makes its row NaN, one in a key the rows that see it (at a scale of zero too).
  * An infinity in a query does the same with an e4m3 cache, and in any query at a scale of zero;
  * else it counts, as one in a key of a bf16 cache does, by the scores that it makes: +inf or NaN
