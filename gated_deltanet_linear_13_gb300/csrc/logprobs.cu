@@ -673,9 +673,11 @@ cudaError_t launch(const GdnLogprobArgs& a, const Pieces& p, cudaStream_t stream
   gdn_token_logprobs_kernel<T, kTop, kEntropy><<<grid, kThreads, 0, stream>>>(a, p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // Few rows: a CTA's warps share one (20 of 32000 logits, with eight warps a row and with one:
-  // 300 rows 14.5 / 24.8 us, 1000 rows 30.1 / 34.4, 1400 rows 41.3 / 39.6).
-  if (a.N <= 152 * 8)
+  // Few rows: a CTA's warps share one.  With eight warps a row and with one, rows of 32000 bf16
+  // logits: 20 alternatives, 300 rows 14.9 / 25.3 us, 1200 33.2 / 36.8, 1400 40.6 / 39.4; one, 300 rows
+  // 13.7 / 15.8, 800 25.0 / 22.4 (fp32 31.8 / 32.3).  Without alternatives a row's few pieces are
+  // all there is to join: 64 rows 6.1 / 6.3, 300 10.2 / 9.6, 1200 20.7 / 19.7; 8 rows of 248320 6.4 / 10.7.
+  if (a.N <= (kTop ? 152 * 8 : 152))
     return launch_pdl(true, gdn_token_logprobs_join_kernel<T, kTop, kWarps>, dim3((unsigned)a.N),
                       dim3(kThreads), 0, stream, a, p);
   return launch_pdl(true, gdn_token_logprobs_join_kernel<T, kTop, 1>,
