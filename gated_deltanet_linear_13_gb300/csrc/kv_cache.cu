@@ -12,7 +12,7 @@
 // Both kernels move eight elements a lane, d / 8 lanes a vector, four tokens of a lane on the way
 // at a time (one: 29.4 and 51.9 us below), and are bound by memory: 16384 bf16 tokens of 4 x 256
 // into an 8-bit cache 19.4 us (5.2 TB/s read and written), 40001 tokens of 8 x 128 out of one
-// 42.7 us (5.8 TB/s); a few tokens cost one launch, 2.4 us.
+// 42.7 us (5.8 TB/s); a few tokens cost one launch, 2.2 us.
 #include <cuda_fp8.h>
 
 #include "common.cuh"

@@ -27,8 +27,8 @@
 // Bound by memory: each logit is read once.  At the copy rate an SM gets 12 bf16 logits a cycle,
 // for which it can issue 128 lane operations; a logit takes about nine (packed fp32 pairs where
 // there are such instructions) and one of 16 exponentials a cycle.  Measured: 1000 rows of 151669
-// in fp32 100 us (6.1 TB/s); 64 rows of 248320 in bf16 with 20 alternatives 17.7 us, of which the
-// pass takes 11 and the join 6; one row 9.1 us, two launches.
+// in fp32 101 us (6.0 TB/s); 64 rows of 248320 in bf16 with 20 alternatives 16.9 us, of which the
+// pass takes 11 and the join 6; one row 8.8 us, two launches.
 #include <float.h>
 
 #include "common.cuh"

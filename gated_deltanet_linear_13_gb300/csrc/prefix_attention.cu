@@ -24,17 +24,22 @@
 // e4m3 numbers (4 + 4 significant bits; only elements below 2^-10 of the row's largest lose
 // bits), so S is two 8-bit products at twice the bf16 rate.  P takes three e5m2 terms (3 bits
 // each and the terms' signs: 11 bits; e5m2 for its range: the smallest probabilities matter when
-// a few keys outweigh thousands).  The keys' scales multiply the scores; the values' scales 2^e_j go into the
-// exponent, P'_j = 2^(t_j + e_j - m) with m bounding t_j + e_j, and come out of the row sum
-// again, l = sum_j P'_j 2^(-e_j).
+// a few keys outweigh thousands).  The keys' scales multiply the scores; the values' scales 2^e_j
+// go into the exponent, P'_j = 2^(t_j + e_j - m) with m bounding t_j + e_j, and come out of the row
+// sum again, l = sum_j P'_j 2^(-e_j).
+//
+// Large scores.  t - m in one rounding, s c - m, holds as long as m = fl(max c) rounds by little
+// (kNear, common.cuh).  With a bf16 cache a row beyond that takes (s - max) c, and its parts are
+// joined by the scores that their references are of.  With an 8-bit cache t + e_j is rounded as a
+// score of its own, and a large maximum is its own reference.
 //
 // Bound: many keys a row tile by the products (D = 256: 2.25 us a tile of 128 keys in bf16, 1.6 in
 // 8 bits: over the three and the five products 87% of the bf16 rate of a library matrix product
 // and about twice that rate; D = 128: 1.2 us, the chain score, softmax, product); many short
 // sequences by memory (128 sequences of up to 2048 tokens of their own on 4096: 104 us, 5.0 TB/s);
 // a few keys by latency (one request on 512 + 37 keys: 12 us with the merge).  Measured in whole:
-// 32 sequences on 16384, 8-bit, 42 us; 16 x 4 tokens on 32771, bf16, 72; 666 tokens on 20000,
-// D = 128, 126.
+// 32 sequences on 16384, 8-bit, 43 us; 16 x 4 tokens on 32771, bf16, 73; 666 tokens on 20000,
+// D = 128, 127.
 #include <float.h>
 
 #include <cuda_fp16.h>
