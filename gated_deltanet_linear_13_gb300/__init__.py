@@ -22,6 +22,8 @@ HEAD_DIM = 128
 GDN_OK = 0
 GDN_F32, GDN_BF16 = 0, 1
 GDN_KV_BF16, GDN_KV_E4M3 = 0, 1
+GDN_ROPE_HALF, GDN_ROPE_INTERLEAVED = 0, 1
+ROPE_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}   # gdn_rope_scaling in include/gdn.h
 STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARGUMENT", 2: "GDN_ERR_UNSUPPORTED",
                 3: "GDN_ERR_WORKSPACE", 4: "GDN_ERR_CUDA", 5: "GDN_ERR_DEVICE_TIMEOUT",
                 6: "GDN_ERR_DEVICE_INDEX"}
@@ -33,7 +35,9 @@ EXPORTED = ("gdn_prefill_workspace_size", "gdn_chunk_prefill", "gdn_decode_step"
             "gdn_get_device_error", "gdn_status_string", "gdn_version",
             "gdn_selftest_device_timeout", "gdn_chunk_prefill_ex",
             "gdn_kv_cache_append", "gdn_kv_cache_read", "gdn_prefix_attention_workspace_size",
-            "gdn_prefix_attention", "gdn_token_logprobs_workspace_size", "gdn_token_logprobs")
+            "gdn_prefix_attention", "gdn_token_logprobs_workspace_size", "gdn_token_logprobs",
+            "gdn_qk_norm_rope", "gdn_rope_phase_steps", "gdn_page_plan", "gdn_page_release",
+            "gdn_verify_tokens_workspace_size", "gdn_verify_tokens")
 NOALLOC_SCRATCH_BYTES = 64 << 20   # GDN_NOALLOC_SCRATCH_BYTES in include/gdn.h
 
 
@@ -73,6 +77,18 @@ class GdnKvCache(ctypes.Structure):
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("format", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p)]
+
+
+class GdnRope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int),
+                ("amplitude", ctypes.c_float), ("phase_steps", ctypes.c_void_p)]
+
+
+class GdnPagePool(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_rows", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("table", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p)]
 
 
 _vp = ctypes.c_void_p
@@ -137,6 +153,24 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.gdn_token_logprobs.restype = ctypes.c_int
     L.gdn_token_logprobs.argtypes = ([i32, i32, ctypes.c_int, _vp, i64, _vp, ctypes.c_float, _vp,
                                       _vp, i32] + [_vp] * 3 + [sz, _vp])
+    f32, f64 = ctypes.c_float, ctypes.c_double
+    L.gdn_qk_norm_rope.restype = ctypes.c_int
+    L.gdn_qk_norm_rope.argtypes = ([i32] * 4 + [ctypes.c_int, _vp, i64, i64, _vp, i64, _vp, _vp,
+                                    f32, _vp, ctypes.POINTER(GdnRope), _vp, i64, _vp, cp, _vp,
+                                    i64, _vp, _vp])
+    L.gdn_rope_phase_steps.restype = ctypes.c_int
+    L.gdn_rope_phase_steps.argtypes = ([i32, f64, ctypes.c_int] + [f64] * 4 +
+                                       [ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(f32)])
+    pp = ctypes.POINTER(GdnPagePool)
+    L.gdn_page_plan.restype = ctypes.c_int
+    L.gdn_page_plan.argtypes = [pp, i32, _vp, _vp, _vp, i32, i32] + [_vp] * 6
+    L.gdn_page_release.restype = ctypes.c_int
+    L.gdn_page_release.argtypes = [pp, i32, _vp, _vp, _vp]
+    L.gdn_verify_tokens_workspace_size.restype = sz
+    L.gdn_verify_tokens_workspace_size.argtypes = [i32, i32, i32, ctypes.c_int, i32]
+    L.gdn_verify_tokens.restype = ctypes.c_int
+    L.gdn_verify_tokens.argtypes = ([i32] * 3 + [ctypes.c_int, _vp, i64, _vp, _vp, i64] +
+                                    [_vp] * 7 + [sz, _vp])
     L.gdn_get_device_error.restype = ctypes.c_int
     L.gdn_get_device_error.argtypes = [_vp]
     L.gdn_selftest_device_timeout.restype = ctypes.c_int
@@ -867,6 +901,251 @@ def gdn_token_logprobs(logits, targets, logprobs, entropy=None, *, top_ids=None,
                               _ptr(top_ids), _ptr(top_logprobs), _ptr(workspace), ws_bytes,
                               _stream_of(stream, dev))
     _check(st, "gdn_token_logprobs")
+
+
+def gdn_rope_phase_steps(rotary_dim: int, base: float = 10000.0, *,
+                         scaling: Optional[str] = None, factor: float = 1.0,
+                         original_context: float = 0.0, beta_fast: float = 32.0,
+                         beta_slow: float = 1.0, device="cuda"):
+    """(phase steps, amplitude) of a rotation for gdn_qk_norm_rope: int64 [rotary_dim / 2] on
+    ``device`` (the bits of the 64-bit steps) and a float.  ``scaling``: None, "linear", "ntk" or
+    "yarn" (see gdn_rope_phase_steps in include/gdn.h)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling: {scaling!r}, expected one of {list(ROPE_SCALINGS)}")
+    steps = (ctypes.c_uint64 * max(1, rotary_dim // 2))()
+    amplitude = ctypes.c_float()
+    st = load_library().gdn_rope_phase_steps(rotary_dim, base, ROPE_SCALINGS[scaling], factor,
+                                             original_context, beta_fast, beta_slow, steps,
+                                             ctypes.byref(amplitude))
+    _check(st, "gdn_rope_phase_steps")
+    signed = [x - (1 << 64) if x >> 63 else x for x in steps][:rotary_dim // 2]
+    return torch.tensor(signed, dtype=torch.int64, device=device), amplitude.value
+
+
+def _head_strides(t: torch.Tensor, name: str, shape, dtype, device):
+    """The token and head strides (elements) of t [n, H, D] with dense vectors."""
+    n, H, D = shape
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    token, head, element = t.stride()
+    if element != 1 and D > 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    if H == 1:
+        head = D
+    return token if n > 1 else (H - 1) * head + D, head
+
+
+def gdn_qk_norm_rope(q, k, positions, phase_steps, q_out, k_out=None, *, q_weight=None,
+                     k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                     amplitude: float = 1.0, v=None, k_cache=None, v_cache=None, slots=None,
+                     k_exp=None, v_exp=None, stream=None) -> None:
+    """RMS norm of query and key heads q [n, Hq, D], k [n, H, D] (bf16 or fp32; q's heads may lie
+    apart, tokens too), rotated by their ``positions`` [n] (int32; see gdn_qk_norm_rope in
+    include/gdn.h) into q_out [n, Hq, D] and k_out [n, H, D].  ``phase_steps`` int64
+    [rotary_dim / 2] and ``amplitude`` come from gdn_rope_phase_steps; None turns nothing.  With a
+    cache (as in gdn_kv_cache_append) the keys and the values v [n, H, D] go to ``slots`` [n], and
+    k_out may be None."""
+    L = load_library()
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must have 3 dimensions: tokens, heads, elements")
+    dtype = q.dtype
+    dt = _dt(q)
+    n, Hq, D = q.shape
+    H = k.shape[1]
+    qs, qh = _head_strides(q, "q", (n, Hq, D), dtype, dev)
+    ks = _token_stride(k, "k", (n, H, D), dtype, dev)
+    qo = _token_stride(q_out, "q_out", (n, Hq, D), dtype, dev)
+    r = 0
+    if phase_steps is not None:
+        r = 2 * phase_steps.numel()
+        _need(phase_steps, "phase_steps", (r // 2,), torch.int64, dev)
+        _need(positions, "positions", (n,), torch.int32, dev)
+    if q_weight is not None:
+        _need(q_weight, "q_weight", (D,), torch.float32, dev)
+    if k_weight is not None:
+        _need(k_weight, "k_weight", (D,), torch.float32, dev)
+    if k_out is not None:
+        _need(k_out, "k_out", (n, H, D), dtype, dev)
+    cache, vp, vs, sp = None, None, 0, None
+    if k_cache is not None:
+        c, cdev = _kv_cache(k_cache, v_cache, k_exp, v_exp)
+        if cdev != dev:
+            raise ValueError(f"k_cache: on {cdev}, expected {dev}")
+        if v is None:
+            raise ValueError("v is required")
+        vs = _token_stride(v, "v", (n, H, D), dtype, dev)
+        _need(slots, "slots", (n,), torch.int32, dev)
+        cache, vp, sp = ctypes.byref(c), v.data_ptr(), slots.data_ptr()
+    elif k_out is None:
+        raise ValueError("k_out or a cache is required")
+    elif v is not None or slots is not None or v_cache is not None:
+        raise ValueError("v, v_cache and slots go with k_cache")
+    rope = GdnRope(r, GDN_ROPE_INTERLEAVED if interleaved else GDN_ROPE_HALF, amplitude,
+                   phase_steps.data_ptr() if r else None)
+    st = L.gdn_qk_norm_rope(n, Hq, H, D, dt, q.data_ptr(), qs, qh, k.data_ptr(), ks,
+                            _ptr(q_weight), _ptr(k_weight), eps,
+                            positions.data_ptr() if r else None, ctypes.byref(rope),
+                            q_out.data_ptr(), qo, _ptr(k_out), cache, vp, vs, sp,
+                            _stream_of(stream, dev))
+    _check(st, "gdn_qk_norm_rope")
+
+
+def _page_pool(table, held, free_pages, free_count, page_size):
+    """(C struct, device) of a pool: table [num_rows, max_pages], held [num_rows], free_pages
+    [num_pages], free_count [1], all int32."""
+    dev = table.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    if table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("table must have 2 dimensions and free_pages 1")
+    i32 = torch.int32
+    rows, columns = table.shape
+    pages = free_pages.shape[0]
+    _need(table, "table", (rows, columns), i32, dev)
+    _need(held, "held", (rows,), i32, dev)
+    _need(free_pages, "free_pages", (pages,), i32, dev)
+    _need(free_count, "free_count", (1,), i32, dev)
+    return GdnPagePool(pages, page_size, rows, columns, table.data_ptr(), held.data_ptr(),
+                       free_pages.data_ptr(), free_count.data_ptr()), dev
+
+
+def gdn_page_plan(kv_len, new_len, slots=None, positions=None, cu_seqlens=None, kv_len_out=None,
+                  pages=None, *, table, held, free_pages, free_count, page_size: int, rows=None,
+                  position_offset: int = 0, stream=None) -> None:
+    """Pages, ``slots`` and ``positions`` [capacity] for new_len [B] more tokens of each of B
+    requests that have kv_len [B] (see gdn_page_plan in include/gdn.h).  The pool (table
+    [num_rows, max_pages], held [num_rows], free_pages [num_pages], free_count [1]; int32) is
+    updated in place; cu_seqlens [B + 1], kv_len_out [B] and the block tables ``pages``
+    [B, max_pages] are written where given.  Request b is row rows[b] (or b) of the pool."""
+    L = load_library()
+    p, dev = _page_pool(table, held, free_pages, free_count, page_size)
+    i32 = torch.int32
+    B = kv_len.shape[0]
+    if rows is None and B > p.num_rows:
+        raise ValueError("the pool has fewer rows than the batch and no rows given")
+    _need(kv_len, "kv_len", (B,), i32, dev)
+    _need(new_len, "new_len", (B,), i32, dev)
+    capacity = 0
+    if slots is not None:
+        capacity = slots.shape[0]
+        _need(slots, "slots", (capacity,), i32, dev)
+    if positions is not None:
+        capacity = capacity if slots is not None else positions.shape[0]
+        _need(positions, "positions", (capacity,), i32, dev)
+    if slots is None and positions is None:          # nothing to be written a token
+        capacity = 0x7fffffff
+    if rows is not None:
+        _need(rows, "rows", (B,), i32, dev)
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", (B + 1,), i32, dev)
+    if kv_len_out is not None:
+        _need(kv_len_out, "kv_len_out", (B,), i32, dev)
+    if pages is not None:
+        _need(pages, "pages", (B, p.max_pages), i32, dev)
+    st = L.gdn_page_plan(ctypes.byref(p), B, _ptr(rows), kv_len.data_ptr(), new_len.data_ptr(),
+                         capacity, position_offset, _ptr(slots), _ptr(positions),
+                         _ptr(cu_seqlens), _ptr(kv_len_out), _ptr(pages), _stream_of(stream, dev))
+    _check(st, "gdn_page_plan")
+
+
+def gdn_page_release(keep_len, *, table, held, free_pages, free_count, page_size: int, rows=None,
+                     stream=None) -> None:
+    """Requests keep the pages of their first keep_len [B] tokens and give the others back (see
+    gdn_page_release in include/gdn.h); the pool as in gdn_page_plan."""
+    L = load_library()
+    p, dev = _page_pool(table, held, free_pages, free_count, page_size)
+    B = keep_len.shape[0]
+    if rows is None and B > p.num_rows:
+        raise ValueError("the pool has fewer rows than the batch and no rows given")
+    _need(keep_len, "keep_len", (B,), torch.int32, dev)
+    if rows is not None:
+        _need(rows, "rows", (B,), torch.int32, dev)
+    st = L.gdn_page_release(ctypes.byref(p), B, _ptr(rows), keep_len.data_ptr(),
+                            _stream_of(stream, dev))
+    _check(st, "gdn_page_release")
+
+
+def gdn_verify_tokens_workspace_size(batch: int, num_drafts: int, vocab: int,
+                                     dtype=torch.bfloat16, draft_logits: bool = True) -> int:
+    dt = GDN_BF16 if dtype == torch.bfloat16 else GDN_F32
+    return int(load_library().gdn_verify_tokens_workspace_size(batch, num_drafts, vocab, dt,
+                                                               int(draft_logits)))
+
+
+def _row_stride(t: torch.Tensor, name: str, shape, dtype, device) -> int:
+    """The row stride (elements) of t [B, T, V]: rows dense, one after the other."""
+    if t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return shape[2]
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    B, T, V = shape
+    outer, row, element = t.stride()
+    if V > 1 and element != 1:
+        raise ValueError(f"{name}: rows must be dense")
+    if T == 1:
+        return outer if B > 1 else V
+    if B > 1 and outer != T * row:
+        raise ValueError(f"{name}: rows must lie at one stride")
+    return row
+
+
+def gdn_verify_tokens(target_logits, tokens, accepted, *, clocks, draft_ids=None,
+                      draft_logits=None, accept_u=None, scale=None, logprobs=None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Verify T drafted tokens ``draft_ids`` [B, T] (int32; negative ones end a row) of each of B
+    sequences under target_logits [B, T + 1, V] (bf16 or fp32) and draft_logits [B, T, V] (or
+    None: the drafts have no distribution), from uniform ``accept_u`` [B, T] and exponential
+    ``clocks`` [B, V] numbers; ``scale`` [B] fp32 inverse temperatures (inf: greedy; negative: left
+    out) or None.  Writes tokens [B, T + 1] (int32: the accepted drafts, the token behind them,
+    then -1), accepted [B] (int32) and logprobs [B, T + 1] (fp32) or None.  T = 0 draws one token
+    a sequence.  See gdn_verify_tokens in include/gdn.h."""
+    L = load_library()
+    if target_logits.dim() != 3:
+        raise ValueError(f"target_logits: shape {tuple(target_logits.shape)}, expected (B, T + 1, V)")
+    dev = target_logits.device
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    B, T1, V = target_logits.shape
+    T = T1 - 1
+    dtype, f32 = target_logits.dtype, torch.float32
+    dt = _dt(target_logits)
+    ts = _row_stride(target_logits, "target_logits", (B, T1, V), dtype, dev)
+    ds = 0
+    if T > 0:
+        _need(draft_ids, "draft_ids", (B, T), torch.int32, dev)
+        _need(accept_u, "accept_u", (B, T), f32, dev)
+        if draft_logits is not None:
+            ds = _row_stride(draft_logits, "draft_logits", (B, T, V), dtype, dev)
+    elif draft_ids is not None or draft_logits is not None or accept_u is not None:
+        raise ValueError("one row a sequence has no drafts: draft_ids, draft_logits and accept_u "
+                         "must be None")
+    _need(clocks, "clocks", (B, V), f32, dev)
+    if scale is not None:
+        _need(scale, "scale", (B,), f32, dev)
+    _need(tokens, "tokens", (B, T1), torch.int32, dev)
+    _need(accepted, "accepted", (B,), torch.int32, dev)
+    if logprobs is not None:
+        _need(logprobs, "logprobs", (B, T1), f32, dev)
+    if workspace is None:
+        need = int(L.gdn_verify_tokens_workspace_size(B, T, V, dt, int(draft_logits is not None)))
+        workspace = _workspace(need, dev, stream)
+    st = L.gdn_verify_tokens(B, T, V, dt, target_logits.data_ptr(), ts, _ptr(draft_ids),
+                             _ptr(draft_logits), ds, _ptr(accept_u), clocks.data_ptr(),
+                             _ptr(scale), tokens.data_ptr(), accepted.data_ptr(), _ptr(logprobs),
+                             workspace.data_ptr(), _workspace_bytes(workspace, dev),
+                             _stream_of(stream, dev))
+    _check(st, "gdn_verify_tokens")
 
 
 def gdn_get_device_error(stream=None) -> int:

@@ -328,6 +328,55 @@ struct GdnLogprobArgs {
 size_t gdn_token_logprobs_bytes(int N, int V, int bf16, int top_k);
 cudaError_t gdn_launch_token_logprobs(const GdnLogprobArgs& a, cudaStream_t stream);
 
+// The norm of n tokens' query and key heads with their rotation by position; keys and values on
+// into a cache.
+struct GdnRopeArgs {
+  int n, Hq, H, D, rotary, interleaved, to_cache;
+  const void* q; long long q_tok, q_head;               // strides in elements
+  const void* k; long long k_tok;
+  const void* v; long long v_tok;
+  const float* wq; const float* wk;                     // [D] or NULL
+  float eps, amplitude;
+  const int32_t* positions;
+  const uint64_t* steps;                                // [rotary / 2], 2^-64 turns a token
+  void* q_out; long long q_out_tok;
+  void* k_out;                                          // or NULL
+  GdnKvCacheArgs cache;
+  const int32_t* slots;
+  float inv_d;                                          // (set by the launcher)
+  int turn;
+};
+cudaError_t gdn_launch_qk_norm_rope(GdnRopeArgs a, int in_bf16, cudaStream_t stream);
+
+// The pool of pages, and a step's requests: len their tokens (or those to keep), more the new ones
+// (NULL: pages are given back).
+constexpr int kGdnMaxRequests = 8192;
+struct GdnPoolArgs {
+  int num_pages, page_shift, num_rows, max_pages;
+  int32_t* table; int32_t* held; int32_t* free_pages; int32_t* free_count;
+};
+struct GdnPlanArgs {
+  int B, capacity, offset;
+  const int32_t* rows; const int32_t* len; const int32_t* more;
+  int32_t* slots; int32_t* positions; int32_t* cu_seqlens; int32_t* len_out; int32_t* pages;
+};
+cudaError_t gdn_launch_page_plan(const GdnPoolArgs& p, const GdnPlanArgs& a, cudaStream_t stream);
+cudaError_t gdn_launch_page_release(const GdnPoolArgs& p, const GdnPlanArgs& a,
+                                    cudaStream_t stream);
+
+// Verification of T drafted tokens of B sequences, V logits a row.
+constexpr int kGdnMaxDrafts = 64;
+struct GdnVerifyArgs {
+  int B, T, V, bf16;
+  const void* target; long long target_stride;          // of a row, in elements
+  const void* draft; long long draft_stride;            // or NULL
+  const int32_t* ids; const float* accept_u; const float* clocks; const float* scale;
+  int32_t* tokens; int32_t* accepted; float* logprobs;
+  void* workspace;
+};
+size_t gdn_verify_tokens_bytes(int B, int T, int V, int bf16, int draft);
+cudaError_t gdn_launch_verify_tokens(const GdnVerifyArgs& a, cudaStream_t stream);
+
 // Per-translation-unit device error words: read and clear (host side, synchronous copy).
 unsigned gdn_take_error_decode();
 unsigned gdn_take_error_conv();
@@ -339,3 +388,6 @@ unsigned gdn_take_error_decode_multi();
 unsigned gdn_take_error_kv_cache();
 unsigned gdn_take_error_prefix_attention();
 unsigned gdn_take_error_logprobs();
+unsigned gdn_take_error_qk_norm_rope();
+unsigned gdn_take_error_pages();
+unsigned gdn_take_error_verify();

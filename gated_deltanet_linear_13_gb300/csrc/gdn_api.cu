@@ -691,6 +691,215 @@ gdn_status gdn_token_logprobs(int32_t rows, int32_t vocab, gdn_dtype dtype, cons
              : GDN_ERR_CUDA;
 }
 
+gdn_status gdn_rope_phase_steps(int32_t rotary_dim, double base, gdn_rope_scaling scaling,
+                                double factor, double original_context, double beta_fast,
+                                double beta_slow, uint64_t* steps, float* amplitude) {
+  const double kTurn = 6.283185307179586476925286766559;
+  if (rotary_dim < 0 || rotary_dim % 2 || !isfinite(base) || !(base > 1.0) || !amplitude ||
+      (rotary_dim > 0 && !steps))
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (scaling != GDN_ROPE_UNSCALED && scaling != GDN_ROPE_LINEAR && scaling != GDN_ROPE_NTK &&
+      scaling != GDN_ROPE_YARN)
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (scaling != GDN_ROPE_UNSCALED && (!isfinite(factor) || !(factor >= 1.0)))
+    return GDN_ERR_INVALID_ARGUMENT;
+  const bool yarn = scaling == GDN_ROPE_YARN;
+  if (yarn && (!isfinite(original_context) || !(original_context > 0.0) || !isfinite(beta_fast) ||
+               !(beta_slow > 0.0) || !(beta_fast > beta_slow)))
+    return GDN_ERR_INVALID_ARGUMENT;
+  *amplitude = yarn ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
+  if (rotary_dim == 0) return GDN_OK;
+  const double r = rotary_dim;
+  if (scaling == GDN_ROPE_NTK && rotary_dim > 2) base *= pow(factor, r / (r - 2.0));
+  if (!isfinite(base)) return GDN_ERR_INVALID_ARGUMENT;
+  double lo = 0.0, span = 1.0;
+  if (yarn) {
+    // the pair that makes `turns` turns over the trained context
+    auto pair_of = [&](double turns) {
+      return r * log(original_context / (turns * kTurn)) / (2.0 * log(base));
+    };
+    lo = fmax(0.0, floor(pair_of(beta_fast)));
+    span = fmax(fmin(r - 1.0, ceil(pair_of(beta_slow))) - lo, 1e-3);
+  }
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double f = pow(base, -2.0 * i / r);
+    if (scaling == GDN_ROPE_LINEAR) f /= factor;
+    if (yarn) {
+      const double w = fmin(1.0, fmax(0.0, (i - lo) / span));
+      f = f / factor * w + f * (1.0 - w);
+    }
+    steps[i] = (uint64_t)nearbyint(f / kTurn * 18446744073709551616.0);   // below 2^64: f <= 1
+  }
+  return GDN_OK;
+}
+
+gdn_status gdn_qk_norm_rope(int32_t n, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                            gdn_dtype dtype, const void* q, int64_t q_token_stride,
+                            int64_t q_head_stride, const void* k, int64_t k_token_stride,
+                            const float* q_weight, const float* k_weight, float eps,
+                            const int32_t* positions, const gdn_rope* rope, void* q_out,
+                            int64_t q_out_token_stride, void* k_out, const gdn_kv_cache* cache,
+                            const void* v, int64_t v_token_stride, const int32_t* slots,
+                            void* stream) {
+  GdnRopeArgs a = {};
+  if (cache) {
+    const gdn_status st = check_kv_cache(cache, &a.cache);
+    if (st != GDN_OK) return st;
+    if (a.cache.H != num_kv_heads || a.cache.D != head_dim) return GDN_ERR_INVALID_ARGUMENT;
+  }
+  if (n < 0 || num_heads < 1 || num_kv_heads < 1 || head_dim < 1 || !is_dtype(dtype) || !rope ||
+      !isfinite(eps) || eps < 0.0f)
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (head_dim % 8 || head_dim > 256 || (long long)num_heads + 2ll * num_kv_heads > 65535)
+    return GDN_ERR_UNSUPPORTED;
+  const int r = rope->rotary_dim;
+  if (r < 0 || r > head_dim || r % 2 || !isfinite(rope->amplitude) ||
+      (rope->layout != GDN_ROPE_HALF && rope->layout != GDN_ROPE_INTERLEAVED))
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (n == 0) return GDN_OK;
+  if (r > 0 && (!rope->phase_steps || (reinterpret_cast<uintptr_t>(rope->phase_steps) & 7u) ||
+                !positions || !aligned4(positions)))
+    return GDN_ERR_INVALID_ARGUMENT;
+  const int64_t D = head_dim, per16 = 16 / (int64_t)elem_bytes(dtype);
+  if (!q || !aligned16(q) || !k || !aligned16(k) || !q_out || !aligned16(q_out) ||
+      !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(k_out))
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (q_head_stride < D || q_head_stride % per16 || q_token_stride % per16 ||
+      q_token_stride < (num_heads - 1) * q_head_stride + D || k_token_stride % per16 ||
+      k_token_stride < num_kv_heads * D || q_out_token_stride % per16 ||
+      q_out_token_stride < num_heads * D)
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (cache) {
+    if (!v || !aligned16(v) || v_token_stride % per16 || v_token_stride < num_kv_heads * D ||
+        !slots || !aligned4(slots))
+      return GDN_ERR_INVALID_ARGUMENT;
+  } else if (!k_out) {
+    return GDN_ERR_INVALID_ARGUMENT;
+  }
+  a.n = n; a.Hq = num_heads; a.H = num_kv_heads; a.D = head_dim; a.rotary = r;
+  a.interleaved = rope->layout == GDN_ROPE_INTERLEAVED; a.to_cache = cache != nullptr;
+  a.q = q; a.q_tok = q_token_stride; a.q_head = q_head_stride;
+  a.k = k; a.k_tok = k_token_stride; a.v = v; a.v_tok = v_token_stride;
+  a.wq = q_weight; a.wk = k_weight; a.eps = eps; a.amplitude = rope->amplitude;
+  a.positions = positions; a.steps = rope->phase_steps;
+  a.q_out = q_out; a.q_out_tok = q_out_token_stride; a.k_out = k_out; a.slots = slots;
+  return gdn_launch_qk_norm_rope(a, dtype == GDN_BF16, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? GDN_OK
+             : GDN_ERR_CUDA;
+}
+
+static gdn_status check_pool(const gdn_page_pool* p, int32_t batch, GdnPoolArgs* out) {
+  if (!p || batch < 0 || p->num_pages < 0 || p->num_rows < 0 || p->max_pages < 0)
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128)
+    return p->page_size < 1 ? GDN_ERR_INVALID_ARGUMENT : GDN_ERR_UNSUPPORTED;
+  if ((long long)p->num_pages * p->page_size > 0x7fffffffLL ||
+      (long long)p->max_pages * p->page_size > 0x7fffffffLL || batch > kGdnMaxRequests)
+    return GDN_ERR_UNSUPPORTED;
+  if (!p->free_count || !aligned4(p->free_count) || !aligned4(p->table) || !aligned4(p->held) ||
+      !aligned4(p->free_pages) || (p->num_pages > 0 && !p->free_pages) ||
+      (p->num_rows > 0 && (!p->held || (p->max_pages > 0 && !p->table))))
+    return GDN_ERR_INVALID_ARGUMENT;
+  out->num_pages = p->num_pages;
+  out->page_shift = __builtin_ctz((unsigned)p->page_size);
+  out->num_rows = p->num_rows;
+  out->max_pages = p->max_pages;
+  out->table = p->table; out->held = p->held;
+  out->free_pages = p->free_pages; out->free_count = p->free_count;
+  return GDN_OK;
+}
+
+gdn_status gdn_page_plan(const gdn_page_pool* pool, int32_t batch, const int32_t* rows,
+                         const int32_t* kv_len, const int32_t* new_len, int32_t capacity,
+                         int32_t position_offset, int32_t* slots, int32_t* positions,
+                         int32_t* cu_seqlens, int32_t* kv_len_out, int32_t* pages, void* stream) {
+  GdnPoolArgs p = {};
+  const gdn_status st = check_pool(pool, batch, &p);
+  if (st != GDN_OK) return st;
+  if (capacity < 0 || position_offset < 0) return GDN_ERR_INVALID_ARGUMENT;
+  if ((long long)pool->max_pages * pool->page_size + position_offset > 0x7fffffffLL)
+    return GDN_ERR_UNSUPPORTED;
+  if (batch > 0 && (!kv_len || !new_len)) return GDN_ERR_INVALID_ARGUMENT;
+  if (!aligned4(rows) || !aligned4(kv_len) || !aligned4(new_len) || !aligned4(slots) ||
+      !aligned4(positions) || !aligned4(cu_seqlens) || !aligned4(kv_len_out) || !aligned4(pages))
+    return GDN_ERR_INVALID_ARGUMENT;
+  GdnPlanArgs a = {};
+  a.B = batch; a.capacity = capacity; a.offset = position_offset;
+  a.rows = rows; a.len = kv_len; a.more = new_len;
+  a.slots = slots; a.positions = positions; a.cu_seqlens = cu_seqlens; a.len_out = kv_len_out;
+  a.pages = pages;
+  return gdn_launch_page_plan(p, a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? GDN_OK
+             : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_page_release(const gdn_page_pool* pool, int32_t batch, const int32_t* rows,
+                            const int32_t* keep_len, void* stream) {
+  GdnPoolArgs p = {};
+  const gdn_status st = check_pool(pool, batch, &p);
+  if (st != GDN_OK) return st;
+  if (batch == 0) return GDN_OK;
+  if (!keep_len || !aligned4(keep_len) || !aligned4(rows)) return GDN_ERR_INVALID_ARGUMENT;
+  GdnPlanArgs a = {};
+  a.B = batch; a.rows = rows; a.len = keep_len;
+  return gdn_launch_page_release(p, a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? GDN_OK
+             : GDN_ERR_CUDA;
+}
+
+static gdn_status check_verify_dims(int32_t batch, int32_t drafts, int32_t vocab,
+                                    gdn_dtype dtype) {
+  if (batch < 0 || drafts < 0 || vocab < 1 || !is_dtype(dtype)) return GDN_ERR_INVALID_ARGUMENT;
+  // slices of sequences and granules of rows are counted in 32 and 52 bits; an index past the row
+  // by a granule stays within 32
+  if (drafts > kGdnMaxDrafts || batch > (1 << 24) || vocab > (1 << 30)) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+size_t gdn_verify_tokens_workspace_size(int32_t batch, int32_t num_drafts, int32_t vocab,
+                                        gdn_dtype dtype, int32_t with_draft_logits) {
+  if (check_verify_dims(batch, num_drafts, vocab, dtype) != GDN_OK || batch == 0) return 0;
+  return gdn_verify_tokens_bytes(batch, num_drafts, vocab, dtype == GDN_BF16,
+                                 with_draft_logits && num_drafts > 0);
+}
+
+gdn_status gdn_verify_tokens(int32_t batch, int32_t num_drafts, int32_t vocab, gdn_dtype dtype,
+                             const void* target_logits, int64_t target_row_stride,
+                             const int32_t* draft_ids, const void* draft_logits,
+                             int64_t draft_row_stride, const float* accept_u,
+                             const float* clocks, const float* scale, int32_t* tokens,
+                             int32_t* accepted, float* logprobs, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  const gdn_status st = check_verify_dims(batch, num_drafts, vocab, dtype);
+  if (st != GDN_OK) return st;
+  if (batch == 0) return GDN_OK;
+  const uintptr_t align = elem_bytes(dtype) - 1;
+  if (!target_logits || (reinterpret_cast<uintptr_t>(target_logits) & align) ||
+      target_row_stride < vocab || !clocks || !tokens || !accepted)
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (num_drafts == 0) draft_ids = nullptr, draft_logits = nullptr, accept_u = nullptr;
+  else if (!draft_ids || !accept_u) return GDN_ERR_INVALID_ARGUMENT;
+  if (draft_logits && ((reinterpret_cast<uintptr_t>(draft_logits) & align) ||
+                       draft_row_stride < vocab))
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (!aligned4(draft_ids) || !aligned4(accept_u) || !aligned4(clocks) || !aligned4(scale) ||
+      !aligned4(tokens) || !aligned4(accepted) || !aligned4(logprobs))
+    return GDN_ERR_INVALID_ARGUMENT;
+  const size_t need = gdn_verify_tokens_bytes(batch, num_drafts, vocab, dtype == GDN_BF16,
+                                              draft_logits != nullptr);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < need) return GDN_ERR_WORKSPACE;
+  GdnVerifyArgs a = {};
+  a.B = batch; a.T = num_drafts; a.V = vocab; a.bf16 = dtype == GDN_BF16;
+  a.target = target_logits; a.target_stride = target_row_stride;
+  a.draft = draft_logits; a.draft_stride = draft_row_stride;
+  a.ids = draft_ids; a.accept_u = accept_u; a.clocks = clocks; a.scale = scale;
+  a.tokens = tokens; a.accepted = accepted; a.logprobs = logprobs; a.workspace = workspace;
+  return gdn_launch_verify_tokens(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? GDN_OK
+             : GDN_ERR_CUDA;
+}
+
 gdn_status gdn_selftest_device_timeout(uint32_t max_iters, void* stream) {
   if (max_iters == 0 || max_iters > (1u << 20)) return GDN_ERR_INVALID_ARGUMENT;
   return gdn_launch_selftest_wait(max_iters, static_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -704,7 +913,8 @@ gdn_status gdn_get_device_error(void* stream) {
                   gdn_take_error_prefill_simt() | gdn_take_error_prefill_tc() |
                   gdn_take_error_varlen() | gdn_take_error_decode_multi() |
                   gdn_take_error_kv_cache() | gdn_take_error_prefix_attention() |
-                  gdn_take_error_logprobs();
+                  gdn_take_error_logprobs() | gdn_take_error_qk_norm_rope() |
+                  gdn_take_error_pages() | gdn_take_error_verify();
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   if (bits & gdn::kErrTimeout) return GDN_ERR_DEVICE_TIMEOUT;
   if (bits & gdn::kErrIndex) return GDN_ERR_DEVICE_INDEX;

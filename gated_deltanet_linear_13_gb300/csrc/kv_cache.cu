@@ -13,9 +13,8 @@
 // at a time (one: 29.4 and 51.9 us below), and are bound by memory: 16384 bf16 tokens of 4 x 256
 // into an 8-bit cache 19.4 us (5.2 TB/s read and written), 40001 tokens of 8 x 128 out of one
 // 42.7 us (5.8 TB/s); a few tokens cost one launch, 2.2 us.
-#include <cuda_fp8.h>
-
 #include "common.cuh"
+#include "kv_cache.cuh"
 
 using namespace gdn;
 
@@ -26,64 +25,6 @@ unsigned gdn_take_error_kv_cache() { return gdn::take_error(g_err_kv); }
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMinExp = -60, kMaxExp = 60;
-
-struct Vec8 {
-  float x[8];
-};
-
-__device__ __forceinline__ Vec8 load8(const __nv_bfloat16* p) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  Vec8 v;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v.x[2 * i] = __uint_as_float(w[i] << 16);
-    v.x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-  return v;
-}
-__device__ __forceinline__ Vec8 load8(const float* p) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  return Vec8{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const Vec8& v) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x[2 * i], v.x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void store8(float* p, const Vec8& v) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v.x[0], v.x[1], v.x[2], v.x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v.x[4], v.x[5], v.x[6], v.x[7]);
-}
-
-// 2^e for a whole e of [-126, 127]
-__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
-__device__ __forceinline__ int scale_exponent(float top) {
-  const uint32_t u = __float_as_uint(top);
-  const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return min(max(e, kMinExp), kMaxExp);
-}
-
-// Row of a token's slot in the cache (of H * page rows a page), or -1: skipped (negative slot) or
-// out of range (recorded).
-__device__ __forceinline__ long long row_of(const GdnKvCacheArgs& c, int slot, int head) {
-  if (slot < 0) return -1;
-  const int page = slot >> c.page_shift, off = slot & ((1 << c.page_shift) - 1);
-  if (page >= c.num_pages) {
-    atomicOr(&g_err_kv, kErrIndex);
-    return -1;
-  }
-  const long long row = (((long long)page * c.H + head) << c.page_shift) + off;
-  return in_bounds(&g_err_kv, head < c.H && row < ((long long)c.num_pages * c.H << c.page_shift))
-             ? row
-             : -1;
-}
 
 // Grid: x tokens, y = keys of head 0 .. H - 1, then values.  d / 8 lanes a vector; a thread has
 // kTokens tokens, kThreads 8 / d apart, their loads issued before any use.
@@ -110,30 +51,18 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_append_kernel(
   }
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
-    const long long row = row_of(c, slot[i], head);
+    long long row = kv_row_of(&g_err_kv, c, slot[i], head);
+    if (!in_bounds(&g_err_kv, head >= 0 && lane * 8 + 8 <= D)) row = -1;
     if constexpr (!kF8) {
       if (row >= 0) store8(static_cast<__nv_bfloat16*>(values ? c.v : c.k) + row * D + lane * 8, x[i]);
     } else {
-      float top = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float m = fabsf(x[i].x[e]);
-        top = m < INFINITY ? fmaxf(top, m) : top;      // false for NaN too
-      }
+      float top = kv_largest(x[i]);
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int e = scale_exponent(top);
-      const float f = pow2i(-e);
-      uint32_t w[2] = {};
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        w[q >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(
-                         make_float2(x[i].x[2 * q] * f, x[i].x[2 * q + 1] * f), __NV_SATFINITE,
-                         __NV_E4M3)
-                     << (16 * (q & 1));
+      const int e = kv_scale_exponent(top);
       if (row >= 0) {
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(values ? c.v : c.k) + row * D + lane * 8) =
-            make_uint2(w[0], w[1]);
+            kv_codes(x[i], e);
         if (lane == 0) (values ? c.v_exp : c.k_exp)[row] = (uint8_t)(e + 127);
       }
     }
@@ -153,7 +82,7 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_read_kernel(GdnKvCacheArgs c,
 #pragma unroll
   for (int i = 0; i < kTokens; ++i) {
     const int t = t0 + i * kStep;
-    row[i] = row_of(c, t < n && in_bounds(&g_err_kv, t >= 0) ? slots[t] : -1, head);
+    row[i] = kv_row_of(&g_err_kv, c, t < n && in_bounds(&g_err_kv, t >= 0) ? slots[t] : -1, head);
   }
   Vec8 x[kTokens];
   if constexpr (!kF8) {

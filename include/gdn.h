@@ -406,7 +406,8 @@ gdn_status gdn_chunk_prefill_noalloc(const gdn_dims* dims, const gdn_opts* opts,
  * "Architecture": [3 DeltaNet + 1 GQA] blocks) and shares prompt prefixes between requests
  * (PR #164 "Hybrid APC Runtime").  The calls below are what such a layer needs next to the
  * recurrent state: its paged key/value cache, the attention of a batch that shares a prefix,
- * and the scores of drafted tokens.
+ * the scores of drafted tokens; the norm and rotation of queries and keys, the block tables of a
+ * step, and the verification of drafted tokens.
  */
 
 /* What a key/value cache holds.  GDN_KV_E4M3: a vector x of head_dim elements (one token, one
@@ -524,6 +525,175 @@ gdn_status gdn_token_logprobs(int32_t rows, int32_t vocab, gdn_dtype dtype, cons
                               float* logprobs, float* entropy, int32_t top_k, int32_t* top_ids,
                               float* top_logprobs, void* workspace, size_t workspace_bytes,
                               void* stream);
+
+/*
+ * gdn_qk_norm_rope -- what stands between a full-attention layer's projection and its attention,
+ * in one pass: the RMS norm of every query and key head, their rotation by position and, with a
+ * cache, the write of keys and values to their slots (as gdn_kv_cache_append would, from the
+ * unrounded keys).
+ * Definition, per token i and head vector x of D elements, in fp32 and rounded once:
+ *     y = x / sqrt(mean(x^2) + eps) * weight          (y = x where the weight is NULL)
+ *     pair p of the first rotary_dim elements, (a, b) = (y_p, y_{p + rotary_dim/2}) in the half
+ *     layout, (y_2p, y_{2p+1}) in the interleaved one:
+ *         (a, b) <- amplitude (a cos w - b sin w, a sin w + b cos w),  w = positions[i] freq_p
+ *     the elements behind them stay as they are.
+ * The angle is exact for every 32-bit position (negative ones turn back): it is kept as a phase,
+ * phase_steps[p] = freq_p / 2 pi 2^64 a token modulo 2^64 (gdn_rope_phase_steps makes them).
+ *   n            tokens.  Rows of padding (a negative slot) are computed like any other.
+ *   q            [n, Hq, D] in dtype: token i at q + i * q_token_stride elements, head h at
+ *                h * q_head_stride behind it (>= D: a gate may lie between the heads).  16-byte
+ *                aligned, both strides a multiple of 16 bytes (of 8 elements for bf16).
+ *   k            [n, H, D], tokens k_token_stride apart, heads dense; aligned as q.
+ *   q_weight, k_weight  [D] fp32, 16-byte aligned, or NULL: no norm.
+ *   eps          >= 0.
+ *   positions    [n] device int32 (may be NULL when rotary_dim is 0).
+ *   rope         rotary_dim 0 .. D (even), the layout, the amplitude, phase_steps
+ *                [rotary_dim / 2] on the device (8-byte aligned; NULL when rotary_dim is 0).
+ *   q_out        [n, Hq, D] in dtype, tokens q_out_token_stride apart, heads dense.  It may be q
+ *                itself (same pointer and strides, heads dense); any other overlap is undefined.
+ *   k_out        [n, H, D] dense in dtype, likewise, or NULL when a cache is given.
+ *   cache        NULL, or the cache that keys and values go to (H and D are its own), with
+ *   v, slots     the values [n, H, D] in dtype, tokens v_token_stride apart, and the tokens'
+ *                slots, as in gdn_kv_cache_append; ignored without a cache.
+ * D is a multiple of 8 up to 256 (128 or 256 with a cache); Hq + 2 H <= 65535.
+ */
+typedef enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_layout;
+
+typedef struct {
+  int32_t rotary_dim;
+  gdn_rope_layout layout;
+  float amplitude;                /* 1 but for contexts extended by GDN_ROPE_YARN */
+  const uint64_t* phase_steps;    /* device, [rotary_dim / 2] */
+} gdn_rope;
+
+gdn_status gdn_qk_norm_rope(int32_t n, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+                            gdn_dtype dtype, const void* q, int64_t q_token_stride,
+                            int64_t q_head_stride, const void* k, int64_t k_token_stride,
+                            const float* q_weight, const float* k_weight, float eps,
+                            const int32_t* positions, const gdn_rope* rope, void* q_out,
+                            int64_t q_out_token_stride, void* k_out, const gdn_kv_cache* cache,
+                            const void* v, int64_t v_token_stride, const int32_t* slots,
+                            void* stream);
+
+/* How the frequencies base^(-2p / rotary_dim) are changed for contexts `factor` (>= 1) times as
+ * long as the trained one.  LINEAR: divided by factor.  NTK: base times factor^(r / (r - 2)), r
+ * the rotary_dim (the slowest pair is divided by factor, the fastest stays; r = 2: nothing).
+ * YARN: pairs that make fewer than beta_slow turns over original_context tokens are divided by
+ * factor, those with more than beta_fast stay, and between the two pairs' indices (rounded
+ * outwards) a ramp mixes both; the amplitude becomes 0.1 ln factor + 1. */
+typedef enum {
+  GDN_ROPE_UNSCALED = 0, GDN_ROPE_LINEAR = 1, GDN_ROPE_NTK = 2, GDN_ROPE_YARN = 3
+} gdn_rope_scaling;
+
+/*
+ * Fills steps[rotary_dim / 2] (HOST memory, to be copied to the device by the caller) and
+ * *amplitude; computed in double.  base > 1; original_context, beta_fast > beta_slow > 0 are read
+ * for YARN only (32 and 1 are usual).
+ */
+gdn_status gdn_rope_phase_steps(int32_t rotary_dim, double base, gdn_rope_scaling scaling,
+                                double factor, double original_context, double beta_fast,
+                                double beta_slow, uint64_t* steps, float* amplitude);
+
+/* The pages that requests hold, and the free ones; all on the device, updated in place by
+ * gdn_page_plan and gdn_page_release. */
+typedef struct {
+  int32_t num_pages;     /* entries of free_pages */
+  int32_t page_size;     /* 16, 32, 64 or 128 tokens */
+  int32_t num_rows;      /* requests that the table has room for */
+  int32_t max_pages;     /* pages of a row; num_pages * page_size, max_pages * page_size < 2^31 */
+  int32_t* table;        /* [num_rows, max_pages]: each row's pages in order */
+  int32_t* held;         /* [num_rows]: pages that the row holds */
+  int32_t* free_pages;   /* [num_pages]: the first *free_count are free, taken from the end */
+  int32_t* free_count;   /* [1] */
+} gdn_page_pool;
+
+/*
+ * gdn_page_plan -- the slots, positions and block tables of a step that adds new_len[b] tokens to
+ * each of B requests, built on the device from the lengths; requests get the pages they lack.
+ * Request b is row r = rows[b] of the pool (b itself when rows is NULL); a negative row leaves
+ * the entry out (no tokens, kv_len_out -1, its block table row untouched).
+ *     need_b  = max(0, ceil((kv_len[b] + new_len[b]) / page_size) - held[r]) more pages, the j-th
+ *               of the whole call (in the order of b) free_pages[*free_count - 1 - j];
+ *     token i of request b (i < new_len[b]) is packed token cu_seqlens[b] + i:
+ *     position = position_offset + kv_len[b] + i,
+ *     slot     = page_size * (page (kv_len[b] + i) / page_size of the request)
+ *                + (kv_len[b] + i) % page_size.
+ *   kv_len, new_len  [B] device int32, >= 0.
+ *   slots, positions [capacity]: of the packed tokens; behind the last one slots are -1 (which
+ *               gdn_kv_cache_append and gdn_qk_norm_rope skip) and positions 0.  Either may be
+ *               NULL.
+ *   cu_seqlens  [B + 1] or NULL: where each request's tokens begin, and their number.
+ *   kv_len_out  [B] or NULL: kv_len + new_len (for gdn_prefix_attention); may be kv_len itself.
+ *   pages       [B, max_pages] or NULL: the requests' block tables; entries behind a request's
+ *               last page are left alone.
+ * Nothing is given when not all can be: if the tokens are more than `capacity`, the pages more
+ * than are free, a request needs more than max_pages, a row is past the table, a length negative
+ * or a count of the pool out of its range, the pool, kv_len_out and pages are left alone, slots
+ * are all -1, positions and cu_seqlens 0, and GDN_ERR_DEVICE_INDEX is recorded.  A page id out of
+ * the pool's range gives slot -1 and is recorded too.  No two entries name one row.
+ * 0 <= B <= 8192.
+ */
+gdn_status gdn_page_plan(const gdn_page_pool* pool, int32_t batch, const int32_t* rows,
+                         const int32_t* kv_len, const int32_t* new_len, int32_t capacity,
+                         int32_t position_offset, int32_t* slots, int32_t* positions,
+                         int32_t* cu_seqlens, int32_t* kv_len_out, int32_t* pages, void* stream);
+
+/*
+ * gdn_page_release -- requests keep the pages of their first keep_len[b] tokens and give the
+ * others back (drafted tokens that were refused; 0: the request ends).  Pages that are already
+ * fewer stay as they are.  What goes back lies on the free pages' end in the reverse of
+ * gdn_page_plan's order, so that giving back all that one call took restores the list.  Entries
+ * of the table behind a row's pages keep their old contents.  A negative row is left out; rows or
+ * lengths out of range, or counts out of the pool's range, leave the pool alone and record
+ * GDN_ERR_DEVICE_INDEX.  No two entries name one row.  0 <= B <= 8192.
+ */
+gdn_status gdn_page_release(const gdn_page_pool* pool, int32_t batch, const int32_t* rows,
+                            const int32_t* keep_len, void* stream);
+
+/*
+ * gdn_verify_tokens -- speculative verification of up to T drafted tokens of each of B sequences
+ * from given random numbers, and the draw of one token behind the last accepted one, so that the
+ * tokens are distributed as the target model's own.  T = 0 draws one token a sequence.
+ * With p_j = softmax(scale[b] target_logits[b, j]), q_j = softmax(scale[b] draft_logits[b, j]) (or
+ * all on the drafted token x_j without draft_logits), the sequence's drafts x_0 .. x_{m-1}:
+ *     accepted = the number of leading j with accept_u[b, j] < p_j(x_j) / q_j(x_j)
+ *     next     = argmax_i w_i / clocks[b, i] over w_i > 0, ties to the lower i, with
+ *                w = max(p_a - q_a, 0) where draft a = accepted < m was refused,
+ *                w = p_m where all were accepted
+ * (the first of exponential clocks with rates w rings at i with probability w_i / sum w).
+ * A refused draft without any w_i > 0 (p = q but for rounding) is itself the next token.
+ *   target_logits [B, T + 1, V] in dtype, rows target_row_stride elements apart (>= V); any
+ *                 alignment of the element's own.  Row j is of the token behind draft j - 1.
+ *   draft_ids     [B, T] device int32: drafts up to the first negative id; the rest of the row is
+ *                 ignored.  An id >= V ends them too and is recorded as GDN_ERR_DEVICE_INDEX.
+ *                 NULL when T is 0.
+ *   draft_logits  [B, T, V] in dtype, rows draft_row_stride apart, or NULL.
+ *   accept_u      [B, T] fp32, uniform on [0, 1); NULL when T is 0.
+ *   clocks        [B, V] fp32, independent exponential numbers; entries that are not above 0
+ *                 (zero, negative, NaN) never ring.
+ *   scale         [B] fp32 inverse temperatures, or NULL (= 1).  +inf: greedy: a draft is accepted
+ *                 if it is the largest logit (the lowest id of equal ones), next is the largest, no
+ *                 random number is read.  Else within [2^-64, 2^64]; any other value (negative,
+ *                 NaN, 0) leaves the sequence out: its outputs are left alone.
+ *   tokens        [B, T + 1] int32: the accepted drafts, next, then -1.
+ *   accepted      [B] int32.
+ *   logprobs      [B, T + 1] fp32 or NULL: log p_j of each token given (at scale 1 for greedy
+ *                 sequences), 0 behind them.
+ * Only the rows of the drafts and of the token behind them are read.  A row that is no
+ * distribution (a NaN or +inf logit, nothing but -inf) accepts nothing; where it is the next
+ * token's, p or q, next is -1 and its logprob 0.
+ *   workspace     gdn_verify_tokens_workspace_size() bytes (0 for invalid sizes), 16-byte aligned.
+ * T <= 64.  Decisions are those of exact arithmetic but where two sides agree to a few 2^-22.
+ */
+size_t gdn_verify_tokens_workspace_size(int32_t batch, int32_t num_drafts, int32_t vocab,
+                                        gdn_dtype dtype, int32_t with_draft_logits);
+gdn_status gdn_verify_tokens(int32_t batch, int32_t num_drafts, int32_t vocab, gdn_dtype dtype,
+                             const void* target_logits, int64_t target_row_stride,
+                             const int32_t* draft_ids, const void* draft_logits,
+                             int64_t draft_row_stride, const float* accept_u,
+                             const float* clocks, const float* scale, int32_t* tokens,
+                             int32_t* accepted, float* logprobs, void* workspace,
+                             size_t workspace_bytes, void* stream);
 
 /*
  * Synchronises `stream`, then returns and clears the device error word: GDN_OK, or the
