@@ -388,6 +388,3 @@ unsigned gdn_take_error_decode_multi();
 unsigned gdn_take_error_kv_cache();
 unsigned gdn_take_error_prefix_attention();
 unsigned gdn_take_error_logprobs();
-unsigned gdn_take_error_qk_norm_rope();
-unsigned gdn_take_error_pages();
-unsigned gdn_take_error_verify();

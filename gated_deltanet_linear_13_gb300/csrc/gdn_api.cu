@@ -913,8 +913,7 @@ gdn_status gdn_get_device_error(void* stream) {
                   gdn_take_error_prefill_simt() | gdn_take_error_prefill_tc() |
                   gdn_take_error_varlen() | gdn_take_error_decode_multi() |
                   gdn_take_error_kv_cache() | gdn_take_error_prefix_attention() |
-                  gdn_take_error_logprobs() | gdn_take_error_qk_norm_rope() |
-                  gdn_take_error_pages() | gdn_take_error_verify();
+                  gdn_take_error_logprobs();
   if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   if (bits & gdn::kErrTimeout) return GDN_ERR_DEVICE_TIMEOUT;
   if (bits & gdn::kErrIndex) return GDN_ERR_DEVICE_INDEX;

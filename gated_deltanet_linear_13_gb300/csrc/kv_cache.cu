@@ -172,3 +172,8 @@ cudaError_t gdn_launch_kv_read(const GdnKvCacheArgs& c, int n, const int32_t* sl
   }
   return cudaGetLastError();
 }
+
+// One error word a translation unit, and reading it is the error query's time (9 us a word): the
+// operators around the cache share its.
+#include "pages.cuh"
+#include "qk_norm_rope.cuh"

@@ -601,3 +601,6 @@ cudaError_t gdn_launch_token_logprobs(const GdnLogprobArgs& a, cudaStream_t stre
   p.tops = reinterpret_cast<uint32_t*>(ws + stats_bytes(a.N));
   return a.bf16 ? launch<__nv_bfloat16>(a, p, stream) : launch<float>(a, p, stream);
 }
+
+// (in this translation unit for its error word: a word more is 9 us more for the error query)
+#include "verify.cuh"

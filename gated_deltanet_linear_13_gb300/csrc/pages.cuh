@@ -6,17 +6,17 @@
 // hundred nanoseconds, so every CTA of one cluster does it for itself and takes its share of the
 // rest; a cluster barrier between the last read of the pool's counts and their update is all the
 // order that is needed, so a call is one launch and keeps nothing between calls.
+// Part of kv_cache.cu, whose error word it uses.
+#pragma once
+
 #include <algorithm>
 
 #include "common.cuh"
 
 using namespace gdn;
 
-static __device__ unsigned int g_err_pages;
-
-unsigned gdn_take_error_pages() { return gdn::take_error(g_err_pages); }
-
 namespace {
+namespace pages {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;                // of the cluster (the portable most)
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(GdnPoolArgs p, 
          totals.b <= (unsigned long long)count;
   cluster_sync();                          // every CTA has read the pool's state and the lengths
   if (!good) {                             // nothing is given
-    if (tid == 0) atomicOr(&g_err_pages, kErrIndex);
+    if (tid == 0) atomicOr(&g_err_kv, kErrIndex);
     for (int t = tid; t < fill; t += threads) {
       if (a.slots) a.slots[t] = -1;
       if (a.positions) a.positions[t] = 0;
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(GdnPoolArgs p, 
   // ---- the requests' new state
   for (int b = tid; b < a.B; b += threads) {
     const int row = s.row[b], need = s.pages[b + 1] - s.pages[b];
-    if (need > 0 && in_bounds(&g_err_pages, row >= 0 && row < p.num_rows))
+    if (need > 0 && in_bounds(&g_err_kv, row >= 0 && row < p.num_rows))
       p.held[row] = s.held[b] + need;
     if (a.len_out)
       a.len_out[b] = row < 0 ? -1 : s.from[b] + s.tokens[b + 1] - s.tokens[b];
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(GdnPoolArgs p, 
     int* table = p.table + (long long)row * p.max_pages;
     int* pages = a.pages ? a.pages + (long long)b * p.max_pages : nullptr;
     for (int c = (pages ? c0 : max(c0, held)) + lane; c < end; c += 32) {
-      if (!in_bounds(&g_err_pages, c >= 0 && c < p.max_pages)) break;
+      if (!in_bounds(&g_err_kv, c >= 0 && c < p.max_pages)) break;
       const bool fresh = c >= held;
       const int page = fresh ? p.free_pages[count - 1 - (first + c - held)] : table[c];
       if (fresh) table[c] = page;
@@ -201,11 +201,11 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(GdnPoolArgs p, 
       if (a.slots) {
         const int c = at >> p.page_shift, held = s.held[b], row = s.row[b];
         int page = -1;
-        if (in_bounds(&g_err_pages, row >= 0 && c < p.max_pages))
+        if (in_bounds(&g_err_kv, row >= 0 && c < p.max_pages))
           page = c < held ? p.table[(long long)row * p.max_pages + c]
                           : p.free_pages[count - 1 - (s.pages[b] + c - held)];
         if (page >= 0 && page < p.num_pages) slot = (page << p.page_shift) + (at & mask);
-        else atomicOr(&g_err_pages, kErrIndex);
+        else atomicOr(&g_err_kv, kErrIndex);
       }
     }
     if (a.slots) a.slots[t] = slot;
@@ -224,13 +224,13 @@ __global__ void __launch_bounds__(kThreads) gdn_page_release_kernel(GdnPoolArgs 
   good = good && count >= 0 && totals.b + (unsigned long long)count <= (unsigned long long)p.num_pages;
   cluster_sync();
   if (!good) {
-    if (tid == 0) atomicOr(&g_err_pages, kErrIndex);
+    if (tid == 0) atomicOr(&g_err_kv, kErrIndex);
     return;
   }
   const int end = count + (int)totals.b;
   for (int b = tid; b < a.B; b += threads)
     if (s.pages[b + 1] > s.pages[b] &&
-        in_bounds(&g_err_pages, s.row[b] >= 0 && s.row[b] < p.num_rows))
+        in_bounds(&g_err_kv, s.row[b] >= 0 && s.row[b] < p.num_rows))
       p.held[s.row[b]] = s.from[b];
   if (tid == 0) *p.free_count = end;
   const int lane = threadIdx.x & 31, warps = ctas * kWarps;
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) gdn_page_release_kernel(GdnPoolArgs 
     const int* table = p.table + (long long)s.row[b] * p.max_pages + kept;
     for (int c = c0 + lane; c < min(c0 + kColumns, given); c += 32) {
       const int to = end - 1 - (first + c);
-      if (in_bounds(&g_err_pages, to >= count && to < p.num_pages && kept + c < p.max_pages))
+      if (in_bounds(&g_err_kv, to >= count && to < p.num_pages && kept + c < p.max_pages))
         p.free_pages[to] = table[c];
     }
   }
@@ -274,17 +274,18 @@ cudaError_t launch(K kernel, const GdnPoolArgs& p, const GdnPlanArgs& a, long lo
   return cudaLaunchKernelEx(&cfg, kernel, p, a);
 }
 
+}  // namespace pages
 }  // namespace
 
 cudaError_t gdn_launch_page_plan(const GdnPoolArgs& p, const GdnPlanArgs& a, cudaStream_t stream) {
   static unsigned done = 0;
   const long long fill = a.slots || a.positions ? a.capacity : 0;
   const long long tables = (long long)a.B * p.max_pages;
-  return launch(gdn_page_plan_kernel, p, a, std::max(fill, tables), &done, stream);
+  return pages::launch(pages::gdn_page_plan_kernel, p, a, std::max(fill, tables), &done, stream);
 }
 
 cudaError_t gdn_launch_page_release(const GdnPoolArgs& p, const GdnPlanArgs& a,
                                     cudaStream_t stream) {
   static unsigned done = 0;
-  return launch(gdn_page_release_kernel, p, a, (long long)a.B * p.max_pages, &done, stream);
+  return pages::launch(pages::gdn_page_release_kernel, p, a, (long long)a.B * p.max_pages, &done, stream);
 }

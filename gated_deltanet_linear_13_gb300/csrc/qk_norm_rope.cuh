@@ -11,16 +11,16 @@
 // D / 8 lanes a vector, eight elements a lane, so a pair's halves lie in one lane (interleaved), in
 // lanes rotary_dim / 16 apart (halves, where rotary_dim / 2 is a multiple of eight: a shuffle), or
 // go through shared memory.  A token's cos and sin are made once for all its heads.
+// Part of kv_cache.cu, whose error word it uses.
+#pragma once
+
 #include "common.cuh"
 #include "kv_cache.cuh"
 
 using namespace gdn;
 
-static __device__ unsigned int g_err_rope;
-
-unsigned gdn_take_error_qk_norm_rope() { return gdn::take_error(g_err_rope); }
-
 namespace {
+namespace rope {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 128;
@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kThreads) gdn_qk_norm_rope_kernel(GdnRopeArgs 
   // ---- cos and sin of the tokens' angles
   for (int i = threadIdx.x; i < tokens * (r / 2); i += kThreads) {
     const int t = i / (r / 2), p = i - t * (r / 2);
-    if (!in_bounds(&g_err_rope, t0 + t < a.n && p < kMaxPairs)) break;
+    if (!in_bounds(&g_err_kv, t0 + t < a.n && p < kMaxPairs)) break;
     const uint64_t phase = (uint64_t)(int64_t)a.positions[t0 + t] * a.steps[p];
     float sn, cs;
     sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &sn, &cs);
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) gdn_qk_norm_rope_kernel(GdnRopeArgs 
                        : h < a.Hq + a.H
                            ? (const T*)a.k + tok * a.k_tok + (long long)(h - a.Hq) * D
                            : (const T*)a.v + tok * a.v_tok + (long long)(h - a.Hq - a.H) * D;
-        if (in_bounds(&g_err_rope, tok < a.n)) x[u] = load8(src + e0);
+        if (in_bounds(&g_err_kv, tok < a.n)) x[u] = load8(src + e0);
       }
     }
 #pragma unroll
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) gdn_qk_norm_rope_kernel(GdnRopeArgs 
         }
       }
       // ---- out
-      const bool live = i < all && mine && in_bounds(&g_err_rope, tok < a.n && e0 + 8 <= D);
+      const bool live = i < all && mine && in_bounds(&g_err_kv, tok < a.n && e0 + 8 <= D);
       if (query) {
         if (live) store8((T*)a.q_out + tok * a.q_out_tok + (long long)h * D + e0, y);
       }
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) gdn_qk_norm_rope_kernel(GdnRopeArgs 
       if constexpr (kTo != kToTensors) {
         const int head = query ? 0 : h - a.Hq - (value ? a.H : 0);
         long long row = -1;
-        if (!query && i < all) row = kv_row_of(&g_err_rope, a.cache, a.slots[tok], head);
+        if (!query && i < all) row = kv_row_of(&g_err_kv, a.cache, a.slots[tok], head);
         if constexpr (kTo == kToBf16) {
           if (row >= 0 && live)
             store8((__nv_bfloat16*)(value ? a.cache.v : a.cache.k) + row * D + e0, y);
@@ -199,13 +199,14 @@ cudaError_t launch(const GdnRopeArgs& a, cudaStream_t stream) {
   return launch<T, 8>(a, stream);
 }
 
+}  // namespace rope
 }  // namespace
 
 cudaError_t gdn_launch_qk_norm_rope(GdnRopeArgs a, int in_bf16, cudaStream_t stream) {
   a.inv_d = 1.0f / (float)a.D;
-  a.turn = a.rotary == 0 ? kNoTurn
-           : a.interleaved ? kNeighbours
-           : a.rotary % 16 == 0 ? kHalvesShuffled
-                                : kHalves;
-  return in_bf16 ? launch<__nv_bfloat16>(a, stream) : launch<float>(a, stream);
+  a.turn = a.rotary == 0 ? rope::kNoTurn
+           : a.interleaved ? rope::kNeighbours
+           : a.rotary % 16 == 0 ? rope::kHalvesShuffled
+                                : rope::kHalves;
+  return in_bf16 ? rope::launch<__nv_bfloat16>(a, stream) : rope::launch<float>(a, stream);
 }

@@ -13,7 +13,8 @@
 // sequence joins the slices.  An element takes part only if w > best E, so there is a division
 // where the best changes and none elsewhere, and p's normaliser cancels: w = e^.. - e^.. (z_p / z_q).
 // The decisions are compared in 32 bits and, where two are within 2^-16 of each other, again in 64.
-#include <float.h>
+// Part of logprobs.cu, whose error word it uses.
+#pragma once
 
 #include "common.cuh"
 #include "logits.cuh"
@@ -26,11 +27,8 @@ using ptx::mul2;
 using ptx::pair;
 using ptx::unpair;
 
-static __device__ unsigned int g_err_verify;
-
-unsigned gdn_take_error_verify() { return gdn::take_error(g_err_verify); }
-
 namespace {
+namespace verify {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 4, kParts = 152 * kCtasPerSm * kWarps;
@@ -126,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gdn_verify_rows_kernel(G
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           const T* at = ap + v * 32 * G::kVec;
-          if (in_bounds(&g_err_verify, at >= ax && at + G::kVec <= ax + a.V))
+          if (in_bounds(&g_err_lp, at >= ax && at + G::kVec <= ax + a.V))
             to[v] = load_inner<false>(at);
         }
       } else {
@@ -198,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gdn_verify_rows_kernel(G
     float z0, z1;
     unpair(z2, &z0, &z1);
     const Row st = warp_merge(Row{m, z0 + z1, m == -INFINITY ? q0 : first}, c);
-    if (lane == 0 && in_bounds(&g_err_verify, b < a.B && part < kParts))
+    if (lane == 0 && in_bounds(&g_err_lp, b < a.B && part < kParts))
       p.stats[row + part] = make_float4(st.m, st.z, __int_as_float(st.q), 0.0f);
     if (q == p.granules) {
       q = 0;
@@ -258,7 +256,7 @@ __global__ void __launch_bounds__(kThreads) gdn_verify_race_kernel(GdnVerifyArgs
   if (threadIdx.x == 0) {
     s_refused = n;
     if (piece == 0 && n < a.T && a.ids[(long long)b * a.T + n] >= a.V)
-      atomicOr(&g_err_verify, kErrIndex);
+      atomicOr(&g_err_lp, kErrIndex);
   }
   pdl_wait();
   // ---- the rows' statistics, a warp a row
@@ -270,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) gdn_verify_race_kernel(GdnVerifyArgs
     const int pieces = (int)(((x1 + 1) * p.parts - 1) / p.total) - c0 + 1;
     Row st{-INFINITY, 0.0f, 0x7fffffff};
     for (int k = lane; k < pieces; k += 32) {
-      if (!in_bounds(&g_err_verify, c0 >= 0 && c0 + k < kParts)) break;
+      if (!in_bounds(&g_err_lp, c0 >= 0 && c0 + k < kParts)) break;
       const float4 v = p.stats[row + c0 + k];
       st = merge(st, Row{v.x, v.y, __float_as_int(v.z)}, c);
     }
@@ -362,7 +360,7 @@ __global__ void __launch_bounds__(kThreads) gdn_verify_race_kernel(GdnVerifyArgs
     if (aligned) {                         // (a slice is a multiple of 16 logits)
       int i = lo + (int)threadIdx.x * kVec;
       for (; i + kVec <= hi; i += kThreads * kVec) {
-        if (!in_bounds(&g_err_verify, i >= 0 && i + kVec <= a.V)) break;
+        if (!in_bounds(&g_err_lp, i >= 0 && i + kVec <= a.V)) break;
         const uint4 ux = *reinterpret_cast<const uint4*>(race.x + i);
         const uint4 uy = race.y ? *reinterpret_cast<const uint4*>(race.y + i) : make_uint4(0, 0, 0, 0);
         float x[kVec], y[kVec], e[kVec];
@@ -381,7 +379,7 @@ __global__ void __launch_bounds__(kThreads) gdn_verify_race_kernel(GdnVerifyArgs
     } else {
 #pragma unroll 4
       for (int i = lo + (int)threadIdx.x; i < hi; i += kThreads) {
-        if (!in_bounds(&g_err_verify, i >= 0 && i < a.V)) break;
+        if (!in_bounds(&g_err_lp, i >= 0 && i < a.V)) break;
         race.offer(weight(ld_elem(race.x + i), race.y ? ld_elem(race.y + i) : 0.0f), race.clocks[i], i);
       }
     }
@@ -448,7 +446,7 @@ __global__ void __launch_bounds__(kThreads) gdn_verify_race_kernel(GdnVerifyArgs
   for (int t = threadIdx.x; t <= a.T; t += kThreads) {
     const int id = t < accepted ? a.ids[(long long)b * a.T + t] : t == accepted ? token : -1;
     const long long to = (long long)b * (a.T + 1) + t;
-    if (!in_bounds(&g_err_verify, id < a.V)) continue;
+    if (!in_bounds(&g_err_lp, id < a.V)) continue;
     a.tokens[to] = id;
     if (a.logprobs) {
       float lp = 0.0f;
@@ -490,18 +488,19 @@ cudaError_t launch(const GdnVerifyArgs& a, const Plan& p, cudaStream_t stream) {
                     dim3(kThreads), 0, stream, a, p);
 }
 
+}  // namespace verify
 }  // namespace
 
 size_t gdn_verify_tokens_bytes(int B, int T, int V, int bf16, int draft) {
-  const Plan p = plan_of(B, T, V, bf16, draft);
-  return stats_bytes(p, B) + best_bytes(p, B) + up(sizeof(int) * (size_t)B);
+  const verify::Plan p = verify::plan_of(B, T, V, bf16, draft);
+  return verify::stats_bytes(p, B) + verify::best_bytes(p, B) + verify::up(sizeof(int) * (size_t)B);
 }
 
 cudaError_t gdn_launch_verify_tokens(const GdnVerifyArgs& a, cudaStream_t stream) {
-  Plan p = plan_of(a.B, a.T, a.V, a.bf16, a.draft != nullptr);
+  verify::Plan p = verify::plan_of(a.B, a.T, a.V, a.bf16, a.draft != nullptr);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.stats = reinterpret_cast<float4*>(ws);
-  p.best = reinterpret_cast<float2*>(ws + stats_bytes(p, a.B));
-  p.done = reinterpret_cast<int*>(ws + stats_bytes(p, a.B) + best_bytes(p, a.B));
-  return a.bf16 ? launch<__nv_bfloat16>(a, p, stream) : launch<float>(a, p, stream);
+  p.best = reinterpret_cast<float2*>(ws + verify::stats_bytes(p, a.B));
+  p.done = reinterpret_cast<int*>(ws + verify::stats_bytes(p, a.B) + verify::best_bytes(p, a.B));
+  return a.bf16 ? verify::launch<__nv_bfloat16>(a, p, stream) : verify::launch<float>(a, p, stream);
 }
