@@ -343,8 +343,8 @@ struct GdnRopeArgs {
   void* k_out;                                          // or NULL
   GdnKvCacheArgs cache;
   const int32_t* slots;
-  float inv_d;                                          // (set by the launcher)
-  int turn;
+  float inv_d;                                          // (these are set by the launcher)
+  int turn, tokens;
 };
 cudaError_t gdn_launch_qk_norm_rope(GdnRopeArgs a, int in_bf16, cudaStream_t stream);
 

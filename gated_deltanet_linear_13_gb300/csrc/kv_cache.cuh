@@ -78,16 +78,19 @@ __device__ __forceinline__ float kv_largest(const Vec8& v) {
   }
   return top;
 }
-// Their e4m3 codes under the scale 2^e.
-__device__ __forceinline__ uint2 kv_codes(const Vec8& v, int e) {
+// The e4m3 codes of four elements under the scale 2^e.
+__device__ __forceinline__ uint32_t kv_codes4(const float* x, int e) {
   const float f = pow2i(-e);
-  uint32_t w[2] = {};
+  uint32_t w = 0;
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
-    w[q >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(
-                     make_float2(v.x[2 * q] * f, v.x[2 * q + 1] * f), __NV_SATFINITE, __NV_E4M3)
-                 << (16 * (q & 1));
-  return make_uint2(w[0], w[1]);
+  for (int q = 0; q < 2; ++q)
+    w |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2 * q] * f, x[2 * q + 1] * f),
+                                            __NV_SATFINITE, __NV_E4M3)
+         << (16 * q);
+  return w;
+}
+__device__ __forceinline__ uint2 kv_codes(const Vec8& v, int e) {
+  return make_uint2(kv_codes4(v.x, e), kv_codes4(v.x + 4, e));
 }
 
 }  // namespace gdn
