@@ -851,9 +851,9 @@ gdn_status gdn_page_release(const gdn_page_pool* pool, int32_t batch, const int3
 static gdn_status check_verify_dims(int32_t batch, int32_t drafts, int32_t vocab,
                                     gdn_dtype dtype) {
   if (batch < 0 || drafts < 0 || vocab < 1 || !is_dtype(dtype)) return GDN_ERR_INVALID_ARGUMENT;
-  // slices of sequences and granules of rows are counted in 32 and 52 bits; an index past the row
-  // by a granule stays within 32
   if (drafts > kGdnMaxDrafts || batch > (1 << 24) || vocab > (1 << 30)) return GDN_ERR_UNSUPPORTED;
+  // the rows' granules (a kilobyte each, at least one a row) are counted in 32 bits
+  if ((double)batch * (2 * drafts + 1) * (vocab / 256 + 2) > 0x7fff0000) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
 

@@ -9,10 +9,12 @@
 // Two passes.  The first reads every row once: its largest logit m and z = sum e^(s (x - m)), as
 // the token log probabilities do it, on one line of granules cut into equal parts (a warp's each).
 // The second knows each sequence's accepted count from them, and runs the race over the one row
-// pair that matters, which L2 still holds where the batch is small: a CTA a slice, the last CTA of a
-// sequence joins the slices.  An element takes part only if w > best E, so there is a division
-// where the best changes and none elsewhere, and p's normaliser cancels: w = e^.. - e^.. (z_p / z_q).
-// The decisions are compared in 32 bits and, where two are within 2^-16 of each other, again in 64.
+// pair that matters, the last sequences first, whose rows L2 still holds: a CTA a slice, the last
+// CTA of a sequence joins the slices.  p's normaliser cancels in the race (w = e^.. - e^.. z_p / z_q),
+// so without drafts the first pass runs it as it goes and the second only joins.
+// A warp keeps the best w / E of its elements so far; an element is looked at closer only if
+// w > best E, nearly, so there is a division where the best changes and none elsewhere.  Where two
+// are within 2^-16 of each other they are compared in 64 bits, and so is a u near its border.
 // Part of logprobs.cu, whose error word it uses.
 #pragma once
 
@@ -31,20 +33,22 @@ namespace {
 namespace verify {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 4, kParts = 152 * kCtasPerSm * kWarps;
+constexpr int kCtasPerSm = 3, kDrawCtasPerSm = 2, kRaceCtasPerSm = 3;
 constexpr int kMaxRows = 2 * kGdnMaxDrafts + 1;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMost = 18446744073709551616.0f;       // 2^64: scales lie within it and its inverse
 constexpr float kClose = 1.0f - 0x1p-16f;
 
 struct Plan {
-  long long total;                         // granules of all rows
   int granules;                            // of a row
   int rows;                                // of a sequence: T + 1 of the target, then the draft's
-  int parts;                               // equal parts of the line, a warp's each
+  int parts;                               // of the line of all rows' granules, a warp's each
+  int each, more;                          // granules of a part, and the first `more` have one more
   int pieces;                              // slices of a sequence's race
   int slice;                               // logits of a slice
-  float4* stats;                           // [row + part]: m, z, granule of the largest
+  float4* stats;                           // [row + part]: m, z, granule of the largest; where
+                                           // the first pass draws: m, z, index (greedy:
+                                           // granule), w / E
   float2* best;                            // [B][pieces]: w / E and its index
   int* done;                               // [B]
 };
@@ -64,12 +68,94 @@ __device__ __forceinline__ Row merge(const Row& a, const Row& b, float c) {
   const float zb = b.m == -INFINITY ? 0.0f : b.z * ptx::ex2_approx((b.m - m) * c);
   return Row{m, za + zb, q};
 }
-__device__ __forceinline__ Row warp_merge(Row a, float c) {
+// A float's bits in the order of the numbers, and back.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float((u & 0x80000000u) ? u & 0x7fffffffu : ~u);
+}
+// The largest of the warp's (no NaN).
+__device__ __forceinline__ float warp_max(float x) {
+  return unordered(__reduce_max_sync(0xffffffffu, ordered(x)));
+}
+__device__ __forceinline__ Row warp_merge(const Row& a, float c) {
+  const float m = warp_max(a.m);
+  const int q = (int)__reduce_min_sync(0xffffffffu, a.m == m ? (unsigned)a.q : 0x7fffffffu);
+  // (where m is -inf every z is 0 or NaN)
+  const float z = a.m == m ? a.z : a.z * ptx::ex2_approx((a.m - m) * c);
+  return Row{m, warp_sum(z), q};
+}
+
+// The sums' reference: a term is 2^(x c - base), base = m c as it rounds, in one rounding, where that
+// is near enough; else 2^((x - m) c).  The first carry 2^rounding(m, c), which settled() takes out.
+struct Reference {
+  float m, base;
+  bool near;
+
+  __device__ __forceinline__ void start() { m = base = -INFINITY, near = false; }
+  // moves to a larger m; returns what sums under the old one are multiplied by
+  __device__ __forceinline__ float raise(float to, float c) {
+    const float f = ptx::ex2_approx(reference_difference(m, to, c));   // (0 from -inf)
+    m = to;
+    base = to * c;
+    near = fabsf(base) <= kNear;
+    return f;
+  }
+  __device__ __forceinline__ float settled(float c) const { return ptx::ex2_approx(-rounding(m, c)); }
+  // the terms of N numbers, two at a time to f
+  template <int N, typename F>
+  __device__ __forceinline__ void terms(const float (&x)[N], float c, F&& f) const {
+    const unsigned long long c2 = pair(c, c);
+    if (near) {
+      const unsigned long long minus = pair(-base, -base);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    a = merge(a, Row{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.z, o),
-                     __shfl_xor_sync(0xffffffffu, a.q, o)}, c);
-  return a;
+      for (int k = 0; k < N; k += 2) {
+        float t0, t1;
+        unpair(fma2(pair(x[k], x[k + 1]), c2, minus), &t0, &t1);
+        f(k, ptx::ex2_approx(t0), ptx::ex2_approx(t1));
+      }
+    } else {
+      const unsigned long long minus = pair(-m, -m);
+#pragma unroll
+      for (int k = 0; k < N; k += 2) {
+        float t0, t1;
+        unpair(mul2(add2(pair(x[k], x[k + 1]), minus), c2), &t0, &t1);
+        f(k, ptx::ex2_approx(t0), ptx::ex2_approx(t1));
+      }
+    }
+  }
+};
+
+// load_vec with the vectors that are only partly the row's out of line (a call waits for its loads;
+// in line they cost the loops registers).
+template <typename T>
+__device__ __noinline__ uint4 partial_vec(const T* row, long long i, int V) {
+  return load_vec<false>(row, i, V);
+}
+template <bool kOnce, typename T>
+__device__ __forceinline__ uint4 edge_vec(const T* row, long long i, int V) {
+  constexpr int kVec = Granule<T>::kVec;
+  constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;     // -inf
+  uint4 u = make_uint4(kNone, kNone, kNone, kNone);
+  if (i >= 0 && i + kVec <= V) u = load_inner<kOnce>(row + i);
+  else if (i + kVec > 0 && i < V) u = partial_vec(row, i, V);
+  return u;
+}
+
+// Granules [first, first + count) of the line.
+struct Part {
+  int first, count;
+};
+__device__ __forceinline__ Part part_at(const Plan& p, int part) {
+  return Part{part * p.each + min(part, p.more), p.each + (part < p.more ? 1 : 0)};
+}
+// The part that granule x is in.
+__device__ __forceinline__ int part_of(const Plan& p, int x) {
+  const int wide = p.more * (p.each + 1);
+  return x < wide ? (int)((unsigned)x / (unsigned)(p.each + 1))
+                  : p.more + (int)((unsigned)(x - wide) / (unsigned)p.each);
 }
 
 __device__ __forceinline__ bool in_range(float s) { return s >= 1.0f / kMost && s <= kMost; }
@@ -96,6 +182,73 @@ __device__ __forceinline__ int drafts_of(const GdnVerifyArgs& a, int b) {
   return n;
 }
 
+// w / E of element i in 64 bits (seldom: out of line, so that it costs the loops no registers).
+template <typename T>
+__device__ __noinline__ double exact_race(const T* x, const T* y, const float* clocks, float mx,
+                                          float my, float ratio, float scale, int i) {
+  double w = exp(((double)ld_elem(x + i) - (double)mx) * (double)scale);
+  if (y) w -= exp(((double)ld_elem(y + i) - (double)my) * (double)scale) * (double)ratio;
+  return w / (double)clocks[i];
+}
+
+// The race of one row pair, as a warp runs it: the same best in all lanes.
+template <typename T>
+struct Race {
+  const T* x;                              // the target's row
+  const T* y;                              // the draft's, or NULL
+  const float* clocks;
+  float mx, my, c, ratio;                  // ratio: z_p / z_q
+  float scale;
+  int never;                               // the refused draft where q is all on it, or -1
+  float best;                              // w / E
+  int at;
+
+  __device__ __forceinline__ void challenge(float r, int i) {
+    bool wins = best == 0.0f || r * kClose > best;
+    if (!wins && r >= best * kClose) {
+      const double mine = exact_race(x, y, clocks, mx, my, ratio, scale, at);
+      const double other = exact_race(x, y, clocks, mx, my, ratio, scale, i);
+      wins = other > mine || (other == mine && i < at);
+    }
+    if (wins) best = r, at = i;
+  }
+  // the lanes' best (r = 0: none), one a lane
+  __device__ __forceinline__ void join(float r, int i) {
+    const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(r)));
+    uint32_t who = __ballot_sync(0xffffffffu, r > 0.0f && r >= top * kClose);
+    while (who) {                          // seldom more than one
+      const int from = __ffs(who) - 1;
+      who &= who - 1;
+      challenge(__shfl_sync(0xffffffffu, r, from), __shfl_sync(0xffffffffu, i, from));
+    }
+  }
+  // N elements of each lane, the k-th of index i0 + k kStep
+  template <int N, int kStep>
+  __device__ __forceinline__ void offer(const float (&w)[N], const float (&e)[N], int i0) {
+    const float floor = best * kClose;
+    float over = 0.0f;                     // (a NaN or an infinite clock stays below)
+#pragma unroll
+    for (int k = 0; k < N; ++k) over = fmaxf(over, fmaf(-floor, e[k], w[k]));
+    if (!__any_sync(0xffffffffu, over > 0.0f)) return;
+    float r = 0.0f;
+    int at_k = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = i0 + k * kStep;
+      if (!(e[k] > 0.0f && w[k] > 0.0f && w[k] > floor * e[k] && i != never)) continue;
+      const float q = __fdiv_rn(w[k], e[k]);
+      if (q > r) r = q, at_k = i;
+    }
+    if (__any_sync(0xffffffffu, r > 0.0f)) join(r, at_k);
+  }
+};
+
+// Whether row j of sequence b is needed: its drafts', and the one behind them (the whole warp).
+__device__ __forceinline__ bool needed(const GdnVerifyArgs& a, int b, int j) {
+  const int n = drafts_of(a, b);
+  return takes_part(a.scale ? a.scale[b] : 1.0f) && (j <= a.T ? j <= n : j - a.T - 1 < n);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) gdn_verify_rows_kernel(GdnVerifyArgs a,
                                                                               Plan p) {
@@ -105,147 +258,295 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gdn_verify_rows_kernel(G
   pdl_trigger();
   for (int b = blockIdx.x * kThreads + threadIdx.x; b < a.B; b += gridDim.x * kThreads) p.done[b] = 0;
   if (part >= p.parts) return;
-  const long long start = p.total * part / p.parts;
-  int left = (int)(p.total * (part + 1) / p.parts - start);
-  const long long row0 = start / p.granules;
-  long long row = row0;                    // of all sequences
-  int q = (int)(start - row * p.granules); // granule of the row
-  int b = (int)(row / p.rows), j = (int)(row - (long long)b * p.rows);
-  // the granules ahead: the sequence, row and granule of the next to be loaded
-  int ab = b, aj = j, aq = q, aleft = left;
-  const T* ax = row_at<T>(a, ab, aj);
-  const T* ap = ax - shift_of(ax) + (long long)aq * G::kLogits + lane * G::kVec;
-  bool wanted = true;                      // (the first row is read before that is known)
+  const Part l = part_at(p, part);
+  int left = l.count, row = (int)((unsigned)l.first / (unsigned)p.granules);
+  int q = l.first - row * p.granules;
+  // The granules ahead: sequence, row and granule of the next to be loaded, and how many are left.
+  // `run` of them (already counted) need nothing looked at: they are wanted and all of them the row's.
+  int ab = (int)((unsigned)row / (unsigned)p.rows), aj = row - ab * p.rows, aq = q, aleft = left, run = 0;
+  const T *ax, *ap;
+  bool wanted = true;                      // (of the first row: for the first granules)
+  auto at_row = [&]() {
+    ax = row_at<T>(a, ab, aj);
+    ap = ax - shift_of(ax) + (long long)aq * G::kLogits + lane * G::kVec;
+  };
+  at_row();
   uint4 ahead[kDepth][2];
-  auto load = [&](uint4 (&to)[2]) {
-    if (aleft <= 0) return;
-    if (wanted) {
-      if (aq > 0 && aq + 2 < p.granules) { // all of it the row's
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const T* at = ap + v * 32 * G::kVec;
-          if (in_bounds(&g_err_lp, at >= ax && at + G::kVec <= ax + a.V))
-            to[v] = load_inner<false>(at);
-        }
-      } else {
-#pragma unroll
-        for (int v = 0; v < 2; ++v) to[v] = load_vec<false>(ax, ap - ax + v * 32 * G::kVec, a.V);
-      }
-    }
-    --aleft;
-    ap += G::kLogits;
-    if (++aq == p.granules) {
+  auto slow_load = [&](uint4 (&to)[2]) {
+    if (aleft == 0) return;
+    if (aq == p.granules) {
       aq = 0;
       if (++aj == p.rows) aj = 0, ++ab;
-      if (aleft > 0) {
-        const int n = drafts_of(a, ab);
-        wanted = takes_part(a.scale ? a.scale[ab] : 1.0f) && (aj <= a.T ? aj <= n : aj - a.T - 1 < n);
-        ax = row_at<T>(a, ab, aj);
-        ap = ax - shift_of(ax) + lane * G::kVec;
+      at_row();
+      wanted = needed(a, ab, aj);
+    }
+    if (wanted)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) to[v] = edge_vec<false>(ax, ap - ax + v * 32 * G::kVec, a.V);
+    ap += G::kLogits;
+    ++aq, --aleft;
+    run = wanted && aq > 0 ? max(0, min(aleft, p.granules - 2 - aq)) : 0;
+    aq += run, aleft -= run;
+  };
+  auto load = [&](uint4 (&to)[2]) {
+    if (run > 0) {
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        const T* at = ap + v * 32 * G::kVec;
+        if (in_bounds(&g_err_lp, at >= ax && at + G::kVec <= ax + a.V)) to[v] = load_inner<false>(at);
       }
+      ap += G::kLogits;
+      --run;
+    } else {
+      slow_load(to);
     }
   };
 #pragma unroll
   for (int i = 0; i < kDepth; ++i) load(ahead[i]);
+  wanted = needed(a, ab, aj);
+  if (!wanted) aq -= run, aleft += run, run = 0;
   while (left > 0) {
     // ---- this warp's granules of a row
-    const float scale = a.scale ? a.scale[b] : 1.0f;
-    const float c = scale_of(scale) * kLog2e;
-    const unsigned long long c2 = pair(c, c);
-    float m = -INFINITY;
-    int first = 0;                         // the first of this lane's granules that holds m
+    const int b = (int)((unsigned)row / (unsigned)p.rows), j = row - b * p.rows;
+    const float c = scale_of(a.scale ? a.scale[b] : 1.0f) * kLog2e;
+    const bool read = needed(a, b, j);   // (then it was loaded)
+    Reference ref;
+    ref.start();
+    int first = 0;                       // the first of this lane's granules that holds m
     unsigned long long z2 = 0;
     const int q0 = q, q1 = q + left < p.granules ? q + left : p.granules;
-    bool read = takes_part(scale);
-    if (row != row0) {       // (as decided when the row was loaded)
-      const int n = drafts_of(a, b);
-      read = read && (j <= a.T ? j <= n : j - a.T - 1 < n);
-    }
 #pragma unroll kDepth
     for (; q < q1; ++q) {
-      if (read) {
-        float f[G::kPer], top, least;
-        widen(ahead[0][0], (const T*)nullptr, f);
-        widen(ahead[0][1], (const T*)nullptr, f + G::kVec);
-        range(ahead[0][0], ahead[0][1], (const T*)nullptr, f, &top, &least);
-        if (top > m) {                     // seldom after the first granules
-          const float s = ptx::ex2_approx((m - top) * c);
-          z2 = mul2(z2, pair(s, s));       // (0 from m = -inf; a NaN stays)
-          m = top;
-          first = q;
-        }
-        if (m != -INFINITY || top != top) {
-          const unsigned long long minus_m = pair(-m, -m);
-#pragma unroll
-          for (int e = 0; e < G::kPer; e += 2) {
-            float t0, t1;
-            unpair(mul2(add2(pair(f[e], f[e + 1]), minus_m), c2), &t0, &t1);
-            z2 = add2(z2, pair(ptx::ex2_approx(t0), ptx::ex2_approx(t1)));
-          }
-        }
-      }
+      float f[G::kPer], top, least;
+      widen(ahead[0][0], (const T*)nullptr, f);
+      widen(ahead[0][1], (const T*)nullptr, f + G::kVec);
+      range(ahead[0][0], ahead[0][1], (const T*)nullptr, f, &top, &least);
 #pragma unroll
       for (int i = 0; i + 1 < kDepth; ++i) {
         ahead[i][0] = ahead[i + 1][0];
         ahead[i][1] = ahead[i + 1][1];
       }
       load(ahead[kDepth - 1]);
+      if (!read) continue;
+      if (top > ref.m) {                 // seldom after the first granules
+        const float s = ref.raise(top, c);
+        z2 = mul2(z2, pair(s, s));       // (a NaN stays)
+        first = q;
+      }
+      if (ref.m != -INFINITY || top != top) {
+        ref.terms(f, c, [&](int, float w0, float w1) { z2 = add2(z2, pair(w0, w1)); });
+      }
     }
     left -= q1 - q0;
     // ---- their statistics
     float z0, z1;
     unpair(z2, &z0, &z1);
-    const Row st = warp_merge(Row{m, z0 + z1, m == -INFINITY ? q0 : first}, c);
-    if (lane == 0 && in_bounds(&g_err_lp, b < a.B && part < kParts))
-      p.stats[row + part] = make_float4(st.m, st.z, __int_as_float(st.q), 0.0f);
-    if (q == p.granules) {
-      q = 0;
-      ++row;
-      if (++j == p.rows) j = 0, ++b;
-    }
+    const Row st = warp_merge(Row{ref.m, ref.m == -INFINITY ? z0 + z1 : (z0 + z1) * ref.settled(c),
+                                  ref.m == -INFINITY ? q0 : first}, c);
+    if (lane == 0 && in_bounds(&g_err_lp, b < a.B && part < p.parts))
+      p.stats[(long long)row + part] = make_float4(st.m, st.z, __int_as_float(st.q), 0.0f);
+    if (q == p.granules) q = 0, ++row;
   }
 }
 
-// Is (v, i) before (w, j) in the race?  The larger, then the lower index.
-__device__ __forceinline__ bool beats(float v, int i, float w, int j) {
-  return v > w || (v == w && i < j);
-}
-
-// The race's elements of one sequence, as each thread of the second kernel needs them.
+// Without drafts: the rows' statistics, and the race of each, in one pass.
 template <typename T>
-struct Race {
-  const T* x;                              // the target's row
-  const T* y;                              // the draft's, or NULL
-  const float* clocks;
-  float mx, my, c, ratio;                  // ratio: z_p / z_q
-  double scale;
-  int never;                               // the refused draft where q is all on it, or -1
-  float best;
-  int at;
-
-  __device__ __forceinline__ void offer(float w, float e, int i) {
-    if (!(w > best * e)) return;           // seldom after the first elements
-    const float r = __fdiv_rn(w, e);
-    if (e > 0.0f && i != never && r > best) best = r, at = i;
-  }
-  // w / E in 64 bits
-  __device__ __forceinline__ double exactly(int i) const {
-    double w = exp(((double)ld_elem(x + i) - (double)mx) * scale);
-    if (y) w -= exp(((double)ld_elem(y + i) - (double)my) * scale) * (double)ratio;
-    return w / (double)clocks[i];
-  }
-};
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) gdn_verify_race_kernel(GdnVerifyArgs a, Plan p) {
+__global__ void __launch_bounds__(kThreads, kDrawCtasPerSm) gdn_verify_draw_rows_kernel(
+    GdnVerifyArgs a, Plan p) {
   using G = Granule<T>;
+  constexpr int kVec = G::kVec;
+  const int lane = threadIdx.x & 31, part = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  pdl_trigger();
+  if (part >= p.parts) return;
+  const Part l = part_at(p, part);
+  int left = l.count, b = (int)((unsigned)l.first / (unsigned)p.granules);
+  int q = l.first - b * p.granules;
+  // the granule ahead: sequence and granule of the next to be loaded
+  int aleft = left, ab = b, aq = q;
+  const T* ax = row_at<T>(a, ab, 0);
+  bool wanted = true;                      // (of the first row: for the first granule)
+  uint4 ahead[2];
+  float clock[2][kVec];
+  auto load = [&](int v) {                 // its v-th vectors
+    if (aleft == 0 || !wanted) return;
+    const long long i = (long long)aq * G::kLogits - shift_of(ax) + (v * 32 + lane) * kVec;
+    const bool inner = aq > 0 && aq + 2 < p.granules;      // all of it the row's
+    if (inner && in_bounds(&g_err_lp, i >= 0 && i + kVec <= a.V)) ahead[v] = load_inner(ax + i);
+    else ahead[v] = edge_vec<true>(ax, i, a.V);
+    const float* e = a.clocks + (long long)ab * a.V + i;
+    if (inner && (reinterpret_cast<uintptr_t>(e) & 15) == 0) {
+#pragma unroll
+      for (int k = 0; k < kVec; k += 4) widen(load_inner(e + k), (const float*)nullptr, clock[v] + k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) clock[v][k] = i + k >= 0 && i + k < a.V ? e[k] : 0.0f;
+    }
+  };
+  auto advance = [&]() {
+    if (aleft == 0 || --aleft == 0) return;
+    if (++aq == p.granules) {
+      aq = 0;
+      ax = row_at<T>(a, ++ab, 0);
+      wanted = takes_part(a.scale ? a.scale[ab] : 1.0f);
+    }
+  };
+  load(0);
+  load(1);
+  advance();
+  wanted = takes_part(a.scale ? a.scale[ab] : 1.0f);
+  while (left > 0) {
+    // ---- this warp's granules of a row
+    const float given = a.scale ? a.scale[b] : 1.0f, scale = scale_of(given), c = scale * kLog2e;
+    const bool read = takes_part(given), races = given != INFINITY;
+    Reference ref;
+    ref.start();
+    const T* x = row_at<T>(a, b, 0);
+    Race<T> race{x, nullptr, a.clocks + (long long)b * a.V, -INFINITY, 0.0f, c, 0.0f, scale, -1,
+                 0.0f, -1};
+    int first = 0;                       // greedy: the first granule that holds the largest
+    unsigned long long z2 = 0;
+    const int q0 = q, q1 = q + left < p.granules ? q + left : p.granules;
+    for (; q < q1; ++q) {
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        float f[kVec], e[kVec], w[kVec];
+        widen(ahead[v], (const T*)nullptr, f);
+        const float top = vector_top(ahead[v], (const T*)nullptr);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) e[k] = clock[v][k];
+        load(v);
+        if (v == 1) advance();
+        if (!read) continue;
+        // one reference for the warp, so that its lanes' races compare
+        if (__any_sync(0xffffffffu, top > ref.m)) {      // seldom after the first granules
+          const float s = ref.raise(warp_max(top > ref.m ? top : ref.m), c);
+          z2 = mul2(z2, pair(s, s));     // (a NaN stays)
+          race.best *= s;
+          race.mx = ref.m;
+          first = q;
+        }
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) w[k] = 0.0f;
+        if (ref.m != -INFINITY || top != top) {
+          ref.terms(f, c, [&](int k, float w0, float w1) {
+            w[k] = w0, w[k + 1] = w1;
+            z2 = add2(z2, pair(w0, w1));
+          });
+        }
+        if (races)
+          race.template offer<kVec, 1>(w, e, q * G::kLogits - shift_of(x) + (v * 32 + lane) * kVec);
+      }
+    }
+    left -= q1 - q0;
+    // ---- what they come to
+    float z0, z1;
+    unpair(z2, &z0, &z1);
+    float z = warp_sum(z0 + z1);
+    if (ref.m != -INFINITY) {
+      const float s = ref.settled(c);
+      z *= s;
+      race.best *= s;
+    }
+    if (lane == 0 && in_bounds(&g_err_lp, b < a.B && part < p.parts))
+      p.stats[(long long)b + part] =
+          races ? make_float4(race.mx, z, __int_as_float(race.at), race.best)
+                : make_float4(race.mx, z, __int_as_float(race.mx == -INFINITY ? q0 : first), 0.0f);
+    if (q == p.granules) q = 0, ++b;
+  }
+}
+
+// The parts of a row on the line: the first, and how many.
+__device__ __forceinline__ Part parts_of(const Plan& p, int row) {
+  const int c0 = part_of(p, row * p.granules);
+  return Part{c0, part_of(p, row * p.granules + p.granules - 1) - c0 + 1};
+}
+
+constexpr int kAheadRace = 2;              // vectors of a thread on the way in the race
+constexpr int kAtOnce = 4;                 // entries of a lane on the way
+// The statistics of a row from its parts' (the whole warp).
+__device__ __forceinline__ Row row_of(const Plan& p, int row, float c) {
+  const Part parts = parts_of(p, row);
+  Row st{-INFINITY, 0.0f, 0x7fffffff};
+  for (int k0 = threadIdx.x & 31; k0 < parts.count; k0 += 32 * kAtOnce) {
+    float4 v[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int at = k0 + 32 * k;
+      const bool some = at < parts.count &&
+                        in_bounds(&g_err_lp, parts.first >= 0 && parts.first + at < p.parts);
+      v[k] = some ? p.stats[(long long)row + parts.first + at]
+                  : make_float4(-INFINITY, 0.0f, __int_as_float(0x7fffffff), 0.0f);
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) st = merge(st, Row{v[k].x, v[k].y, __float_as_int(v[k].z)}, c);
+  }
+  return warp_merge(st, c);
+}
+
+// The first of a granule's logits that equals m (the whole warp).
+template <typename T>
+__device__ __forceinline__ int first_equal(const T* x, int V, int q, float m) {
+  const long long at = (long long)q * Granule<T>::kLogits - shift_of(x);
+  int id = 0x7fffffff;
+#pragma unroll 4
+  for (int e = threadIdx.x & 31; e < Granule<T>::kLogits; e += 32)
+    if (at + e >= 0 && at + e < V && ld_elem(x + at + e) == m) id = min(id, (int)(at + e));
+  return (int)__reduce_min_sync(0xffffffffu, (unsigned)id);
+}
+
+// Without drafts: joins a sequence's parts, a warp a sequence.
+template <typename T>
+__global__ void __launch_bounds__(32) gdn_verify_draw_kernel(GdnVerifyArgs a, Plan p) {
+  const int b = blockIdx.x, lane = threadIdx.x;
+  const float given = a.scale ? a.scale[b] : 1.0f;
+  if (!takes_part(given)) return;
+  const bool greedy = given == INFINITY;
+  const float scale = scale_of(given), c = scale * kLog2e;
+  const T* x = row_at<T>(a, b, 0);
+  pdl_wait();
+  const Row st = row_of(p, b, c);
+  int token = -1;
+  const bool dead = !(st.z > 0.0f);        // 0 or NaN: no distribution
+  if (!dead && greedy) {
+    token = first_equal(x, a.V, st.q, st.m);
+  } else if (!dead) {
+    Race<T> race{x, nullptr, a.clocks + (long long)b * a.V, st.m, 0.0f, c, 0.0f, scale, -1, 0.0f, -1};
+    const Part parts = parts_of(p, b);
+    float r[kAtOnce];
+    int at[kAtOnce];
+    for (int k0 = 0; k0 < parts.count; k0 += 32 * kAtOnce) {
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int entry = k0 + 32 * k + lane;
+        const float4 v = entry < parts.count ? p.stats[(long long)b + parts.first + entry]
+                                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        // to the row's reference
+        r[k] = v.w > 0.0f ? v.w * ptx::ex2_approx((v.x - st.m) * c) : 0.0f;
+        at[k] = __float_as_int(v.z);
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) race.join(r[k], at[k]);
+    }
+    token = race.at;
+  }
+  if (lane > 0 || !in_bounds(&g_err_lp, token < a.V)) return;
+  a.tokens[b] = token;
+  a.accepted[b] = 0;
+  if (a.logprobs)
+    a.logprobs[b] = token >= 0 ? (ld_elem(x + token) - st.m) * scale - kLn2 * log2f(st.z) : 0.0f;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, kRaceCtasPerSm) gdn_verify_race_kernel(GdnVerifyArgs a, Plan p) {
+  using G = Granule<T>;
+  constexpr int kVec = G::kVec;
   __shared__ Row s_row[kMaxRows];
   __shared__ int s_arg[kGdnMaxDrafts + 1];            // greedy: the rows' largest
-  __shared__ int s_refused, s_last;
+  __shared__ int s_refused;
   __shared__ float s_best[kWarps];
   __shared__ int s_at[kWarps];
-  __shared__ int s_winner;
-  const int b = blockIdx.x / p.pieces, piece = blockIdx.x - b * p.pieces;
+  // the last sequences first: their rows were read last
+  const int b = a.B - 1 - blockIdx.x / p.pieces, piece = blockIdx.x % p.pieces;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float given = a.scale ? a.scale[b] : 1.0f;
   if (!takes_part(given)) return;
@@ -258,60 +559,45 @@ __global__ void __launch_bounds__(kThreads) gdn_verify_race_kernel(GdnVerifyArgs
     if (piece == 0 && n < a.T && a.ids[(long long)b * a.T + n] >= a.V)
       atomicOr(&g_err_lp, kErrIndex);
   }
+  // ---- what the decisions need of the inputs
+  const int t = threadIdx.x;
+  int id = -1;
+  float u = 0.0f, xi = 0.0f, yi = 0.0f;
+  if (t < n) {
+    id = a.ids[(long long)b * a.T + t];
+    u = a.accept_u[(long long)b * a.T + t];
+    xi = ld_elem(row_at<T>(a, b, t) + id);
+    if (a.draft) yi = ld_elem(row_at<T>(a, b, a.T + 1 + t) + id);
+  }
   pdl_wait();
   // ---- the rows' statistics, a warp a row
   for (int i = warp; i < n + 1 + (a.draft ? n : 0); i += kWarps) {
     const int j = i <= n ? i : a.T + 1 + i - n - 1;    // row of the sequence
-    const long long row = (long long)b * p.rows + j;
-    const long long x0 = row * p.granules, x1 = x0 + p.granules - 1;
-    const int c0 = (int)(((x0 + 1) * p.parts - 1) / p.total);
-    const int pieces = (int)(((x1 + 1) * p.parts - 1) / p.total) - c0 + 1;
-    Row st{-INFINITY, 0.0f, 0x7fffffff};
-    for (int k = lane; k < pieces; k += 32) {
-      if (!in_bounds(&g_err_lp, c0 >= 0 && c0 + k < kParts)) break;
-      const float4 v = p.stats[row + c0 + k];
-      st = merge(st, Row{v.x, v.y, __float_as_int(v.z)}, c);
-    }
-    st = warp_merge(st, c);
+    const Row st = row_of(p, b * p.rows + j, c);
     if (lane == 0) s_row[j] = st;
-    if (greedy && j <= a.T) {              // the first of the granule's logits that is the largest
-      const T* x = row_at<T>(a, b, j);
-      const long long at = (long long)st.q * G::kLogits - shift_of(x);
-      int id = 0x7fffffff;
-      for (int e = lane; e < G::kLogits; e += 32)
-        if (at + e >= 0 && at + e < a.V && ld_elem(x + at + e) == st.m) id = min(id, (int)(at + e));
-      id = (int)__reduce_min_sync(0xffffffffu, (unsigned)id);
-      if (lane == 0) s_arg[j] = id;
+    if (greedy && j <= a.T) {
+      const int arg = first_equal(row_at<T>(a, b, j), a.V, st.q, st.m);
+      if (lane == 0) s_arg[j] = arg;
     }
   }
   __syncthreads();
   auto dead = [&](int j) { return !(s_row[j].z > 0.0f); };    // 0 or NaN: no distribution
   // ---- the drafts
-  if ((int)threadIdx.x < n) {
-    const int t = threadIdx.x, id = a.ids[(long long)b * a.T + t];
+  if (t < n) {
     bool good = !dead(t);
     if (good && greedy) {
       good = id == s_arg[t];
     } else if (good) {
-      const T* x = row_at<T>(a, b, t);
-      const float u = a.accept_u[(long long)b * a.T + t];
       const Row& px = s_row[t];
-      const float xi = ld_elem(x + id);
       float e = (xi - px.m) * c, size = fabsf(e), z = px.z;
-      double far = ((double)xi - (double)px.m) * (double)scale;
       if (a.draft) {
         const Row& py = s_row[a.T + 1 + t];
-        if (dead(a.T + 1 + t)) {
-          good = false;
-        } else {
-          const float yi = ld_elem(row_at<T>(a, b, a.T + 1 + t) + id);
-          // q = 0: accepted unless p = 0 too
-          const float ey = (yi - py.m) * c;
-          e -= ey;
-          size = fmaxf(size, fabsf(ey));
-          far -= ((double)yi - (double)py.m) * (double)scale;
-          z /= py.z;
-        }
+        // q = 0: accepted unless p = 0 too
+        const float ey = (yi - py.m) * c;
+        e -= ey;
+        size = fmaxf(size, fabsf(ey));
+        z /= py.z;
+        good = !dead(a.T + 1 + t);
       }
       if (good && xi == -INFINITY) {
         good = false;
@@ -319,7 +605,11 @@ __global__ void __launch_bounds__(kThreads) gdn_verify_race_kernel(GdnVerifyArgs
         const float r = ptx::ex2_approx(e) / z;
         good = u < r;
         // near the border, or where the exponents are rounded by much: in 64 bits
-        if (fabsf(u - r) <= r * 0x1p-14f || !(size < 64.0f)) good = (double)u < exp(far) / (double)z;
+        if (fabsf(u - r) <= r * 0x1p-14f || !(size < 64.0f)) {
+          double far = ((double)xi - (double)px.m) * (double)scale;
+          if (a.draft) far -= ((double)yi - (double)s_row[a.T + 1 + t].m) * (double)scale;
+          good = (double)u < exp(far) / (double)z;
+        }
       }
     }
     if (!good) atomicMin(&s_refused, t);
@@ -335,140 +625,140 @@ __global__ void __launch_bounds__(kThreads) gdn_verify_race_kernel(GdnVerifyArgs
     token = hopeless ? -1 : s_arg[accepted];
   } else if (!hopeless) {
     // ---- the race over this CTA's slice
-    Race<T> race;
-    race.x = row_at<T>(a, b, accepted);
-    race.y = refused && a.draft ? row_at<T>(a, b, yj) : nullptr;
-    race.clocks = a.clocks + (long long)b * a.V;
-    race.mx = s_row[accepted].m;
-    race.my = race.y ? s_row[yj].m : 0.0f;
-    race.ratio = race.y ? s_row[accepted].z / s_row[yj].z : 0.0f;
-    race.c = c;
-    race.scale = scale;
-    race.never = refused && !a.draft ? last_draft : -1;
-    race.best = 0.0f;
-    race.at = -1;
+    const T* x = row_at<T>(a, b, accepted);
+    const T* y = refused && a.draft ? row_at<T>(a, b, yj) : nullptr;
+    const float* clocks = a.clocks + (long long)b * a.V;
+    Race<T> race{x, y, clocks, s_row[accepted].m, y ? s_row[yj].m : 0.0f, c,
+                 y ? s_row[accepted].z / s_row[yj].z : 0.0f, scale,
+                 refused && !a.draft ? last_draft : -1, 0.0f, -1};
     const int lo = piece * p.slice, hi = min(a.V, lo + p.slice);
-    auto weight = [&](float x, float y) {
-      float w = ptx::ex2_approx((x - race.mx) * c);
-      if (race.y) w -= ptx::ex2_approx((y - race.my) * c) * race.ratio;
-      return w;
-    };
-    constexpr int kVec = G::kVec;
-    const bool aligned =
-        ((reinterpret_cast<uintptr_t>(race.x) | reinterpret_cast<uintptr_t>(race.clocks) |
-          (race.y ? reinterpret_cast<uintptr_t>(race.y) : 0)) & 15) == 0;
-    if (aligned) {                         // (a slice is a multiple of 16 logits)
-      int i = lo + (int)threadIdx.x * kVec;
-      for (; i + kVec <= hi; i += kThreads * kVec) {
-        if (!in_bounds(&g_err_lp, i >= 0 && i + kVec <= a.V)) break;
-        const uint4 ux = *reinterpret_cast<const uint4*>(race.x + i);
-        const uint4 uy = race.y ? *reinterpret_cast<const uint4*>(race.y + i) : make_uint4(0, 0, 0, 0);
-        float x[kVec], y[kVec], e[kVec];
-#pragma unroll
-        for (int k = 0; k < kVec; k += 4) {
-          const uint4 ue = load_inner(race.clocks + i + k);
-          widen(ue, (const float*)nullptr, e + k);
-        }
-        widen(ux, race.x, x);
-        widen(uy, race.x, y);
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) race.offer(weight(x[k], y[k]), e[k], i + k);
-      }
-      for (; i < hi; ++i)                  // at most one thread's, the row's last logits
-        race.offer(weight(ld_elem(race.x + i), race.y ? ld_elem(race.y + i) : 0.0f), race.clocks[i], i);
-    } else {
-#pragma unroll 4
-      for (int i = lo + (int)threadIdx.x; i < hi; i += kThreads) {
-        if (!in_bounds(&g_err_lp, i >= 0 && i < a.V)) break;
-        race.offer(weight(ld_elem(race.x + i), race.y ? ld_elem(race.y + i) : 0.0f), race.clocks[i], i);
-      }
-    }
-    // ---- the slice's best; of those close to it the best in 64 bits
-    auto block_best = [&](float v, int i) {
-      for (int o = 16; o > 0; o >>= 1) {
-        const float w = __shfl_xor_sync(0xffffffffu, v, o);
-        const int k = __shfl_xor_sync(0xffffffffu, i, o);
-        if (beats(w, k, v, i)) v = w, i = k;
-      }
-      if (lane == 0) s_best[warp] = v, s_at[warp] = i;
-      __syncthreads();
-      v = s_best[0], i = s_at[0];
-#pragma unroll
-      for (int k = 1; k < kWarps; ++k)
-        if (beats(s_best[k], s_at[k], v, i)) v = s_best[k], i = s_at[k];
-      return make_float2(v, __int_as_float(i));
-    };
-    __shared__ double s_value[kThreads];
-    __shared__ int s_index[kThreads];
-    // the best (v, i) of the block's threads; several near it are compared in 64 bits
-    auto settle = [&](float v, int i) {
-      const float2 top = block_best(v, i);
-      const bool near = v > 0.0f && v >= top.x * kClose;
-      if (__syncthreads_count(near) < 2) return top;
-      s_value[threadIdx.x] = near ? race.exactly(i) : -1.0;             // (rare)
-      s_index[threadIdx.x] = i;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        int w = 0;
-        for (int k = 1; k < kThreads; ++k)
-          if (s_value[k] > s_value[w] || (s_value[k] == s_value[w] && s_index[k] < s_index[w])) w = k;
-        s_winner = w;
-      }
-      __syncthreads();
-      const float2 r = make_float2(top.x, __int_as_float(s_index[s_winner]));
-      __syncthreads();
+    auto weight = [&](float v, float w) {
+      float r = ptx::ex2_approx((v - race.mx) * c);
+      if (y) r = fmaf(-race.ratio, ptx::ex2_approx((w - race.my) * c), r);
       return r;
     };
-    const float2 mine = settle(race.best, race.at);
+    const bool aligned = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(clocks) |
+                           (y ? reinterpret_cast<uintptr_t>(y) : 0)) & 15) == 0;
+    if (aligned) {                         // (a slice is a multiple of 16 logits)
+      const int whole = hi & ~(kVec - 1);
+      uint4 ux[kAheadRace], uy[kAheadRace], ue[kAheadRace][kVec / 4];
+      auto fetch = [&](int k, int i) {
+        if (i >= whole || !in_bounds(&g_err_lp, i >= 0 && i + kVec <= a.V)) return;
+        ux[k] = *reinterpret_cast<const uint4*>(x + i);
+        if (y) uy[k] = *reinterpret_cast<const uint4*>(y + i);
+#pragma unroll
+        for (int e = 0; e < kVec / 4; ++e) ue[k][e] = load_inner(clocks + i + 4 * e);
+      };
+      constexpr int kStride = kThreads * kVec;
+      int i = lo + (int)threadIdx.x * kVec;
+#pragma unroll
+      for (int k = 0; k < kAheadRace; ++k) fetch(k, i + k * kStride);
+      for (; i - lane * kVec < whole; i += kAheadRace * kStride) {
+#pragma unroll
+        for (int k = 0; k < kAheadRace; ++k) {
+          const int at = i + k * kStride;
+          float v[kVec], w[kVec], e[kVec];
+          widen(ux[k], x, v);
+          widen(uy[k], x, w);
+#pragma unroll
+          for (int c4 = 0; c4 < kVec / 4; ++c4) widen(ue[k][c4], (const float*)nullptr, e + 4 * c4);
+          fetch(k, at + kAheadRace * kStride);
+#pragma unroll
+          for (int c1 = 0; c1 < kVec; ++c1) {
+            w[c1] = weight(v[c1], w[c1]);
+            if (at >= whole) w[c1] = e[c1] = 0.0f;
+          }
+          race.template offer<kVec, 1>(w, e, at);
+        }
+      }
+      if (warp == 0 && whole < hi) {       // the row's last logits
+        float w[1] = {0.0f}, e[1] = {0.0f};
+        const int i = whole + lane;
+        if (i < hi) w[0] = weight(ld_elem(x + i), y ? ld_elem(y + i) : 0.0f), e[0] = clocks[i];
+        race.template offer<1, 1>(w, e, i);
+      }
+    } else {
+      for (int i0 = lo + warp * 32 * kVec; i0 < hi; i0 += kThreads * kVec) {
+        float v[kVec], w[kVec], e[kVec];
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+          const int i = i0 + 32 * k + lane;
+          const bool in = i < hi && in_bounds(&g_err_lp, i >= 0 && i < a.V);
+          v[k] = in ? ld_elem(x + i) : -INFINITY;
+          w[k] = in && y ? ld_elem(y + i) : -INFINITY;
+          e[k] = in ? clocks[i] : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) w[k] = weight(v[k], w[k]);
+        race.template offer<kVec, 32>(w, e, i0 + lane);
+      }
+    }
+    // ---- the slice's best
+    if (lane == 0) s_best[warp] = race.best, s_at[warp] = race.at;
+    __syncthreads();
+    if (warp > 0) return;
+    race.best = 0.0f, race.at = -1;
+    race.join(lane < kWarps ? s_best[lane] : 0.0f, lane < kWarps ? s_at[lane] : -1);
     // ---- the last CTA of the sequence joins the slices
     if (p.pieces > 1) {
-      if (threadIdx.x == 0) {
-        p.best[(long long)b * p.pieces + piece] = mine;
-        __threadfence();
-        s_last = atomicAdd(&p.done[b], 1) == p.pieces - 1;
+      float2* slices = p.best + (long long)b * p.pieces;
+      int last = 0;
+      if (lane == 0) {
+        __stcg(&slices[piece], make_float2(race.best, __int_as_float(race.at)));
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;\n"
+                     : "=r"(last) : "l"(&p.done[b]) : "memory");
       }
-      __syncthreads();
-      if (!s_last) return;
-      __threadfence();
-      float v = 0.0f;
-      int i = -1;
-      for (int k = threadIdx.x; k < p.pieces; k += kThreads) {
-        const float2 r = __ldcg(&p.best[(long long)b * p.pieces + k]);
-        if (beats(r.x, __float_as_int(r.y), v, i)) v = r.x, i = __float_as_int(r.y);
+      if (__shfl_sync(0xffffffffu, last, 0) != p.pieces - 1) return;
+      __threadfence();                     // (lane 0 acquired for the others)
+      race.best = 0.0f, race.at = -1;
+      for (int k0 = 0; k0 < p.pieces; k0 += 32 * kAtOnce) {
+        float2 r[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const int slice = k0 + 32 * k + lane;
+          r[k] = slice < p.pieces ? __ldcg(&slices[slice]) : make_float2(0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) race.join(r[k].x, __float_as_int(r[k].y));
       }
-      token = __float_as_int(settle(v, i).y);
-    } else {
-      token = __float_as_int(mine.y);
     }
+    token = race.at;
     if (token < 0 && refused) token = last_draft;      // p = q but for rounding
   }
+  if (warp > 0) return;
   // ---- what the sequence gets
-  for (int t = threadIdx.x; t <= a.T; t += kThreads) {
-    const int id = t < accepted ? a.ids[(long long)b * a.T + t] : t == accepted ? token : -1;
-    const long long to = (long long)b * (a.T + 1) + t;
-    if (!in_bounds(&g_err_lp, id < a.V)) continue;
-    a.tokens[to] = id;
+  for (int k = lane; k <= a.T; k += 32) {
+    const int given_id = k < accepted ? a.ids[(long long)b * a.T + k] : k == accepted ? token : -1;
+    const long long to = (long long)b * (a.T + 1) + k;
+    if (!in_bounds(&g_err_lp, given_id < a.V)) continue;
+    a.tokens[to] = given_id;
     if (a.logprobs) {
       float lp = 0.0f;
-      if (id >= 0)
-        lp = (ld_elem(row_at<T>(a, b, t) + id) - s_row[t].m) * scale - kLn2 * log2f(s_row[t].z);
+      if (given_id >= 0)
+        lp = (ld_elem(row_at<T>(a, b, k) + given_id) - s_row[k].m) * scale - kLn2 * log2f(s_row[k].z);
       a.logprobs[to] = lp;
     }
   }
-  if (threadIdx.x == 0) a.accepted[b] = accepted;
+  if (lane == 0) a.accepted[b] = accepted;
 }
 
-constexpr int kRaceCtas = 152 * 4, kLeastSlice = 2048;
+constexpr int kRaceCtas = 152 * kRaceCtasPerSm, kLeastSlice = 2048, kLeastGranules = 4;
 
 Plan plan_of(int B, int T, int V, int bf16, bool draft) {
   Plan p = {};
   p.granules = granules_of(V, bf16);
   p.rows = T + 1 + (draft ? T : 0);
-  p.total = (long long)p.granules * p.rows * B;
-  p.parts = (int)(p.total < kParts ? p.total : kParts);
-  int pieces = (kRaceCtas + B - 1) / B;
-  const int most = (V + kLeastSlice - 1) / kLeastSlice;
-  pieces = pieces < most ? pieces : most;
+  const int total = p.granules * p.rows * B;
+  // a few granules a part: the second pass joins what the parts of a row leave
+  const int most = (total + kLeastGranules - 1) / kLeastGranules;
+  const int warps = 152 * kWarps * (T ? kCtasPerSm : kDrawCtasPerSm);
+  p.parts = most < warps ? most : warps;
+  p.each = total / p.parts;
+  p.more = total % p.parts;
+  // slices: one round of CTAs
+  int pieces = kRaceCtas / B;
+  const int pieces_most = (V + kLeastSlice - 1) / kLeastSlice;
+  pieces = pieces < 1 ? 1 : pieces < pieces_most ? pieces : pieces_most;
   p.slice = ((V + pieces - 1) / pieces + 15) & ~15;
   p.pieces = (V + p.slice - 1) / p.slice;
   return p;
@@ -481,9 +771,13 @@ size_t best_bytes(const Plan& p, int B) { return up(sizeof(float2) * (size_t)p.p
 
 template <typename T>
 cudaError_t launch(const GdnVerifyArgs& a, const Plan& p, cudaStream_t stream) {
-  gdn_verify_rows_kernel<T><<<(p.parts + kWarps - 1) / kWarps, kThreads, 0, stream>>>(a, p);
+  const int grid = (p.parts + kWarps - 1) / kWarps;
+  if (a.T == 0) gdn_verify_draw_rows_kernel<T><<<grid, kThreads, 0, stream>>>(a, p);
+  else gdn_verify_rows_kernel<T><<<grid, kThreads, 0, stream>>>(a, p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  if (a.T == 0)
+    return launch_pdl(true, gdn_verify_draw_kernel<T>, dim3((unsigned)a.B), dim3(32), 0, stream, a, p);
   return launch_pdl(true, gdn_verify_race_kernel<T>, dim3((unsigned)(p.pieces * a.B)),
                     dim3(kThreads), 0, stream, a, p);
 }
