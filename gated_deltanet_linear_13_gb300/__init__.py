@@ -712,6 +712,11 @@ def _kv_cache(k_cache, v_cache, k_exp, v_exp):
             v_exp.is_contiguous()):                  # the usual case at once
         return GdnKvCache(shape[0], shape[2], shape[1], shape[3], GDN_KV_E4M3, k_cache.data_ptr(),
                           v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr()), dev
+    if (dtype is torch.bfloat16 and len(shape) == 4 and k_exp is None and v_exp is None and
+            v_cache.dtype is dtype and v_cache.shape == shape and dev == v_cache.device and
+            dev.type == "cuda" and k_cache.is_contiguous() and v_cache.is_contiguous()):
+        return GdnKvCache(shape[0], shape[2], shape[1], shape[3], GDN_KV_BF16, k_cache.data_ptr(),
+                          v_cache.data_ptr(), None, None), dev
     if dev.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
     if len(shape) != 4:
@@ -922,15 +927,9 @@ def gdn_rope_phase_steps(rotary_dim: int, base: float = 10000.0, *,
     return torch.tensor(signed, dtype=torch.int64, device=device), amplitude.value
 
 
-def _head_strides(t: torch.Tensor, name: str, shape, dtype, device):
+def _head_strides(t: torch.Tensor, name: str, shape):
     """The token and head strides (elements) of t [n, H, D] with dense vectors."""
     n, H, D = shape
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
     token, head, element = t.stride()
     if element != 1 and D > 1:
         raise ValueError(f"{name}: the last dimension must be dense")
@@ -949,65 +948,78 @@ def gdn_qk_norm_rope(q, k, positions, phase_steps, q_out, k_out=None, *, q_weigh
     [rotary_dim / 2] and ``amplitude`` come from gdn_rope_phase_steps; None turns nothing.  With a
     cache (as in gdn_kv_cache_append) the keys and the values v [n, H, D] go to ``slots`` [n], and
     k_out may be None."""
-    L = load_library()
-    dev = q.device
+    L = _lib or load_library()
+    dev, dtype, shape, kshape = q.device, q.dtype, q.shape, k.shape
     if dev.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
-    if q.dim() != 3 or k.dim() != 3:
+    if len(shape) != 3 or len(kshape) != 3:
         raise ValueError("q and k must have 3 dimensions: tokens, heads, elements")
-    dtype = q.dtype
     dt = _dt(q)
-    n, Hq, D = q.shape
-    H = k.shape[1]
-    qs, qh = _head_strides(q, "q", (n, Hq, D), dtype, dev)
-    ks = _token_stride(k, "k", (n, H, D), dtype, dev)
-    qo = _token_stride(q_out, "q_out", (n, Hq, D), dtype, dev)
-    r = 0
+    n, Hq, D = shape
+    H = kshape[1]
+    qs, qh = _head_strides(q, "q", shape)
+    kshape = (n, H, D)
+    ks = _token_stride(k, "k", kshape, dtype, dev)
+    if (q_out.shape == shape and q_out.dtype is dtype and q_out.device == dev and
+            q_out.is_contiguous()):
+        qo = Hq * D
+    else:
+        qo = _token_stride(q_out, "q_out", shape, dtype, dev)
+    r, pp, sp = 0, None, None
     if phase_steps is not None:
         r = 2 * phase_steps.numel()
         _need(phase_steps, "phase_steps", (r // 2,), torch.int64, dev)
         _need(positions, "positions", (n,), torch.int32, dev)
+        if r:
+            pp, sp = positions.data_ptr(), phase_steps.data_ptr()
+    qw = kw = ko = None
     if q_weight is not None:
         _need(q_weight, "q_weight", (D,), torch.float32, dev)
+        qw = q_weight.data_ptr()
     if k_weight is not None:
         _need(k_weight, "k_weight", (D,), torch.float32, dev)
+        kw = k_weight.data_ptr()
     if k_out is not None:
-        _need(k_out, "k_out", (n, H, D), dtype, dev)
-    cache, vp, vs, sp = None, None, 0, None
+        _need(k_out, "k_out", kshape, dtype, dev)
+        ko = k_out.data_ptr()
+    cache, vp, vs, slot = None, None, 0, None
     if k_cache is not None:
         c, cdev = _kv_cache(k_cache, v_cache, k_exp, v_exp)
         if cdev != dev:
             raise ValueError(f"k_cache: on {cdev}, expected {dev}")
         if v is None:
             raise ValueError("v is required")
-        vs = _token_stride(v, "v", (n, H, D), dtype, dev)
+        vs = _token_stride(v, "v", kshape, dtype, dev)
         _need(slots, "slots", (n,), torch.int32, dev)
-        cache, vp, sp = ctypes.byref(c), v.data_ptr(), slots.data_ptr()
-    elif k_out is None:
+        cache, vp, slot = ctypes.byref(c), v.data_ptr(), slots.data_ptr()
+    elif ko is None:
         raise ValueError("k_out or a cache is required")
     elif v is not None or slots is not None or v_cache is not None:
         raise ValueError("v, v_cache and slots go with k_cache")
-    rope = GdnRope(r, GDN_ROPE_INTERLEAVED if interleaved else GDN_ROPE_HALF, amplitude,
-                   phase_steps.data_ptr() if r else None)
-    st = L.gdn_qk_norm_rope(n, Hq, H, D, dt, q.data_ptr(), qs, qh, k.data_ptr(), ks,
-                            _ptr(q_weight), _ptr(k_weight), eps,
-                            positions.data_ptr() if r else None, ctypes.byref(rope),
-                            q_out.data_ptr(), qo, _ptr(k_out), cache, vp, vs, sp,
+    rope = GdnRope(r, GDN_ROPE_INTERLEAVED if interleaved else GDN_ROPE_HALF, amplitude, sp)
+    st = L.gdn_qk_norm_rope(n, Hq, H, D, dt, q.data_ptr(), qs, qh, k.data_ptr(), ks, qw, kw, eps,
+                            pp, ctypes.byref(rope), q_out.data_ptr(), qo, ko, cache, vp, vs, slot,
                             _stream_of(stream, dev))
-    _check(st, "gdn_qk_norm_rope")
+    if st:
+        _check(st, "gdn_qk_norm_rope")
 
 
 def _page_pool(table, held, free_pages, free_count, page_size):
     """(C struct, device) of a pool: table [num_rows, max_pages], held [num_rows], free_pages
     [num_pages], free_count [1], all int32."""
-    dev = table.device
+    dev, i32, tshape, fshape = table.device, torch.int32, table.shape, free_pages.shape
     if dev.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
-    if table.dim() != 2 or free_pages.dim() != 1:
+    if len(tshape) != 2 or len(fshape) != 1:
         raise ValueError("table must have 2 dimensions and free_pages 1")
-    i32 = torch.int32
-    rows, columns = table.shape
-    pages = free_pages.shape[0]
+    rows, columns = tshape
+    pages = fshape[0]
+    if (held.shape == (rows,) and free_count.shape == (1,) and
+            i32 is table.dtype is held.dtype is free_pages.dtype is free_count.dtype and
+            dev == held.device == free_pages.device == free_count.device and
+            table.is_contiguous() and held.is_contiguous() and free_pages.is_contiguous()):
+        return GdnPagePool(pages, page_size, rows, columns, table.data_ptr(), held.data_ptr(),
+                           free_pages.data_ptr(), free_count.data_ptr()), dev
     _need(table, "table", (rows, columns), i32, dev)
     _need(held, "held", (rows,), i32, dev)
     _need(free_pages, "free_pages", (pages,), i32, dev)
@@ -1024,52 +1036,64 @@ def gdn_page_plan(kv_len, new_len, slots=None, positions=None, cu_seqlens=None, 
     [num_rows, max_pages], held [num_rows], free_pages [num_pages], free_count [1]; int32) is
     updated in place; cu_seqlens [B + 1], kv_len_out [B] and the block tables ``pages``
     [B, max_pages] are written where given.  Request b is row rows[b] (or b) of the pool."""
-    L = load_library()
+    L = _lib or load_library()
     p, dev = _page_pool(table, held, free_pages, free_count, page_size)
     i32 = torch.int32
-    B = kv_len.shape[0]
+    shape = kv_len.shape
+    B = shape[0]
     if rows is None and B > p.num_rows:
         raise ValueError("the pool has fewer rows than the batch and no rows given")
-    _need(kv_len, "kv_len", (B,), i32, dev)
-    _need(new_len, "new_len", (B,), i32, dev)
-    capacity = 0
+    if not (len(shape) == 1 and new_len.shape == shape and i32 is kv_len.dtype is new_len.dtype and
+            dev == kv_len.device == new_len.device and kv_len.is_contiguous() and
+            new_len.is_contiguous()):
+        _need(kv_len, "kv_len", (B,), i32, dev)
+        _need(new_len, "new_len", (B,), i32, dev)
+    capacity = 0x7fffffff                            # (nothing to be written a token)
+    sp = pp = rp = cp = op = tp = None
     if slots is not None:
         capacity = slots.shape[0]
         _need(slots, "slots", (capacity,), i32, dev)
+        sp = slots.data_ptr()
     if positions is not None:
-        capacity = capacity if slots is not None else positions.shape[0]
+        if slots is None:
+            capacity = positions.shape[0]
         _need(positions, "positions", (capacity,), i32, dev)
-    if slots is None and positions is None:          # nothing to be written a token
-        capacity = 0x7fffffff
+        pp = positions.data_ptr()
     if rows is not None:
-        _need(rows, "rows", (B,), i32, dev)
+        _need(rows, "rows", shape, i32, dev)
+        rp = rows.data_ptr()
     if cu_seqlens is not None:
         _need(cu_seqlens, "cu_seqlens", (B + 1,), i32, dev)
+        cp = cu_seqlens.data_ptr()
     if kv_len_out is not None:
-        _need(kv_len_out, "kv_len_out", (B,), i32, dev)
+        _need(kv_len_out, "kv_len_out", shape, i32, dev)
+        op = kv_len_out.data_ptr()
     if pages is not None:
         _need(pages, "pages", (B, p.max_pages), i32, dev)
-    st = L.gdn_page_plan(ctypes.byref(p), B, _ptr(rows), kv_len.data_ptr(), new_len.data_ptr(),
-                         capacity, position_offset, _ptr(slots), _ptr(positions),
-                         _ptr(cu_seqlens), _ptr(kv_len_out), _ptr(pages), _stream_of(stream, dev))
-    _check(st, "gdn_page_plan")
+        tp = pages.data_ptr()
+    st = L.gdn_page_plan(ctypes.byref(p), B, rp, kv_len.data_ptr(), new_len.data_ptr(), capacity,
+                         position_offset, sp, pp, cp, op, tp, _stream_of(stream, dev))
+    if st:
+        _check(st, "gdn_page_plan")
 
 
 def gdn_page_release(keep_len, *, table, held, free_pages, free_count, page_size: int, rows=None,
                      stream=None) -> None:
     """Requests keep the pages of their first keep_len [B] tokens and give the others back (see
     gdn_page_release in include/gdn.h); the pool as in gdn_page_plan."""
-    L = load_library()
+    L = _lib or load_library()
     p, dev = _page_pool(table, held, free_pages, free_count, page_size)
     B = keep_len.shape[0]
     if rows is None and B > p.num_rows:
         raise ValueError("the pool has fewer rows than the batch and no rows given")
     _need(keep_len, "keep_len", (B,), torch.int32, dev)
+    rp = None
     if rows is not None:
         _need(rows, "rows", (B,), torch.int32, dev)
-    st = L.gdn_page_release(ctypes.byref(p), B, _ptr(rows), keep_len.data_ptr(),
-                            _stream_of(stream, dev))
-    _check(st, "gdn_page_release")
+        rp = rows.data_ptr()
+    st = L.gdn_page_release(ctypes.byref(p), B, rp, keep_len.data_ptr(), _stream_of(stream, dev))
+    if st:
+        _check(st, "gdn_page_release")
 
 
 def gdn_verify_tokens_workspace_size(batch: int, num_drafts: int, vocab: int,

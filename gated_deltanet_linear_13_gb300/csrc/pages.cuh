@@ -2,10 +2,12 @@
 // lengths on the device.
 //
 // Both calls are a scan over the B requests (tokens and pages that each adds or gives back), a few
-// words a token or table entry behind it, and the new state of the pool.  The scan is a few
-// hundred nanoseconds, so every CTA of one cluster does it for itself and takes its share of the
-// rest; a cluster barrier between the last read of the pool's counts and their update is all the
-// order that is needed, so a call is one launch and keeps nothing between calls.
+// words a token or table entry behind it, and the new state of the pool.  The scan is a microsecond,
+// so every CTA does it for itself and takes its share of the rest.  The pool's counts must not change
+// before the last CTA has read them: the CTAs of one cluster meet at its barrier, which is one
+// launch; a large step writes its outputs with many CTAs and the state in a second launch, set up
+// beside the first.  Nothing is kept between calls.  Bound by latency: a launch (2.2 us), two loads
+// that depend on each other, the barrier and a table entry's load: 3.5 us a call for 64 requests.
 // Part of kv_cache.cu, whose error word it uses.
 #pragma once
 
@@ -18,9 +20,14 @@ using namespace gdn;
 namespace {
 namespace pages {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kMostThreads = 1024, kMostWarps = kMostThreads / 32;
 constexpr int kMaxCtas = 8;                // of the cluster (the portable most)
-constexpr int kColumns = 128;              // of a block table a warp takes at a time
+constexpr int kAtOnce = 4, kColumns = 32 * kAtOnce;   // of a block table a warp takes at a time
+// Words of output up to which one cluster does everything; above, many CTAs write the outputs and a
+// second launch the state (a plan and a release: 20000 tokens 10.3 us in one cluster, 9.2 in two
+// launches; 80000 13.1 / 9.5; 240000 21.9 / 10.7).
+constexpr long long kOneCluster = 16384;
+constexpr int kInRow = 4;                  // tokens of a lane, 32 apart
 
 struct Shared {                            // [B + 1] and [B]
   int* tokens;                             // first packed token of each request, then their number
@@ -50,32 +57,46 @@ __device__ __forceinline__ void cluster_sync() {
                "barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
-// Sums of two numbers over the threads before this one; *totals gets the block's.
+// Two numbers below 2^31 a thread: their sums over the threads before this one (modulo 2^32, right
+// where the totals are below that), and the block's exact totals.
 struct Two {
+  unsigned a, b;
+};
+struct Totals {
   unsigned long long a, b;
 };
-__device__ __forceinline__ Two scan(Two x, Two* totals) {
-  __shared__ Two s_warp[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Two sum = x;
+__device__ __forceinline__ Two scan(Two x, Totals* totals) {
+  struct Warp {
+    unsigned a, b, a_low, a_high, b_low, b_high;
+  };
+  __shared__ Warp s_warp[kMostWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  constexpr unsigned kAll = 0xffffffffu;
+  auto inclusive = [&](Two v) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long a = __shfl_up_sync(0xffffffffu, sum.a, o);
-    const unsigned long long b = __shfl_up_sync(0xffffffffu, sum.b, o);
-    if (lane >= o) sum.a += a, sum.b += b;
-  }
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned a = __shfl_up_sync(kAll, v.a, o), b = __shfl_up_sync(kAll, v.b, o);
+      if (lane >= o) v.a += a, v.b += b;
+    }
+    return v;
+  };
+  const Two sum = inclusive(x);
+  // (in halves, whose sums over 8192 requests stay below 2^32)
+  const Warp mine{0, 0, __reduce_add_sync(kAll, x.a & 0xffffu), __reduce_add_sync(kAll, x.a >> 16),
+                  __reduce_add_sync(kAll, x.b & 0xffffu), __reduce_add_sync(kAll, x.b >> 16)};
   __syncthreads();                         // (the warps' sums of the scan before are read)
-  if (lane == 31) s_warp[warp] = sum;
-  __syncthreads();
-  Two before{0, 0}, all{0, 0};
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const Two t = s_warp[w];
-    if (w < warp) before.a += t.a, before.b += t.b;
-    all.a += t.a, all.b += t.b;
+  if (lane == 31) {
+    s_warp[warp] = mine;
+    s_warp[warp].a = sum.a, s_warp[warp].b = sum.b;
   }
-  *totals = all;
-  return Two{before.a + sum.a - x.a, before.b + sum.b - x.b};
+  __syncthreads();
+  const Warp w = lane < warps ? s_warp[lane] : Warp{0, 0, 0, 0, 0, 0};
+  const Two all = inclusive(Two{w.a, w.b});
+  const unsigned a0 = __shfl_sync(kAll, all.a, warp > 0 ? warp - 1 : 0);
+  const unsigned b0 = __shfl_sync(kAll, all.b, warp > 0 ? warp - 1 : 0);
+  totals->a = ((unsigned long long)__reduce_add_sync(kAll, w.a_high) << 16) + __reduce_add_sync(kAll, w.a_low);
+  totals->b = ((unsigned long long)__reduce_add_sync(kAll, w.b_high) << 16) + __reduce_add_sync(kAll, w.b_low);
+  return Two{(warp > 0 ? a0 : 0) + sum.a - x.a, (warp > 0 ? b0 : 0) + sum.b - x.b};
 }
 
 // What request b adds (tokens, pages) or gives back (pages); false: out of range.
@@ -97,27 +118,28 @@ __device__ __forceinline__ bool request(const GdnPoolArgs& p, const GdnPlanArgs&
   if (a.more) {                            // a plan
     if (pages > p.max_pages) return false;
     s.from[b] = len;
-    *out = Two{(unsigned long long)more, pages > held ? (unsigned long long)(pages - held) : 0};
+    *out = Two{(unsigned)more, pages > held ? (unsigned)(pages - held) : 0u};
   } else {
     s.from[b] = (int)(pages < held ? pages : held);
-    *out = Two{0, (unsigned long long)(held - s.from[b])};
+    *out = Two{0, (unsigned)(held - s.from[b])};
   }
   return true;
 }
 
 // Fills s; false (in every thread): some request is out of range.
 __device__ __forceinline__ bool scan_requests(const GdnPoolArgs& p, const GdnPlanArgs& a,
-                                              const Shared& s, Two* totals) {
-  Two sum{0, 0};
+                                              const Shared& s, Totals* totals) {
+  Totals sum{0, 0};
   bool good = true;
-  for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+  for (int b0 = 0; b0 < a.B; b0 += blockDim.x) {
     const int b = b0 + threadIdx.x;
-    Two x{0, 0}, block;
+    Two x{0, 0};
+    Totals block;
     if (b < a.B) good = request(p, a, b, s, &x) && good;
     const Two before = scan(x, &block);
     if (b < a.B) {
-      s.tokens[b] = (int)(sum.a + before.a);
-      s.pages[b] = (int)(sum.b + before.b);
+      s.tokens[b] = (int)((unsigned)sum.a + before.a);
+      s.pages[b] = (int)((unsigned)sum.b + before.b);
     }
     sum.a += block.a;
     sum.b += block.b;
@@ -141,28 +163,9 @@ __device__ __forceinline__ int request_of(const Shared& s, int B, int t) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(GdnPoolArgs p, GdnPlanArgs a) {
-  extern __shared__ int smem[];
-  const Shared s = carve(smem, a.B);
-  const int rank = cluster_rank(), ctas = cluster_size();
-  const int tid = rank * kThreads + threadIdx.x, threads = ctas * kThreads;
-  const int count = *p.free_count, fill = a.slots || a.positions ? a.capacity : 0;
-  Two totals;
-  bool good = scan_requests(p, a, s, &totals);
-  good = good && count >= 0 && count <= p.num_pages && totals.a <= (unsigned long long)a.capacity &&
-         totals.b <= (unsigned long long)count;
-  cluster_sync();                          // every CTA has read the pool's state and the lengths
-  if (!good) {                             // nothing is given
-    if (tid == 0) atomicOr(&g_err_kv, kErrIndex);
-    for (int t = tid; t < fill; t += threads) {
-      if (a.slots) a.slots[t] = -1;
-      if (a.positions) a.positions[t] = 0;
-    }
-    if (a.cu_seqlens)
-      for (int b = tid; b <= a.B; b += threads) a.cu_seqlens[b] = 0;
-    return;
-  }
-  // ---- the requests' new state
+// The pool's and the requests' state after a plan.
+__device__ __forceinline__ void write_state(const GdnPoolArgs& p, const GdnPlanArgs& a,
+                                            const Shared& s, int left, int tid, int threads) {
   for (int b = tid; b < a.B; b += threads) {
     const int row = s.row[b], need = s.pages[b + 1] - s.pages[b];
     if (need > 0 && in_bounds(&g_err_kv, row >= 0 && row < p.num_rows))
@@ -172,9 +175,45 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(GdnPoolArgs p, 
   }
   if (a.cu_seqlens)
     for (int b = tid; b <= a.B; b += threads) a.cu_seqlens[b] = s.tokens[b];
-  if (tid == 0) *p.free_count = count - (int)totals.b;
+  if (tid == 0) *p.free_count = left;
+}
+
+// What a launch of the plan does: all of it (one cluster), or its two halves, the outputs by many
+// CTAs, then the pool's new state by one, which reads everything before it waits for the other.
+enum { kAll = 0, kOutputs = 1, kState = 2 };
+
+template <int kPart>
+__global__ void __launch_bounds__(kMostThreads) gdn_page_plan_kernel(GdnPoolArgs p, GdnPlanArgs a) {
+  extern __shared__ int smem[];
+  const Shared s = carve(smem, a.B);
+  const int rank = kPart == kAll ? cluster_rank() : blockIdx.x;
+  const int ctas = kPart == kAll ? cluster_size() : gridDim.x;
+  const int tid = rank * blockDim.x + threadIdx.x, threads = ctas * blockDim.x;
+  if (kPart == kOutputs) pdl_trigger();
+  const int count = *p.free_count, fill = a.slots || a.positions ? a.capacity : 0;
+  Totals totals;
+  bool good = scan_requests(p, a, s, &totals);
+  good = good && count >= 0 && count <= p.num_pages && totals.a <= (unsigned long long)a.capacity &&
+         totals.b <= (unsigned long long)count;
+  // every CTA has read the pool's state and the lengths before they change
+  if (kPart == kAll) cluster_sync();
+  if (kPart == kState) pdl_wait();
+  if (!good) {                             // nothing is given
+    if (kPart != kOutputs && tid == 0) atomicOr(&g_err_kv, kErrIndex);
+    if (kPart != kState)
+      for (int t = tid; t < fill; t += threads) {
+        if (a.slots) a.slots[t] = -1;
+        if (a.positions) a.positions[t] = 0;
+      }
+    if (kPart != kOutputs && a.cu_seqlens)
+      for (int b = tid; b <= a.B; b += threads) a.cu_seqlens[b] = 0;
+    return;
+  }
+  // ---- the requests' new state
+  if (kPart != kOutputs) write_state(p, a, s, count - (int)totals.b, tid, threads);
+  if (kPart == kState) return;
   // ---- block tables: a warp kColumns of a request's pages at a time
-  const int lane = threadIdx.x & 31, warps = ctas * kWarps;
+  const int lane = threadIdx.x & 31, warps = threads >> 5;
   const int pieces = (p.max_pages + kColumns - 1) / kColumns;
   for (long long w = tid >> 5; w < (long long)a.B * pieces; w += warps) {
     const int b = (int)(w / pieces), c0 = (int)(w - (long long)b * pieces) * kColumns;
@@ -183,43 +222,64 @@ __global__ void __launch_bounds__(kThreads) gdn_page_plan_kernel(GdnPoolArgs p, 
     if (row < 0) continue;
     int* table = p.table + (long long)row * p.max_pages;
     int* pages = a.pages ? a.pages + (long long)b * p.max_pages : nullptr;
-    for (int c = (pages ? c0 : max(c0, held)) + lane; c < end; c += 32) {
-      if (!in_bounds(&g_err_kv, c >= 0 && c < p.max_pages)) break;
-      const bool fresh = c >= held;
-      const int page = fresh ? p.free_pages[count - 1 - (first + c - held)] : table[c];
-      if (fresh) table[c] = page;
-      if (pages) pages[c] = page;
+    int page[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int c = c0 + k * 32 + lane;
+      page[k] = 0;
+      if (c < end && (pages || c >= held) && in_bounds(&g_err_kv, c >= 0 && c < p.max_pages))
+        page[k] = c >= held ? p.free_pages[count - 1 - (first + c - held)] : table[c];
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int c = c0 + k * 32 + lane;
+      if (c >= end || !in_bounds(&g_err_kv, c >= 0 && c < p.max_pages)) continue;
+      if (c >= held) table[c] = page[k];
+      if (pages) pages[c] = page[k];
     }
   }
-  // ---- the tokens
+  // ---- the tokens, a warp kInRow times 32 in a row (a lane looks its request up once, as long as
+  // its next token belongs to it too)
   const int total = (int)totals.a, mask = (1 << p.page_shift) - 1;
-  for (int t = tid; t < fill; t += threads) {
-    int slot = -1, position = 0;
-    if (t < total) {
-      const int b = request_of(s, a.B, t), at = s.from[b] + t - s.tokens[b];
-      position = a.offset + at;
-      if (a.slots) {
-        const int c = at >> p.page_shift, held = s.held[b], row = s.row[b];
-        int page = -1;
-        if (in_bounds(&g_err_kv, row >= 0 && c < p.max_pages))
-          page = c < held ? p.table[(long long)row * p.max_pages + c]
-                          : p.free_pages[count - 1 - (s.pages[b] + c - held)];
-        if (page >= 0 && page < p.num_pages) slot = (page << p.page_shift) + (at & mask);
-        else atomicOr(&g_err_kv, kErrIndex);
+  for (long long t1 = (long long)(tid >> 5) * (32 * kInRow); t1 < fill; t1 += (long long)warps * (32 * kInRow)) {
+    const int* table = nullptr;            // of the lane's request
+    const int* fresh = nullptr;            // its new pages, from the end
+    int until = 0, back = 0, held = 0;     // where its tokens end, and what is taken off a packed token
+    int at[kInRow], page[kInRow];
+#pragma unroll
+    for (int k = 0; k < kInRow; ++k) {
+      const long long t = t1 + k * 32 + lane;
+      page[k] = at[k] = -1;
+      if (t >= total) continue;
+      if (t >= until) {
+        const int b = request_of(s, a.B, (int)t), row = s.row[b];
+        until = s.tokens[b + 1], back = s.tokens[b] - s.from[b], held = s.held[b];
+        table = p.table + (long long)row * p.max_pages;
+        fresh = p.free_pages + (count - 1 - s.pages[b] + held);
       }
+      at[k] = (int)t - back;
+      const int c = at[k] >> p.page_shift;
+      if (a.slots && in_bounds(&g_err_kv, c >= 0 && c < p.max_pages)) page[k] = c < held ? table[c] : fresh[-c];
     }
-    if (a.slots) a.slots[t] = slot;
-    if (a.positions) a.positions[t] = position;
+#pragma unroll
+    for (int k = 0; k < kInRow; ++k) {
+      const long long t = t1 + k * 32 + lane;
+      if (t >= fill) continue;
+      const bool some = page[k] >= 0 && page[k] < p.num_pages;
+      if (a.slots && t < total && !some) atomicOr(&g_err_kv, kErrIndex);
+      if (a.slots) a.slots[t] = some ? (page[k] << p.page_shift) + (at[k] & mask) : -1;
+      if (a.positions) a.positions[t] = at[k] >= 0 ? a.offset + at[k] : 0;
+    }
   }
 }
 
-__global__ void __launch_bounds__(kThreads) gdn_page_release_kernel(GdnPoolArgs p, GdnPlanArgs a) {
+__global__ void __launch_bounds__(kMostThreads) gdn_page_release_kernel(GdnPoolArgs p, GdnPlanArgs a) {
   extern __shared__ int smem[];
   const Shared s = carve(smem, a.B);
   const int rank = cluster_rank(), ctas = cluster_size();
-  const int tid = rank * kThreads + threadIdx.x, threads = ctas * kThreads;
+  const int tid = rank * blockDim.x + threadIdx.x, threads = ctas * blockDim.x;
   const int count = *p.free_count;
-  Two totals;
+  Totals totals;
   bool good = scan_requests(p, a, s, &totals);
   good = good && count >= 0 && totals.b + (unsigned long long)count <= (unsigned long long)p.num_pages;
   cluster_sync();
@@ -233,28 +293,35 @@ __global__ void __launch_bounds__(kThreads) gdn_page_release_kernel(GdnPoolArgs 
         in_bounds(&g_err_kv, s.row[b] >= 0 && s.row[b] < p.num_rows))
       p.held[s.row[b]] = s.from[b];
   if (tid == 0) *p.free_count = end;
-  const int lane = threadIdx.x & 31, warps = ctas * kWarps;
+  const int lane = threadIdx.x & 31, warps = threads >> 5;
   const int pieces = (p.max_pages + kColumns - 1) / kColumns;
   for (long long w = tid >> 5; w < (long long)a.B * pieces; w += warps) {
     const int b = (int)(w / pieces), c0 = (int)(w - (long long)b * pieces) * kColumns;
     const int first = s.pages[b], given = s.pages[b + 1] - first, kept = s.from[b];
     if (given == 0) continue;
     const int* table = p.table + (long long)s.row[b] * p.max_pages + kept;
-    for (int c = c0 + lane; c < min(c0 + kColumns, given); c += 32) {
-      const int to = end - 1 - (first + c);
-      if (in_bounds(&g_err_kv, to >= count && to < p.num_pages && kept + c < p.max_pages))
-        p.free_pages[to] = table[c];
+    int page[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int c = c0 + k * 32 + lane;
+      page[k] = c < given && in_bounds(&g_err_kv, kept + c < p.max_pages) ? table[c] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int c = c0 + k * 32 + lane, to = end - 1 - (first + c);
+      if (c < given && in_bounds(&g_err_kv, to >= count && to < p.num_pages)) p.free_pages[to] = page[k];
     }
   }
 }
 
-// CTAs of the cluster for `words` of output: one CTA's threads take a few words each before
-// another CTA is worth its place.
+// The cluster for `words` of output: first more CTAs, then more threads, so that each thread has a
+// few words.
 template <typename K>
 cudaError_t launch(K kernel, const GdnPoolArgs& p, const GdnPlanArgs& a, long long words,
                    unsigned* done, cudaStream_t stream) {
-  int ctas = 1;
-  while (ctas < kMaxCtas && words > (long long)ctas * kThreads * 2) ctas *= 2;
+  int threads = 256, ctas = 1;
+  while (ctas < kMaxCtas && words > (long long)ctas * threads * 2) ctas *= 2;
+  while (threads < kMostThreads && words > (long long)ctas * threads * 4) threads *= 2;
   const size_t smem = shared_bytes(a.B);
   if (smem > 48 * 1024) {
     const cudaError_t e = set_smem_once(kernel, (int)shared_bytes(kGdnMaxRequests), done);
@@ -262,7 +329,7 @@ cudaError_t launch(K kernel, const GdnPoolArgs& p, const GdnPlanArgs& a, long lo
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -278,10 +345,24 @@ cudaError_t launch(K kernel, const GdnPoolArgs& p, const GdnPlanArgs& a, long lo
 }  // namespace
 
 cudaError_t gdn_launch_page_plan(const GdnPoolArgs& p, const GdnPlanArgs& a, cudaStream_t stream) {
-  static unsigned done = 0;
+  static unsigned done[3] = {};
   const long long fill = a.slots || a.positions ? a.capacity : 0;
-  const long long tables = (long long)a.B * p.max_pages;
-  return pages::launch(pages::gdn_page_plan_kernel, p, a, std::max(fill, tables), &done, stream);
+  const long long words = std::max(fill, (long long)a.B * p.max_pages);
+  if (words <= pages::kOneCluster)
+    return pages::launch(pages::gdn_page_plan_kernel<pages::kAll>, p, a, words, &done[0], stream);
+  const size_t smem = pages::shared_bytes(a.B);
+  if (smem > 48 * 1024) {
+    const int most = (int)pages::shared_bytes(kGdnMaxRequests);
+    cudaError_t e = set_smem_once(pages::gdn_page_plan_kernel<pages::kOutputs>, most, &done[1]);
+    if (e == cudaSuccess) e = set_smem_once(pages::gdn_page_plan_kernel<pages::kState>, most, &done[2]);
+    if (e != cudaSuccess) return e;
+  }
+  const unsigned ctas = (unsigned)std::min(152ll, (words + 2047) / 2048);
+  pages::gdn_page_plan_kernel<pages::kOutputs><<<ctas, 512, smem, stream>>>(p, a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_pdl(true, pages::gdn_page_plan_kernel<pages::kState>, dim3(1), dim3(512), smem, stream,
+                    p, a);
 }
 
 cudaError_t gdn_launch_page_release(const GdnPoolArgs& p, const GdnPlanArgs& a,
