@@ -33,7 +33,10 @@ namespace {
 namespace verify {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 3, kDrawCtasPerSm = 2, kRaceCtasPerSm = 3;
+constexpr int kCtasPerSm = 3, kRaceCtasPerSm = 3;
+// of the pass that also draws: 128 rows of 151936 in bf16 26.8 us (three: registers spill, 39.9); 64 of
+// 151936 in fp32 20.6 us with two, 19.2 with three
+constexpr int draw_ctas(bool bf16) { return bf16 ? 2 : 3; }
 constexpr int kMaxRows = 2 * kGdnMaxDrafts + 1;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMost = 18446744073709551616.0f;       // 2^64: scales lie within it and its inverse
@@ -222,22 +225,31 @@ struct Race {
       challenge(__shfl_sync(0xffffffffu, r, from), __shfl_sync(0xffffffffu, i, from));
     }
   }
-  // N elements of each lane, the k-th of index i0 + k kStep
-  template <int N, int kStep>
-  __device__ __forceinline__ void offer(const float (&w)[N], const float (&e)[N], int i0) {
+  // N elements of each lane, the k-th of index at(k)
+  template <int N, typename At>
+  __device__ __forceinline__ void offer(const float (&w)[N], const float (&e)[N], At&& at_of) {
     const float floor = best * kClose;
     float over = 0.0f;                     // (a NaN or an infinite clock stays below)
+    if constexpr (N % 2 == 0) {
+      const unsigned long long minus = pair(-floor, -floor);
 #pragma unroll
-    for (int k = 0; k < N; ++k) over = fmaxf(over, fmaf(-floor, e[k], w[k]));
+      for (int k = 0; k < N; k += 2) {
+        float o0, o1;
+        unpair(fma2(pair(e[k], e[k + 1]), minus, pair(w[k], w[k + 1])), &o0, &o1);
+        over = fmaxf(over, fmaxf(o0, o1));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k) over = fmaxf(over, fmaf(-floor, e[k], w[k]));
+    }
     if (!__any_sync(0xffffffffu, over > 0.0f)) return;
     float r = 0.0f;
     int at_k = 0;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const int i = i0 + k * kStep;
-      if (!(e[k] > 0.0f && w[k] > 0.0f && w[k] > floor * e[k] && i != never)) continue;
+      if (!(e[k] > 0.0f && w[k] > 0.0f && w[k] > floor * e[k] && at_of(k) != never)) continue;
       const float q = __fdiv_rn(w[k], e[k]);
-      if (q > r) r = q, at_k = i;
+      if (q > r) r = q, at_k = at_of(k);
     }
     if (__any_sync(0xffffffffu, r > 0.0f)) join(r, at_k);
   }
@@ -351,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gdn_verify_rows_kernel(G
 
 // Without drafts: the rows' statistics, and the race of each, in one pass.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, kDrawCtasPerSm) gdn_verify_draw_rows_kernel(
+__global__ void __launch_bounds__(kThreads, draw_ctas(sizeof(T) == 2)) gdn_verify_draw_rows_kernel(
     GdnVerifyArgs a, Plan p) {
   using G = Granule<T>;
   constexpr int kVec = G::kVec;
@@ -407,34 +419,36 @@ __global__ void __launch_bounds__(kThreads, kDrawCtasPerSm) gdn_verify_draw_rows
     unsigned long long z2 = 0;
     const int q0 = q, q1 = q + left < p.granules ? q + left : p.granules;
     for (; q < q1; ++q) {
+      float f[G::kPer], e[G::kPer], w[G::kPer], top, least;
+      widen(ahead[0], (const T*)nullptr, f);
+      widen(ahead[1], (const T*)nullptr, f + kVec);
+      range(ahead[0], ahead[1], (const T*)nullptr, f, &top, &least);
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        float f[kVec], e[kVec], w[kVec];
-        widen(ahead[v], (const T*)nullptr, f);
-        const float top = vector_top(ahead[v], (const T*)nullptr);
+      for (int k = 0; k < G::kPer; ++k) e[k] = clock[k / kVec][k % kVec];
+      load(0);
+      load(1);
+      advance();
+      if (!read) continue;
+      // one reference for the warp, so that its lanes' races compare
+      if (__any_sync(0xffffffffu, top > ref.m)) {        // seldom after the first granules
+        const float s = ref.raise(warp_max(top > ref.m ? top : ref.m), c);
+        z2 = mul2(z2, pair(s, s));         // (a NaN stays)
+        race.best *= s;
+        race.mx = ref.m;
+        first = q;
+      }
+      if (ref.m == -INFINITY && !(top != top)) {
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) e[k] = clock[v][k];
-        load(v);
-        if (v == 1) advance();
-        if (!read) continue;
-        // one reference for the warp, so that its lanes' races compare
-        if (__any_sync(0xffffffffu, top > ref.m)) {      // seldom after the first granules
-          const float s = ref.raise(warp_max(top > ref.m ? top : ref.m), c);
-          z2 = mul2(z2, pair(s, s));     // (a NaN stays)
-          race.best *= s;
-          race.mx = ref.m;
-          first = q;
-        }
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) w[k] = 0.0f;
-        if (ref.m != -INFINITY || top != top) {
-          ref.terms(f, c, [&](int k, float w0, float w1) {
-            w[k] = w0, w[k + 1] = w1;
-            z2 = add2(z2, pair(w0, w1));
-          });
-        }
-        if (races)
-          race.template offer<kVec, 1>(w, e, q * G::kLogits - shift_of(x) + (v * 32 + lane) * kVec);
+        for (int k = 0; k < G::kPer; ++k) w[k] = 0.0f;
+      } else {
+        ref.terms(f, c, [&](int k, float w0, float w1) {
+          w[k] = w0, w[k + 1] = w1;
+          z2 = add2(z2, pair(w0, w1));
+        });
+      }
+      if (races) {
+        const int i0 = q * G::kLogits - shift_of(x) + lane * kVec;
+        race.offer(w, e, [&](int k) { return i0 + k / kVec * 32 * kVec + k % kVec; });
       }
     }
     left -= q1 - q0;
@@ -463,23 +477,30 @@ __device__ __forceinline__ Part parts_of(const Plan& p, int row) {
 
 constexpr int kAheadRace = 2;              // vectors of a thread on the way in the race
 constexpr int kAtOnce = 4;                 // entries of a lane on the way
-// The statistics of a row from its parts' (the whole warp).
-__device__ __forceinline__ Row row_of(const Plan& p, int row, float c) {
-  const Part parts = parts_of(p, row);
-  Row st{-INFINITY, 0.0f, 0x7fffffff};
-  for (int k0 = threadIdx.x & 31; k0 < parts.count; k0 += 32 * kAtOnce) {
-    float4 v[kAtOnce];
+// Entries k0 + lane, + 32, ... of the parts of a row (none: as of no logits).
+__device__ __forceinline__ void entries_of(const Plan& p, int row, const Part& parts, int k0,
+                                           float4 (&v)[kAtOnce]) {
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      const int at = k0 + 32 * k;
-      const bool some = at < parts.count &&
-                        in_bounds(&g_err_lp, parts.first >= 0 && parts.first + at < p.parts);
-      v[k] = some ? p.stats[(long long)row + parts.first + at]
-                  : make_float4(-INFINITY, 0.0f, __int_as_float(0x7fffffff), 0.0f);
-    }
+  for (int k = 0; k < kAtOnce; ++k) {
+    const int at = k0 + 32 * k + (threadIdx.x & 31);
+    const bool some = at < parts.count &&
+                      in_bounds(&g_err_lp, parts.first >= 0 && parts.first + at < p.parts);
+    v[k] = some ? p.stats[(long long)row + parts.first + at]
+                : make_float4(-INFINITY, 0.0f, __int_as_float(0x7fffffff), 0.0f);
+  }
+}
+// The statistics of a row from its parts' (the whole warp); v keeps the first entries.
+__device__ __forceinline__ Row row_of(const Plan& p, int row, const Part& parts, float c,
+                                      float4 (&v)[kAtOnce]) {
+  Row st{-INFINITY, 0.0f, 0x7fffffff};
+  for (int k0 = 32 * kAtOnce; k0 < parts.count; k0 += 32 * kAtOnce) {
+    entries_of(p, row, parts, k0, v);
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) st = merge(st, Row{v[k].x, v[k].y, __float_as_int(v[k].z)}, c);
   }
+  entries_of(p, row, parts, 0, v);
+#pragma unroll
+  for (int k = 0; k < kAtOnce; ++k) st = merge(st, Row{v[k].x, v[k].y, __float_as_int(v[k].z)}, c);
   return warp_merge(st, c);
 }
 
@@ -503,29 +524,22 @@ __global__ void __launch_bounds__(32) gdn_verify_draw_kernel(GdnVerifyArgs a, Pl
   const bool greedy = given == INFINITY;
   const float scale = scale_of(given), c = scale * kLog2e;
   const T* x = row_at<T>(a, b, 0);
+  const Part parts = parts_of(p, b);
+  float4 v[kAtOnce];
   pdl_wait();
-  const Row st = row_of(p, b, c);
+  const Row st = row_of(p, b, parts, c, v);
   int token = -1;
   const bool dead = !(st.z > 0.0f);        // 0 or NaN: no distribution
   if (!dead && greedy) {
     token = first_equal(x, a.V, st.q, st.m);
   } else if (!dead) {
     Race<T> race{x, nullptr, a.clocks + (long long)b * a.V, st.m, 0.0f, c, 0.0f, scale, -1, 0.0f, -1};
-    const Part parts = parts_of(p, b);
-    float r[kAtOnce];
-    int at[kAtOnce];
     for (int k0 = 0; k0 < parts.count; k0 += 32 * kAtOnce) {
+      if (k0 > 0) entries_of(p, b, parts, k0, v);
 #pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const int entry = k0 + 32 * k + lane;
-        const float4 v = entry < parts.count ? p.stats[(long long)b + parts.first + entry]
-                                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        // to the row's reference
-        r[k] = v.w > 0.0f ? v.w * ptx::ex2_approx((v.x - st.m) * c) : 0.0f;
-        at[k] = __float_as_int(v.z);
-      }
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) race.join(r[k], at[k]);
+      for (int k = 0; k < kAtOnce; ++k)    // to the row's reference
+        race.join(v[k].w > 0.0f ? v[k].w * ptx::ex2_approx((v[k].x - st.m) * c) : 0.0f,
+                  __float_as_int(v[k].z));
     }
     token = race.at;
   }
@@ -573,7 +587,9 @@ __global__ void __launch_bounds__(kThreads, kRaceCtasPerSm) gdn_verify_race_kern
   // ---- the rows' statistics, a warp a row
   for (int i = warp; i < n + 1 + (a.draft ? n : 0); i += kWarps) {
     const int j = i <= n ? i : a.T + 1 + i - n - 1;    // row of the sequence
-    const Row st = row_of(p, b * p.rows + j, c);
+    float4 v[kAtOnce];
+    const int row = b * p.rows + j;
+    const Row st = row_of(p, row, parts_of(p, row), c, v);
     if (lane == 0) s_row[j] = st;
     if (greedy && j <= a.T) {
       const int arg = first_equal(row_at<T>(a, b, j), a.V, st.q, st.m);
@@ -668,20 +684,21 @@ __global__ void __launch_bounds__(kThreads, kRaceCtasPerSm) gdn_verify_race_kern
             w[c1] = weight(v[c1], w[c1]);
             if (at >= whole) w[c1] = e[c1] = 0.0f;
           }
-          race.template offer<kVec, 1>(w, e, at);
+          race.offer(w, e, [&](int k1) { return at + k1; });
         }
       }
       if (warp == 0 && whole < hi) {       // the row's last logits
         float w[1] = {0.0f}, e[1] = {0.0f};
         const int i = whole + lane;
         if (i < hi) w[0] = weight(ld_elem(x + i), y ? ld_elem(y + i) : 0.0f), e[0] = clocks[i];
-        race.template offer<1, 1>(w, e, i);
+        race.offer(w, e, [&](int) { return i; });
       }
     } else {
-      for (int i0 = lo + warp * 32 * kVec; i0 < hi; i0 += kThreads * kVec) {
-        float v[kVec], w[kVec], e[kVec];
+      constexpr int kN = 8;                // elements of a lane at a time, 32 apart
+      for (int i0 = lo + warp * 32 * kN; i0 < hi; i0 += kThreads * kN) {
+        float v[kN], w[kN], e[kN];
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) {
+        for (int k = 0; k < kN; ++k) {
           const int i = i0 + 32 * k + lane;
           const bool in = i < hi && in_bounds(&g_err_lp, i >= 0 && i < a.V);
           v[k] = in ? ld_elem(x + i) : -INFINITY;
@@ -689,8 +706,8 @@ __global__ void __launch_bounds__(kThreads, kRaceCtasPerSm) gdn_verify_race_kern
           e[k] = in ? clocks[i] : 0.0f;
         }
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) w[k] = weight(v[k], w[k]);
-        race.template offer<kVec, 32>(w, e, i0 + lane);
+        for (int k = 0; k < kN; ++k) w[k] = weight(v[k], w[k]);
+        race.offer(w, e, [&](int k) { return i0 + lane + 32 * k; });
       }
     }
     // ---- the slice's best
@@ -751,7 +768,7 @@ Plan plan_of(int B, int T, int V, int bf16, bool draft) {
   const int total = p.granules * p.rows * B;
   // a few granules a part: the second pass joins what the parts of a row leave
   const int most = (total + kLeastGranules - 1) / kLeastGranules;
-  const int warps = 152 * kWarps * (T ? kCtasPerSm : kDrawCtasPerSm);
+  const int warps = 152 * kWarps * (T ? kCtasPerSm : draw_ctas(bf16));
   p.parts = most < warps ? most : warps;
   p.each = total / p.parts;
   p.more = total % p.parts;
