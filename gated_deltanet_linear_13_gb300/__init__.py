@@ -179,8 +179,22 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.gdn_status_string.argtypes = [ctypes.c_int]
     L.gdn_version.restype = ctypes.c_int32
     L.gdn_version.argtypes = []
+    _bind_marshal(L)
     _lib = L
     return L
+
+
+_native = None
+
+
+def _bind_marshal(L: ctypes.CDLL) -> None:
+    """The binding's native part (csrc/marshal.cpp), on the functions of this library."""
+    global _native
+    from . import _marshal as m
+    m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+             (L.gdn_qk_norm_rope, L.gdn_page_plan, L.gdn_page_release, L.gdn_verify_tokens)),
+           getattr(torch._C, "_cuda_getCurrentRawStream", None))
+    _native = m
 
 
 # ---------------------------------------------------------------- marshalling helpers
@@ -949,6 +963,12 @@ def gdn_qk_norm_rope(q, k, positions, phase_steps, q_out, k_out=None, *, q_weigh
     cache (as in gdn_kv_cache_append) the keys and the values v [n, H, D] go to ``slots`` [n], and
     k_out may be None."""
     L = _lib or load_library()
+    st = _native.qk_norm_rope(q, k, positions, phase_steps, q_out, k_out, q_weight, k_weight, eps,
+                              interleaved, amplitude, v, k_cache, v_cache, slots, k_exp, v_exp,
+                              None if stream is None else _stream(stream))
+    if st is not None:
+        return _check(st, "gdn_qk_norm_rope")
+    # anything unusual, with what is wrong
     dev, dtype, shape, kshape = q.device, q.dtype, q.shape, k.shape
     if dev.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
@@ -1037,6 +1057,12 @@ def gdn_page_plan(kv_len, new_len, slots=None, positions=None, cu_seqlens=None, 
     updated in place; cu_seqlens [B + 1], kv_len_out [B] and the block tables ``pages``
     [B, max_pages] are written where given.  Request b is row rows[b] (or b) of the pool."""
     L = _lib or load_library()
+    st = _native.page_plan(kv_len, new_len, slots, positions, cu_seqlens, kv_len_out, pages, table,
+                           held, free_pages, free_count, page_size, rows, position_offset,
+                           None if stream is None else _stream(stream))
+    if st is not None:
+        return _check(st, "gdn_page_plan")
+    # anything unusual, with what is wrong
     p, dev = _page_pool(table, held, free_pages, free_count, page_size)
     i32 = torch.int32
     shape = kv_len.shape
@@ -1082,6 +1108,11 @@ def gdn_page_release(keep_len, *, table, held, free_pages, free_count, page_size
     """Requests keep the pages of their first keep_len [B] tokens and give the others back (see
     gdn_page_release in include/gdn.h); the pool as in gdn_page_plan."""
     L = _lib or load_library()
+    st = _native.page_release(keep_len, table, held, free_pages, free_count, page_size, rows,
+                              None if stream is None else _stream(stream))
+    if st is not None:
+        return _check(st, "gdn_page_release")
+    # anything unusual, with what is wrong
     p, dev = _page_pool(table, held, free_pages, free_count, page_size)
     B = keep_len.shape[0]
     if rows is None and B > p.num_rows:
@@ -1134,7 +1165,14 @@ def gdn_verify_tokens(target_logits, tokens, accepted, *, clocks, draft_ids=None
     out) or None.  Writes tokens [B, T + 1] (int32: the accepted drafts, the token behind them,
     then -1), accepted [B] (int32) and logprobs [B, T + 1] (fp32) or None.  T = 0 draws one token
     a sequence.  See gdn_verify_tokens in include/gdn.h."""
-    L = load_library()
+    L = _lib or load_library()
+    if workspace is not None:
+        st = _native.verify_tokens(target_logits, tokens, accepted, clocks, draft_ids, draft_logits,
+                                   accept_u, scale, logprobs, workspace,
+                                   None if stream is None else _stream(stream))
+        if st is not None:
+            return _check(st, "gdn_verify_tokens")
+    # a workspace to be made, or anything unusual, with what is wrong
     if target_logits.dim() != 3:
         raise ValueError(f"target_logits: shape {tuple(target_logits.shape)}, expected (B, T + 1, V)")
     dev = target_logits.device
