@@ -189,7 +189,10 @@ __global__ void __launch_bounds__(kMostThreads) gdn_page_plan_kernel(GdnPoolArgs
   const int rank = kPart == kAll ? cluster_rank() : blockIdx.x;
   const int ctas = kPart == kAll ? cluster_size() : gridDim.x;
   const int tid = rank * blockDim.x + threadIdx.x, threads = ctas * blockDim.x;
-  if (kPart == kOutputs) pdl_trigger();
+  // Nothing is read before everything earlier is done; the second half of a large plan, which may
+  // start from here on, reads the pool beside the first.
+  if (kPart != kState) pdl_wait();
+  pdl_trigger();
   const int count = *p.free_count, fill = a.slots || a.positions ? a.capacity : 0;
   Totals totals;
   bool good = scan_requests(p, a, s, &totals);
@@ -278,6 +281,8 @@ __global__ void __launch_bounds__(kMostThreads) gdn_page_release_kernel(GdnPoolA
   const Shared s = carve(smem, a.B);
   const int rank = cluster_rank(), ctas = cluster_size();
   const int tid = rank * blockDim.x + threadIdx.x, threads = ctas * blockDim.x;
+  pdl_wait();
+  pdl_trigger();
   const int count = *p.free_count;
   Totals totals;
   bool good = scan_requests(p, a, s, &totals);
@@ -332,12 +337,14 @@ cudaError_t launch(K kernel, const GdnPoolArgs& p, const GdnPlanArgs& a, long lo
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, p, a);
 }
 
@@ -358,8 +365,8 @@ cudaError_t gdn_launch_page_plan(const GdnPoolArgs& p, const GdnPlanArgs& a, cud
     if (e != cudaSuccess) return e;
   }
   const unsigned ctas = (unsigned)std::min(152ll, (words + 2047) / 2048);
-  pages::gdn_page_plan_kernel<pages::kOutputs><<<ctas, 512, smem, stream>>>(p, a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(true, pages::gdn_page_plan_kernel<pages::kOutputs>, dim3(ctas),
+                                   dim3(512), smem, stream, p, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(true, pages::gdn_page_plan_kernel<pages::kState>, dim3(1), dim3(512), smem, stream,
                     p, a);
