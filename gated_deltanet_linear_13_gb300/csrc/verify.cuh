@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gdn_verify_rows_kernel(G
   using G = Granule<T>;
   constexpr int kDepth = 2;                // granules on the way
   const int lane = threadIdx.x & 31, part = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  pdl_wait();                              // (nothing is read before)
   pdl_trigger();
   for (int b = blockIdx.x * kThreads + threadIdx.x; b < a.B; b += gridDim.x * kThreads) p.done[b] = 0;
   if (part >= p.parts) return;
@@ -368,6 +369,7 @@ __global__ void __launch_bounds__(kThreads, draw_ctas(sizeof(T) == 2)) gdn_verif
   using G = Granule<T>;
   constexpr int kVec = G::kVec;
   const int lane = threadIdx.x & 31, part = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  pdl_wait();                              // (nothing is read before)
   pdl_trigger();
   if (part >= p.parts) return;
   const Part l = part_at(p, part);
@@ -527,6 +529,7 @@ __global__ void __launch_bounds__(32) gdn_verify_draw_kernel(GdnVerifyArgs a, Pl
   const Part parts = parts_of(p, b);
   float4 v[kAtOnce];
   pdl_wait();
+  pdl_trigger();
   const Row st = row_of(p, b, parts, c, v);
   int token = -1;
   const bool dead = !(st.z > 0.0f);        // 0 or NaN: no distribution
@@ -584,6 +587,7 @@ __global__ void __launch_bounds__(kThreads, kRaceCtasPerSm) gdn_verify_race_kern
     if (a.draft) yi = ld_elem(row_at<T>(a, b, a.T + 1 + t) + id);
   }
   pdl_wait();
+  pdl_trigger();
   // ---- the rows' statistics, a warp a row
   for (int i = warp; i < n + 1 + (a.draft ? n : 0); i += kWarps) {
     const int j = i <= n ? i : a.T + 1 + i - n - 1;    // row of the sequence
@@ -789,9 +793,10 @@ size_t best_bytes(const Plan& p, int B) { return up(sizeof(float2) * (size_t)p.p
 template <typename T>
 cudaError_t launch(const GdnVerifyArgs& a, const Plan& p, cudaStream_t stream) {
   const int grid = (p.parts + kWarps - 1) / kWarps;
-  if (a.T == 0) gdn_verify_draw_rows_kernel<T><<<grid, kThreads, 0, stream>>>(a, p);
-  else gdn_verify_rows_kernel<T><<<grid, kThreads, 0, stream>>>(a, p);
-  const cudaError_t e = cudaGetLastError();
+  // (a few CTAs are set up beside the kernel before, as in qk_norm_rope.cuh)
+  const cudaError_t e =
+      launch_pdl(grid <= 152, a.T ? gdn_verify_rows_kernel<T> : gdn_verify_draw_rows_kernel<T>,
+                 dim3((unsigned)grid), dim3(kThreads), 0, stream, a, p);
   if (e != cudaSuccess) return e;
   if (a.T == 0)
     return launch_pdl(true, gdn_verify_draw_kernel<T>, dim3((unsigned)a.B), dim3(32), 0, stream, a, p);
