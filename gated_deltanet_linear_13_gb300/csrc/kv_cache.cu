@@ -60,9 +60,10 @@ __global__ void __launch_bounds__(kThreads) gdn_kv_append_kernel(
 #pragma unroll
       for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       const int e = kv_scale_exponent(top);
+      const uint2 codes = kv_codes(x[i], e);
       if (row >= 0) {
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(values ? c.v : c.k) + row * D + lane * 8) =
-            kv_codes(x[i], e);
+            codes;
         if (lane == 0) (values ? c.v_exp : c.k_exp)[row] = (uint8_t)(e + 127);
       }
     }

@@ -348,9 +348,10 @@ cudaError_t launch(GdnRopeArgs a, int tokens, int parts, cudaStream_t stream) {
   const size_t smem = kRagged ? sizeof(float) * kPer * (kTokens * 2 * L + kThreads) : 0;
   a.tokens = tokens;
   const dim3 grid((unsigned)((a.n + (long long)tokens - 1) / tokens), (unsigned)parts);
-  // A few CTAs are set up beside the kernel before (one token 2.8 -> 2.6 us).  More would be placed
-  // where that kernel leaves room, unevenly (2500 tokens in fp32 12.9 -> 15.6 us).
-  const bool beside = (long long)grid.x * grid.y <= 152;
+  // Where two calls' CTAs fit beside each other (six an SM), they are set up beside the kernel
+  // before (100 tokens of 24 + 4 + 4 heads of 256 3.5 -> 3.2 us).  More would be placed where that
+  // kernel leaves room, unevenly (2500 tokens in fp32 12.9 -> 15.6 us).
+  const bool beside = (long long)grid.x * grid.y <= 152 * 3;
   return launch_pdl(beside, gdn_qk_norm_rope_kernel<T, L, kTo, kTokens, kHeads, kRagged>, grid,
                     dim3(kThreads), smem, stream, a);
 }

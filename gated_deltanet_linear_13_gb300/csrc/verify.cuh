@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, kRaceCtasPerSm) gdn_verify_race_kern
   if (lane == 0) a.accepted[b] = accepted;
 }
 
-constexpr int kRaceCtas = 152 * kRaceCtasPerSm, kLeastSlice = 2048, kLeastGranules = 4;
+constexpr int kRaceCtas = 152 * kRaceCtasPerSm, kLeastSlice = 2048, kLeastGranules = 2;
 
 Plan plan_of(int B, int T, int V, int bf16, bool draft) {
   Plan p = {};
@@ -793,7 +793,7 @@ size_t best_bytes(const Plan& p, int B) { return up(sizeof(float2) * (size_t)p.p
 template <typename T>
 cudaError_t launch(const GdnVerifyArgs& a, const Plan& p, cudaStream_t stream) {
   const int grid = (p.parts + kWarps - 1) / kWarps;
-  // (a few CTAs are set up beside the kernel before, as in qk_norm_rope.cuh)
+  // (a few CTAs are set up beside the kernel before: one request 11.5 -> 11.1 us)
   const cudaError_t e =
       launch_pdl(grid <= 152, a.T ? gdn_verify_rows_kernel<T> : gdn_verify_draw_rows_kernel<T>,
                  dim3((unsigned)grid), dim3(kThreads), 0, stream, a, p);
