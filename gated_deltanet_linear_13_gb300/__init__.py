@@ -5,7 +5,9 @@ The gated delta rule (Gated DeltaNet) behind a C ABI (``include/gdn.h``):
 This module only marshals torch tensors into pointers and sizes: every step of the path runs
 in the CUDA kernels of ``libgdn.so``.  It checks shapes, dtypes, devices and contiguity
 before handing raw pointers to the library (a wrong size would otherwise let a kernel read
-past a buffer).  If ``libgdn.so`` is missing the import fails: there is no fallback.
+past a buffer).  The usual call of the serving step's operators is checked and marshalled by a
+native part (``csrc/marshal.cpp``), whatever it leaves by the checks here.  If ``libgdn.so`` is
+missing loading it fails: there is no fallback.
 """
 from __future__ import annotations
 
@@ -190,7 +192,11 @@ _native = None
 def _bind_marshal(L: ctypes.CDLL) -> None:
     """The binding's native part (csrc/marshal.cpp), on the functions of this library."""
     global _native
-    from . import _marshal as m
+    try:
+        from . import _marshal as m
+    except ImportError as e:
+        raise OSError("the binding's native part (_marshal.so) cannot be loaded: build it with "
+                      "`python -m gated_deltanet_linear_13_gb300.build_lib`") from e
     m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
              (L.gdn_qk_norm_rope, L.gdn_page_plan, L.gdn_page_release, L.gdn_verify_tokens)),
            getattr(torch._C, "_cuda_getCurrentRawStream", None))

@@ -750,7 +750,8 @@ gdn_status gdn_qk_norm_rope(int32_t n, int32_t num_heads, int32_t num_kv_heads, 
   if (n < 0 || num_heads < 1 || num_kv_heads < 1 || head_dim < 1 || !is_dtype(dtype) || !rope ||
       !isfinite(eps) || eps < 0.0f)
     return GDN_ERR_INVALID_ARGUMENT;
-  if (head_dim % 8 || head_dim > 256 || (long long)num_heads + 2ll * num_kv_heads > 65535)
+  if (head_dim % 8 || head_dim > 256 || (long long)num_heads + 2ll * num_kv_heads > 65535 ||
+      n > (1 << 30))
     return GDN_ERR_UNSUPPORTED;
   const int r = rope->rotary_dim;
   if (r < 0 || r > head_dim || r % 2 || !isfinite(rope->amplitude) ||

@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kMostThreads) gdn_page_plan_kernel(GdnPoolArgs
   if (!good) {                             // nothing is given
     if (kPart != kOutputs && tid == 0) atomicOr(&g_err_kv, kErrIndex);
     if (kPart != kState)
-      for (int t = tid; t < fill; t += threads) {
+      for (long long t = tid; t < fill; t += threads) {
         if (a.slots) a.slots[t] = -1;
         if (a.positions) a.positions[t] = 0;
       }

@@ -531,7 +531,8 @@ gdn_status gdn_token_logprobs(int32_t rows, int32_t vocab, gdn_dtype dtype, cons
  * in one pass: the RMS norm of every query and key head, their rotation by position and, with a
  * cache, the write of keys and values to their slots (as gdn_kv_cache_append would, from the
  * unrounded keys).
- * Definition, per token i and head vector x of D elements, in fp32 and rounded once:
+ * Definition, per token i and head vector x of D elements, in fp32 and rounded once (elements
+ * whose squares pass fp32's range make the vector's norm infinite):
  *     y = x / sqrt(mean(x^2) + eps) * weight          (y = x where the weight is NULL)
  *     pair p of the first rotary_dim elements, (a, b) = (y_p, y_{p + rotary_dim/2}) in the half
  *     layout, (y_2p, y_{2p+1}) in the interleaved one:
@@ -555,7 +556,7 @@ gdn_status gdn_token_logprobs(int32_t rows, int32_t vocab, gdn_dtype dtype, cons
  *   cache        NULL, or the cache that keys and values go to (H and D are its own), with
  *   v, slots     the values [n, H, D] in dtype, tokens v_token_stride apart, and the tokens'
  *                slots, as in gdn_kv_cache_append; ignored without a cache.
- * D is a multiple of 8 up to 256 (128 or 256 with a cache); Hq + 2 H <= 65535.
+ * D is a multiple of 8 up to 256 (128 or 256 with a cache); Hq + 2 H <= 65535; n <= 2^30.
  */
 typedef enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_layout;
 
@@ -661,7 +662,8 @@ gdn_status gdn_page_release(const gdn_page_pool* pool, int32_t batch, const int3
  *                w = max(p_a - q_a, 0) where draft a = accepted < m was refused,
  *                w = p_m where all were accepted
  * (the first of exponential clocks with rates w rings at i with probability w_i / sum w).
- * A refused draft without any w_i > 0 (p = q but for rounding) is itself the next token.
+ * A refused draft without any w_i > 0 (p = q but for rounding) is itself the next token; where all
+ * were accepted and no clock of a w_i > 0 rings, next is -1.
  *   target_logits [B, T + 1, V] in dtype, rows target_row_stride elements apart (>= V); any
  *                 alignment of the element's own.  Row j is of the token behind draft j - 1.
  *   draft_ids     [B, T] device int32: drafts up to the first negative id; the rest of the row is
@@ -673,7 +675,7 @@ gdn_status gdn_page_release(const gdn_page_pool* pool, int32_t batch, const int3
  *                 (zero, negative, NaN) never ring.
  *   scale         [B] fp32 inverse temperatures, or NULL (= 1).  +inf: greedy: a draft is accepted
  *                 if it is the largest logit (the lowest id of equal ones), next is the largest, no
- *                 random number is read.  Else within [2^-64, 2^64]; any other value (negative,
+ *                 random number counts.  Else within [2^-64, 2^64]; any other value (negative,
  *                 NaN, 0) leaves the sequence out: its outputs are left alone.
  *   tokens        [B, T + 1] int32: the accepted drafts, next, then -1.
  *   accepted      [B] int32.
@@ -683,7 +685,8 @@ gdn_status gdn_page_release(const gdn_page_pool* pool, int32_t batch, const int3
  * distribution (a NaN or +inf logit, nothing but -inf) accepts nothing; where it is the next
  * token's, p or q, next is -1 and its logprob 0.
  *   workspace     gdn_verify_tokens_workspace_size() bytes (0 for invalid sizes), 16-byte aligned.
- * T <= 64.  Decisions are those of exact arithmetic but where two sides agree to a few 2^-22.
+ * T <= 64.  Decisions are those of exact arithmetic but where two sides agree to 2^-18; a weight
+ * below 2^-126 of its row's largest probability counts as 0.
  */
 size_t gdn_verify_tokens_workspace_size(int32_t batch, int32_t num_drafts, int32_t vocab,
                                         gdn_dtype dtype, int32_t with_draft_logits);

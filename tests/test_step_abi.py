@@ -48,7 +48,7 @@ def _rope(L, **kw):
 BAD_ROPE = [
     (dict(n=-1), 1), (dict(hq=0), 1), (dict(h=0), 1), (dict(d=0), 1), (dict(dt=7), 1),
     (dict(no_rope=True), 1), (dict(eps=-1.0), 1), (dict(eps=math.nan), 1), (dict(eps=math.inf), 1),
-    (dict(d=260), 2), (dict(d=264), 2), (dict(d=100), 2), (dict(hq=65535), 2),
+    (dict(n=(1 << 30) + 1), 2), (dict(d=260), 2), (dict(d=264), 2), (dict(d=100), 2), (dict(hq=65535), 2),
     (dict(rot=-2), 1), (dict(rot=63), 1), (dict(rot=258), 1), (dict(layout=2), 1),
     (dict(amp=math.nan), 1), (dict(steps=None), 1), (dict(steps=A + 4), 1), (dict(pos=None), 1),
     (dict(pos=A + 2), 1), (dict(q=None), 1), (dict(q=A + 8), 1), (dict(k=None), 1),
