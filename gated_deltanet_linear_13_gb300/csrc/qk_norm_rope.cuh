@@ -15,9 +15,9 @@
 // its heads, while the first heads are on their way; a lane group takes kHeads heads of a token at
 // a time, so that addresses and weights cost once for all of them: what bounds the pass beside
 // memory is instructions (each vector finding its own took 228 a vector and 119 us below; this takes 117).
-// Measured: 16384 tokens of 24 + 4 + 4 heads of 256 in bf16 into a bf16 cache 90 us (6.0 TB/s read and
-// written, 88% of the copy rate), 2501 tokens of 16 + 2 heads of 128 in fp32 12.4 us (latency: four
-// rounds of vectors a lane group behind the launch and the angles), 64 tokens 2.9 us, one 2.6: the
+// Measured: 16384 tokens of 24 + 4 + 4 heads of 256 in bf16 into a bf16 cache 89 us (6.0 TB/s read and
+// written, 89% of the copy rate), 2501 tokens of 16 + 2 heads of 128 in fp32 11.8 us (latency: four
+// rounds of vectors a lane group behind the launch and the angles), 64 tokens 2.8 us, one 2.5: the
 // launch.
 // Part of kv_cache.cu, whose error word it uses.
 #pragma once
@@ -113,7 +113,6 @@ template <typename T, int L, int kTo, int kTokens, int kHeads, bool kRagged>
 __global__ void __launch_bounds__(kThreads, kRagged ? 4 : 6) gdn_qk_norm_rope_kernel(GdnRopeArgs a) {
   constexpr int kGroups = kThreads / L;
   pdl_wait();                              // (nothing is read before)
-  pdl_trigger();
   __shared__ float4 s_cos[kTokens][kRun / 4][L], s_sin[kTokens][kRun / 4][L];   // of a lane's pairs
   __shared__ float4 s_weight[2][kPer / 4][L];
   __shared__ long long s_row[kTokens];     // of head 0 of the token's slot (-1: none)
@@ -346,6 +345,9 @@ __global__ void __launch_bounds__(kThreads, kRagged ? 4 : 6) gdn_qk_norm_rope_ke
     }
     u = next;
   }
+  // Only now: CTAs of the next kernel that came earlier would land where this one leaves room,
+  // unevenly (2501 tokens in fp32 13.1 us, so 11.9; with an ordinary launch 14.4 in a stream).
+  pdl_trigger();
 }
 
 template <typename T, int L, int kTo, int kTokens, int kHeads, bool kRagged>
@@ -353,11 +355,8 @@ cudaError_t launch(GdnRopeArgs a, int tokens, int parts, cudaStream_t stream) {
   const size_t smem = kRagged ? sizeof(float) * kPer * (kTokens * 2 * L + kThreads) : 0;
   a.tokens = tokens;
   const dim3 grid((unsigned)((a.n + (long long)tokens - 1) / tokens), (unsigned)parts);
-  // Where two calls' CTAs fit beside each other (six an SM), they are set up beside the kernel
-  // before (100 tokens of 24 + 4 + 4 heads of 256 3.5 -> 3.2 us).  More would be placed where that
-  // kernel leaves room, unevenly (2500 tokens in fp32 12.9 -> 15.6 us).
-  const bool beside = (long long)grid.x * grid.y <= 152 * 3;
-  return launch_pdl(beside, gdn_qk_norm_rope_kernel<T, L, kTo, kTokens, kHeads, kRagged>, grid,
+  // (set up while the kernel before ends: 128 tokens into the 8-bit cache 6.2 -> 3.9 us in a stream)
+  return launch_pdl(true, gdn_qk_norm_rope_kernel<T, L, kTo, kTokens, kHeads, kRagged>, grid,
                     dim3(kThreads), smem, stream, a);
 }
 

@@ -16,7 +16,7 @@
 // w > best E, nearly, so there is a division where the best changes and none elsewhere.  Where two
 // are within 2^-16 of each other they are compared in 64 bits, and so is a u near its border.
 //
-// Bound by memory where the batch is large: 64 sequences of 4 drafts over 248320 logits in bf16 67 us
+// Bound by memory where the batch is large: 64 sequences of 4 drafts over 248320 logits in bf16 66 us
 // (250 MB of rows in 42 us, 5.9 TB/s, then 90 MB), 128 draws of 151936 27 us (105 MB); by instructions
 // and exponentials next to it (a granule of a row 130 instructions a warp, sixteen exponentials a
 // lane).  By latency where it is small: one sequence of 3 drafts 11 us, of which the rows take 3.3,
@@ -802,9 +802,9 @@ size_t best_bytes(const Plan& p, int B) { return up(sizeof(float2) * (size_t)p.p
 template <typename T>
 cudaError_t launch(const GdnVerifyArgs& a, const Plan& p, cudaStream_t stream) {
   const int grid = (p.parts + kWarps - 1) / kWarps;
-  // (a few CTAs are set up beside the kernel before: one request 11.5 -> 11.1 us)
+  // (set up while the kernel before ends: one request 14.2 -> 11.2 us in a stream)
   const cudaError_t e =
-      launch_pdl(grid <= 152, a.T ? gdn_verify_rows_kernel<T> : gdn_verify_draw_rows_kernel<T>,
+      launch_pdl(true, a.T ? gdn_verify_rows_kernel<T> : gdn_verify_draw_rows_kernel<T>,
                  dim3((unsigned)grid), dim3(kThreads), 0, stream, a, p);
   if (e != cudaSuccess) return e;
   if (a.T == 0)
