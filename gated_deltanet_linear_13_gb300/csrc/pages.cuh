@@ -241,10 +241,11 @@ __global__ void __launch_bounds__(kMostThreads) gdn_page_plan_kernel(GdnPoolArgs
       if (pages) pages[c] = page[k];
     }
   }
-  // ---- the tokens, a warp kInRow times 32 in a row (a lane looks its request up once, as long as
-  // its next token belongs to it too)
+  // ---- the tokens, a warp up to kInRow times 32 in a row, as many as there are for it (a lane looks
+  // its request up once, as long as its next token belongs to it too)
   const int total = (int)totals.a, mask = (1 << p.page_shift) - 1;
-  for (long long t1 = (long long)(tid >> 5) * (32 * kInRow); t1 < fill; t1 += (long long)warps * (32 * kInRow)) {
+  const int in_row = fill <= threads ? 1 : fill <= 2 * threads ? 2 : kInRow;
+  for (long long t1 = (long long)(tid >> 5) * (32 * in_row); t1 < fill; t1 += (long long)warps * (32 * in_row)) {
     const int* table = nullptr;            // of the lane's request
     const int* fresh = nullptr;            // its new pages, from the end
     int until = 0, back = 0, held = 0;     // where its tokens end, and what is taken off a packed token
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(kMostThreads) gdn_page_plan_kernel(GdnPoolArgs
     for (int k = 0; k < kInRow; ++k) {
       const long long t = t1 + k * 32 + lane;
       page[k] = at[k] = -1;
-      if (t >= total) continue;
+      if (k >= in_row || t >= total) continue;
       if (t >= until) {
         const int b = request_of(s, a.B, (int)t), row = s.row[b];
         until = s.tokens[b + 1], back = s.tokens[b] - s.from[b], held = s.held[b];
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kMostThreads) gdn_page_plan_kernel(GdnPoolArgs
 #pragma unroll
     for (int k = 0; k < kInRow; ++k) {
       const long long t = t1 + k * 32 + lane;
-      if (t >= fill) continue;
+      if (k >= in_row || t >= fill) continue;
       const bool some = page[k] >= 0 && page[k] < p.num_pages;
       if (a.slots && t < total && !some) atomicOr(&g_err_kv, kErrIndex);
       if (a.slots) a.slots[t] = some ? (page[k] << p.page_shift) + (at[k] & mask) : -1;
