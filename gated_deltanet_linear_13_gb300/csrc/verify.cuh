@@ -529,7 +529,7 @@ template <typename T>
 __global__ void __launch_bounds__(32) gdn_verify_draw_kernel(GdnVerifyArgs a, Plan p) {
   const int b = blockIdx.x, lane = threadIdx.x;
   const float given = a.scale ? a.scale[b] : 1.0f;
-  if (!takes_part(given)) return;
+  if (!takes_part(given)) return pdl_wait();           // (see the race's)
   const bool greedy = given == INFINITY;
   const float scale = scale_of(given), c = scale * kLog2e;
   const T* x = row_at<T>(a, b, 0);
@@ -574,9 +574,11 @@ __global__ void __launch_bounds__(kThreads, kRaceCtasPerSm) gdn_verify_race_kern
   const int b = a.B - 1 - blockIdx.x / p.pieces, piece = blockIdx.x % p.pieces;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float given = a.scale ? a.scale[b] : 1.0f;
-  if (!takes_part(given)) return;
+  // (also where all sequences are left out this grid ends behind the rows', as the kernel after it,
+  // which may write what they read and use the workspace again, waits for this one alone)
+  if (!takes_part(given)) return pdl_wait();
   const bool greedy = given == INFINITY;
-  if (greedy && piece > 0) return;
+  if (greedy && piece > 0) return;         // (piece 0 waits)
   const float scale = scale_of(given), c = scale * kLog2e;
   const int n = drafts_of(a, b);
   if (threadIdx.x == 0) {
