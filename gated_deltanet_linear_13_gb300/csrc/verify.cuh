@@ -516,11 +516,21 @@ __device__ __forceinline__ Row row_of(const Plan& p, int row, const Part& parts,
 // The first of a granule's logits that equals m (the whole warp).
 template <typename T>
 __device__ __forceinline__ int first_equal(const T* x, int V, int q, float m) {
+  constexpr int kVec = Granule<T>::kVec;
   const long long at = (long long)q * Granule<T>::kLogits - shift_of(x);
   int id = 0x7fffffff;
-#pragma unroll 4
-  for (int e = threadIdx.x & 31; e < Granule<T>::kLogits; e += 32)
-    if (at + e >= 0 && at + e < V && ld_elem(x + at + e) == m) id = min(id, (int)(at + e));
+  uint4 u[2];
+#pragma unroll
+  for (int v = 0; v < 2; ++v) u[v] = edge_vec<false>(x, at + (v * 32 + (int)(threadIdx.x & 31)) * kVec, V);
+#pragma unroll
+  for (int v = 1; v >= 0; --v) {
+    const long long i = at + (v * 32 + (int)(threadIdx.x & 31)) * kVec;
+    float f[kVec];
+    widen(u[v], (const T*)nullptr, f);
+#pragma unroll
+    for (int k = kVec - 1; k >= 0; --k)
+      if (i + k >= 0 && i + k < V && f[k] == m) id = (int)(i + k);
+  }
   return (int)__reduce_min_sync(0xffffffffu, (unsigned)id);
 }
 
