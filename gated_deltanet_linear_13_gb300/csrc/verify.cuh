@@ -17,7 +17,7 @@
 // are within 2^-16 of each other they are compared in 64 bits, and so is a u near its border.
 //
 // Bound by memory where the batch is large: 64 sequences of 4 drafts over 248320 logits in bf16 66 us
-// (250 MB of rows in 42 us, 5.9 TB/s, then 90 MB), 128 draws of 151936 27 us (105 MB); by instructions
+// (250 MB of rows in 42 us, 5.9 TB/s, then 90 MB), 128 draws of 151936 23 us (105 MB); by instructions
 // and exponentials next to it (a granule of a row 130 instructions a warp, sixteen exponentials a
 // lane).  By latency where it is small: one sequence of 3 drafts 11 us, of which the rows take 3.3,
 // the second kernel's start behind the first 1.8, statistics and decisions 1.3, a slice 1.8, the join
@@ -385,15 +385,17 @@ __global__ void __launch_bounds__(kThreads, draw_ctas(sizeof(T) == 2)) gdn_verif
   // the granule ahead: sequence and granule of the next to be loaded
   int aleft = left, ab = b, aq = q;
   const T* ax = row_at<T>(a, ab, 0);
-  bool wanted = true;                      // (of the first row: for the first granule)
+  // 0: nothing, 1: the row (greedy), 2: its clocks too (of the first row: for the first granule)
+  int wanted = 2;
   uint4 ahead[2];
   float clock[2][kVec];
   auto load = [&](int v) {                 // its v-th vectors
-    if (aleft == 0 || !wanted) return;
+    if (aleft == 0 || wanted == 0) return;
     const long long i = (long long)aq * G::kLogits - shift_of(ax) + (v * 32 + lane) * kVec;
     const bool inner = aq > 0 && aq + 2 < p.granules;      // all of it the row's
     if (inner && in_bounds(&g_err_lp, i >= 0 && i + kVec <= a.V)) ahead[v] = load_inner(ax + i);
     else ahead[v] = edge_vec<true>(ax, i, a.V);
+    if (wanted == 1) return;               // (128 greedy rows of 151936 in bf16 22.0 us, so 15.9)
     const float* e = a.clocks + (long long)ab * a.V + i;
     if (inner && (reinterpret_cast<uintptr_t>(e) & 15) == 0) {
 #pragma unroll
@@ -403,18 +405,22 @@ __global__ void __launch_bounds__(kThreads, draw_ctas(sizeof(T) == 2)) gdn_verif
       for (int k = 0; k < kVec; ++k) clock[v][k] = i + k >= 0 && i + k < a.V ? e[k] : 0.0f;
     }
   };
+  auto look = [&]() {
+    const float given = a.scale ? a.scale[ab] : 1.0f;
+    wanted = given == INFINITY ? 1 : in_range(given) ? 2 : 0;
+  };
   auto advance = [&]() {
     if (aleft == 0 || --aleft == 0) return;
     if (++aq == p.granules) {
       aq = 0;
       ax = row_at<T>(a, ++ab, 0);
-      wanted = takes_part(a.scale ? a.scale[ab] : 1.0f);
+      look();
     }
   };
   load(0);
   load(1);
   advance();
-  wanted = takes_part(a.scale ? a.scale[ab] : 1.0f);
+  look();
   while (left > 0) {
     // ---- this warp's granules of a row
     const float given = a.scale ? a.scale[b] : 1.0f, scale = scale_of(given), c = scale * kLog2e;
