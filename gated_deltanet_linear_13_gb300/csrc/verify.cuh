@@ -59,7 +59,7 @@ struct Plan {
   float4* stats;                           // [row + part]: m, z, granule of the largest; where
                                            // the first pass draws: m, z, index (greedy:
                                            // granule), w / E
-  float2* best;                            // [B][pieces]: w / E and its index
+  float4* best;                            // [B][pieces]: w / E, its index and its logit
   int* done;                               // [B]
 };
 
@@ -584,6 +584,8 @@ __global__ void __launch_bounds__(kThreads, kRaceCtasPerSm) gdn_verify_race_kern
   __shared__ Row s_row[kMaxRows];
   __shared__ int s_arg[kGdnMaxDrafts + 1];            // greedy: the rows' largest
   __shared__ int s_refused;
+  __shared__ int s_id[kGdnMaxDrafts];                 // the drafts, and their logits
+  __shared__ float s_x[kGdnMaxDrafts];
   __shared__ float s_best[kWarps];
   __shared__ int s_at[kWarps];
   // the last sequences first: their rows were read last
@@ -611,15 +613,20 @@ __global__ void __launch_bounds__(kThreads, kRaceCtasPerSm) gdn_verify_race_kern
     u = a.accept_u[(long long)b * a.T + t];
     xi = ld_elem(row_at<T>(a, b, t) + id);
     if (a.draft) yi = ld_elem(row_at<T>(a, b, a.T + 1 + t) + id);
+    s_id[t] = id, s_x[t] = xi;
   }
+  // (a warp's first row, whose parts are known)
+  const int rows = n + 1 + (a.draft ? n : 0);
+  auto row_of_sequence = [&](int i) { return i <= n ? i : a.T + 1 + i - n - 1; };
+  Part parts = parts_of(p, b * p.rows + row_of_sequence(min(warp, rows - 1)));
   pdl_wait();
   pdl_trigger();
   // ---- the rows' statistics, a warp a row
-  for (int i = warp; i < n + 1 + (a.draft ? n : 0); i += kWarps) {
-    const int j = i <= n ? i : a.T + 1 + i - n - 1;    // row of the sequence
+  for (int i = warp; i < rows; i += kWarps) {
+    const int j = row_of_sequence(i), row = b * p.rows + j;
     float4 v[kAtOnce];
-    const int row = b * p.rows + j;
-    const Row st = row_of(p, row, parts_of(p, row), c, v);
+    if (i >= kWarps) parts = parts_of(p, row);
+    const Row st = row_of(p, row, parts, c, v);
     if (lane == 0) s_row[j] = st;
     if (greedy && j <= a.T) {
       const int arg = first_equal(row_at<T>(a, b, j), a.V, st.q, st.m);
@@ -661,14 +668,16 @@ __global__ void __launch_bounds__(kThreads, kRaceCtasPerSm) gdn_verify_race_kern
     if (!good) atomicMin(&s_refused, t);
   }
   __syncthreads();
-  const int accepted = s_refused, last_draft = accepted < n ? a.ids[(long long)b * a.T + accepted] : -1;
+  const int accepted = s_refused, last_draft = accepted < n ? s_id[accepted] : -1;
   const bool refused = accepted < n;
   const int yj = a.T + 1 + accepted;
   const bool hopeless = dead(accepted) || (refused && a.draft && !greedy && dead(yj));
   if (hopeless && piece > 0) return;
   int token = -1;
+  float logit = 0.0f;                      // the token's
   if (greedy) {
     token = hopeless ? -1 : s_arg[accepted];
+    logit = s_row[accepted].m;
   } else if (!hopeless) {
     // ---- the race over this CTA's slice
     const T* x = row_at<T>(a, b, accepted);
@@ -746,12 +755,13 @@ __global__ void __launch_bounds__(kThreads, kRaceCtasPerSm) gdn_verify_race_kern
     if (warp > 0) return;
     race.best = 0.0f, race.at = -1;
     race.join(lane < kWarps ? s_best[lane] : 0.0f, lane < kWarps ? s_at[lane] : -1);
+    if (race.at >= 0 && in_bounds(&g_err_lp, race.at < a.V)) logit = ld_elem(x + race.at);   // (in L1)
     // ---- the last CTA of the sequence joins the slices
     if (p.pieces > 1) {
-      float2* slices = p.best + (long long)b * p.pieces;
+      float4* slices = p.best + (long long)b * p.pieces;
       int last = 0;
       if (lane == 0) {
-        __stcg(&slices[piece], make_float2(race.best, __int_as_float(race.at)));
+        __stcg(&slices[piece], make_float4(race.best, __int_as_float(race.at), logit, 0.0f));
         asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;\n"
                      : "=r"(last) : "l"(&p.done[b]) : "memory");
       }
@@ -760,30 +770,36 @@ __global__ void __launch_bounds__(kThreads, kRaceCtasPerSm) gdn_verify_race_kern
       __syncwarp();
       race.best = 0.0f, race.at = -1;
       for (int k0 = 0; k0 < p.pieces; k0 += 32 * kAtOnce) {
-        float2 r[kAtOnce];
+        float4 r[kAtOnce];
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
           const int slice = k0 + 32 * k + lane;
-          r[k] = slice < p.pieces ? __ldcg(&slices[slice]) : make_float2(0.0f, 0.0f);
+          r[k] = slice < p.pieces ? __ldcg(&slices[slice])
+                                  : make_float4(0.0f, __int_as_float(-1), 0.0f, 0.0f);
         }
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) race.join(r[k].x, __float_as_int(r[k].y));
+        for (int k = 0; k < kAtOnce; ++k) {
+          race.join(r[k].x, __float_as_int(r[k].y));
+          const uint32_t who =
+              __ballot_sync(0xffffffffu, race.at >= 0 && __float_as_int(r[k].y) == race.at);
+          if (who) logit = __shfl_sync(0xffffffffu, r[k].z, __ffs(who) - 1);
+        }
       }
     }
     token = race.at;
-    if (token < 0 && refused) token = last_draft;      // p = q but for rounding
+    if (token < 0 && refused) token = last_draft, logit = s_x[accepted];   // p = q but for rounding
   }
   if (warp > 0) return;
   // ---- what the sequence gets
   for (int k = lane; k <= a.T; k += 32) {
-    const int given_id = k < accepted ? a.ids[(long long)b * a.T + k] : k == accepted ? token : -1;
+    const int given_id = k < accepted ? s_id[k] : k == accepted ? token : -1;
     const long long to = (long long)b * (a.T + 1) + k;
     if (!in_bounds(&g_err_lp, given_id < a.V)) continue;
     a.tokens[to] = given_id;
     if (a.logprobs) {
       float lp = 0.0f;
       if (given_id >= 0)
-        lp = (ld_elem(row_at<T>(a, b, k) + given_id) - s_row[k].m) * scale - kLn2 * log2f(s_row[k].z);
+        lp = ((k < accepted ? s_x[k] : logit) - s_row[k].m) * scale - kLn2 * log2f(s_row[k].z);
       a.logprobs[to] = lp;
     }
   }
@@ -815,7 +831,7 @@ size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t stats_bytes(const Plan& p, int B) {
   return up(sizeof(float4) * ((size_t)p.rows * B + p.parts));
 }
-size_t best_bytes(const Plan& p, int B) { return up(sizeof(float2) * (size_t)p.pieces * B); }
+size_t best_bytes(const Plan& p, int B) { return up(sizeof(float4) * (size_t)p.pieces * B); }
 
 template <typename T>
 cudaError_t launch(const GdnVerifyArgs& a, const Plan& p, cudaStream_t stream) {
@@ -843,7 +859,7 @@ cudaError_t gdn_launch_verify_tokens(const GdnVerifyArgs& a, cudaStream_t stream
   verify::Plan p = verify::plan_of(a.B, a.T, a.V, a.bf16, a.draft != nullptr);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.stats = reinterpret_cast<float4*>(ws);
-  p.best = reinterpret_cast<float2*>(ws + verify::stats_bytes(p, a.B));
+  p.best = reinterpret_cast<float4*>(ws + verify::stats_bytes(p, a.B));
   p.done = reinterpret_cast<int*>(ws + verify::stats_bytes(p, a.B) + verify::best_bytes(p, a.B));
   return a.bf16 ? verify::launch<__nv_bfloat16>(a, p, stream) : verify::launch<float>(a, p, stream);
 }
