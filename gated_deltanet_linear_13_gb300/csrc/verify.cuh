@@ -25,6 +25,8 @@
 // Part of logprobs.cu, whose error word it uses.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "logits.cuh"
 #include "sm100_ptx.cuh"
@@ -490,7 +492,6 @@ __device__ __forceinline__ Part parts_of(const Plan& p, int row) {
   return Part{c0, part_of(p, row * p.granules + p.granules - 1) - c0 + 1};
 }
 
-constexpr int kAheadRace = 2;              // vectors of a thread on the way in the race
 constexpr int kAtOnce = 4;                 // entries of a lane on the way
 // Entries k0 + lane, + 32, ... of the parts of a row (none: as of no logits).
 __device__ __forceinline__ void entries_of(const Plan& p, int row, const Part& parts, int k0,
@@ -692,61 +693,111 @@ __global__ void __launch_bounds__(kThreads, kRaceCtasPerSm) gdn_verify_race_kern
       if (y) r = fmaf(-race.ratio, ptx::ex2_approx((w - race.my) * c), r);
       return r;
     };
-    const bool aligned = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(clocks) |
-                           (y ? reinterpret_cast<uintptr_t>(y) : 0)) & 15) == 0;
-    if (aligned) {                         // (a slice is a multiple of 16 logits)
-      const int whole = hi & ~(kVec - 1);
-      uint4 ux[kAheadRace], uy[kAheadRace], ue[kAheadRace][kVec / 4];
+    // x in its own vectors, from lo2 to hi2 (not the row's first logit nor its last two: what is
+    // loaded beside a vector of y's is the row's too)
+    const int shift = shift_of(x), from = max(lo, 1), to = min(hi, a.V - 2);
+    const int lo2 = min(hi, from + (-(from + shift) & (kVec - 1)));
+    const int hi2 = max(lo2, to - ((to + shift) & (kVec - 1)));
+    const bool wide_y = !y || shift_of(y) == shift;
+    const bool wide_e = (reinterpret_cast<uintptr_t>(clocks + lo2) & 15) == 0;
+    auto vectors = [&](auto all_wide) {    // all_wide: y's and the clocks' vectors lie as x's do
+      constexpr bool kWide = decltype(all_wide)::value;
+      const bool odd = !kWide && !wide_y && (reinterpret_cast<uintptr_t>(y + lo2) & 2);
+      constexpr int kWords = kWide ? 4 : 5, kAhead = kWide ? 2 : 1;
+      uint4 ux[kAhead];
+      uint32_t uy[kAhead][kWords];
+      float ue[kAhead][kVec];
       auto fetch = [&](int k, int i) {
-        if (i >= whole || !in_bounds(&g_err_lp, i >= 0 && i + kVec <= a.V)) return;
-        ux[k] = *reinterpret_cast<const uint4*>(x + i);
-        if (y) uy[k] = *reinterpret_cast<const uint4*>(y + i);
+        if (i >= hi2 || !in_bounds(&g_err_lp, i >= 1 && i + kVec + 2 <= a.V)) return;
+        ux[k] = load_inner<false>(x + i);
+        if (y && (kWide || wide_y)) {
+          const uint4 u = load_inner<false>(y + i);
+          uy[k][0] = u.x, uy[k][1] = u.y, uy[k][2] = u.z, uy[k][3] = u.w;
+        } else if (y) {
+          const uint32_t* at =
+              reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(y + i) & ~(uintptr_t)3);
 #pragma unroll
-        for (int e = 0; e < kVec / 4; ++e) ue[k][e] = load_inner(clocks + i + 4 * e);
+          for (int q = 0; q < kWords; ++q) uy[k][q] = at[q];
+        }
+        if (kWide || wide_e) {
+#pragma unroll
+          for (int q = 0; q < kVec; q += 4)
+            widen(load_inner(clocks + i + q), (const float*)nullptr, ue[k] + q);
+        } else {
+#pragma unroll
+          for (int q = 0; q < kVec; ++q) ue[k][q] = clocks[i + q];
+        }
       };
       constexpr int kStride = kThreads * kVec;
-      int i = lo + (int)threadIdx.x * kVec;
+      int i = lo2 + (int)threadIdx.x * kVec;
 #pragma unroll
-      for (int k = 0; k < kAheadRace; ++k) fetch(k, i + k * kStride);
-      for (; i - lane * kVec < whole; i += kAheadRace * kStride) {
+      for (int k = 0; k < kAhead; ++k) fetch(k, i + k * kStride);
+      for (; i - lane * kVec < hi2; i += kAhead * kStride) {
 #pragma unroll
-        for (int k = 0; k < kAheadRace; ++k) {
+        for (int k = 0; k < kAhead; ++k) {
           const int at = i + k * kStride;
           float v[kVec], w[kVec], e[kVec];
           widen(ux[k], x, v);
-          widen(uy[k], x, w);
+          if (odd) {
 #pragma unroll
-          for (int c4 = 0; c4 < kVec / 4; ++c4) widen(ue[k][c4], (const float*)nullptr, e + 4 * c4);
-          fetch(k, at + kAheadRace * kStride);
-#pragma unroll
-          for (int c1 = 0; c1 < kVec; ++c1) {
-            w[c1] = weight(v[c1], w[c1]);
-            if (at >= whole) w[c1] = e[c1] = 0.0f;
+            for (int q = 0; q < 4; ++q)
+              uy[k][q] = __funnelshift_r(uy[k][q], uy[k][kWords - 4 + q], 16);
           }
-          race.offer(w, e, [&](int k1) { return at + k1; });
+          widen(make_uint4(uy[k][0], uy[k][1], uy[k][2], uy[k][3]), x, w);
+#pragma unroll
+          for (int q = 0; q < kVec; ++q) e[q] = ue[k][q];
+          fetch(k, at + kAhead * kStride);
+#pragma unroll
+          for (int q = 0; q < kVec; ++q) {
+            w[q] = weight(v[q], w[q]);
+            if (at >= hi2) w[q] = e[q] = 0.0f;
+          }
+          race.offer(w, e, [&](int q) { return at + q; });
         }
       }
-      if (warp == 0 && whole < hi) {       // the row's last logits
+      if (warp == 0) {                     // the slice's logits before and behind them, up to nine each
+        const int at = lane < 16 ? lo + lane : hi2 + lane - 16;
         float w[1] = {0.0f}, e[1] = {0.0f};
-        const int i = whole + lane;
-        if (i < hi) w[0] = weight(ld_elem(x + i), y ? ld_elem(y + i) : 0.0f), e[0] = clocks[i];
-        race.offer(w, e, [&](int) { return i; });
+        if (at < (lane < 16 ? lo2 : hi) && in_bounds(&g_err_lp, at >= 0 && at < a.V))
+          w[0] = weight(ld_elem(x + at), y ? ld_elem(y + at) : 0.0f), e[0] = clocks[at];
+        race.offer(w, e, [&](int) { return at; });
       }
+    };
+    // 16-bit logits are read so whatever the others' alignment: y's vectors as the words that hold
+    // them, clocks one by one (64 sequences of 4 drafts over 151669 logits element by element 62 us,
+    // so 57).  32-bit ones element by element: 16 of 7 drafts over 151669 26.5 us, so 27
+    // to 28.
+    if (wide_y && wide_e) {
+      vectors(std::true_type{});
+    } else if constexpr (sizeof(T) == 2) {
+      vectors(std::false_type{});
     } else {
-      constexpr int kN = 8;                // elements of a lane at a time, 32 apart
-      for (int i0 = lo + warp * 32 * kN; i0 < hi; i0 += kThreads * kN) {
-        float v[kN], w[kN], e[kN];
+      constexpr int kN = 4, kAhead = 2;    // a lane's elements, 32 apart, and how often
+      float v[kAhead][kN], w[kAhead][kN], e[kAhead][kN];
+      auto fetch = [&](int d, int i0) {
 #pragma unroll
         for (int k = 0; k < kN; ++k) {
           const int i = i0 + 32 * k + lane;
           const bool in = i < hi && in_bounds(&g_err_lp, i >= 0 && i < a.V);
-          v[k] = in ? ld_elem(x + i) : -INFINITY;
-          w[k] = in && y ? ld_elem(y + i) : -INFINITY;
-          e[k] = in ? clocks[i] : 0.0f;
+          v[d][k] = in ? ld_elem(x + i) : -INFINITY;
+          w[d][k] = in && y ? ld_elem(y + i) : -INFINITY;
+          e[d][k] = in ? clocks[i] : 0.0f;
         }
+      };
+      constexpr int kStride = kThreads * kN;
+      int i0 = lo + warp * 32 * kN;
 #pragma unroll
-        for (int k = 0; k < kN; ++k) w[k] = weight(v[k], w[k]);
-        race.offer(w, e, [&](int k) { return i0 + lane + 32 * k; });
+      for (int d = 0; d < kAhead; ++d) fetch(d, i0 + d * kStride);
+      for (; i0 < hi; i0 += kAhead * kStride) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+          const int at = i0 + d * kStride;
+          float w1[kN], e1[kN];
+#pragma unroll
+          for (int k = 0; k < kN; ++k) w1[k] = weight(v[d][k], w[d][k]), e1[k] = e[d][k];
+          fetch(d, at + kAhead * kStride);
+          race.offer(w1, e1, [&](int k) { return at + lane + 32 * k; });
+        }
       }
     }
     // ---- the slice's best
