@@ -22,7 +22,7 @@ namespace pages {
 
 constexpr int kMostThreads = 1024, kMostWarps = kMostThreads / 32;
 constexpr int kMaxCtas = 8;                // of the cluster (the portable most)
-constexpr int kAtOnce = 4, kColumns = 32 * kAtOnce;   // of a block table a warp takes at a time
+constexpr int kAtOnce = 4;                 // entries of a block table on the way in a lane
 // Words of output up to which one cluster does everything; above, many CTAs write the outputs and a
 // second launch the state (a plan and a release: 20000 tokens 10.3 us in one cluster, 9.2 in two
 // launches; 80000 13.1 / 9.5; 240000 21.9 / 10.7).
@@ -163,6 +163,21 @@ __device__ __forceinline__ int request_of(const Shared& s, int B, int t) {
   return lo;
 }
 
+// How block tables are shared out: `lanes` neighbours (a power of two) take a request's entries,
+// kAtOnce each at a time, so that short tables leave no warp waiting for one request after the other
+// (a plan and a release of 151 requests of one page 14.6 us with a warp each).
+struct Tables {
+  int lanes, lane, columns, pieces;        // of a request's table: entries at a time, and how often
+  int first, step;                         // of the pieces: this lane's first, and the next
+};
+__device__ __forceinline__ Tables share_tables(int max_pages, int tid, int threads) {
+  const int needed = (max_pages + kAtOnce - 1) / kAtOnce;
+  const int shift = needed <= 1 ? 0 : min(5, 32 - __clz(needed - 1));
+  const int columns = kAtOnce << shift;
+  return Tables{1 << shift, tid & ((1 << shift) - 1), columns, (max_pages + columns - 1) / columns,
+                tid >> shift, threads >> shift};
+}
+
 // The pool's and the requests' state after a plan.
 __device__ __forceinline__ void write_state(const GdnPoolArgs& p, const GdnPlanArgs& a,
                                             const Shared& s, int left, int tid, int threads) {
@@ -215,27 +230,27 @@ __global__ void __launch_bounds__(kMostThreads) gdn_page_plan_kernel(GdnPoolArgs
   // ---- the requests' new state
   if (kPart != kOutputs) write_state(p, a, s, count - (int)totals.b, tid, threads);
   if (kPart == kState) return;
-  // ---- block tables: a warp kColumns of a request's pages at a time
+  // ---- block tables
   const int lane = threadIdx.x & 31, warps = threads >> 5;
-  const int pieces = (p.max_pages + kColumns - 1) / kColumns;
-  for (long long w = tid >> 5; w < (long long)a.B * pieces; w += warps) {
-    const int b = (int)(w / pieces), c0 = (int)(w - (long long)b * pieces) * kColumns;
+  const Tables l = share_tables(p.max_pages, tid, threads);
+  for (long long w = l.first; w < (long long)a.B * l.pieces; w += l.step) {
+    const int b = (int)(w / l.pieces), c0 = (int)(w - (long long)b * l.pieces) * l.columns;
     const int row = s.row[b], held = s.held[b], first = s.pages[b];
-    const int end = min(c0 + kColumns, held + s.pages[b + 1] - first);
+    const int end = min(c0 + l.columns, held + s.pages[b + 1] - first);
     if (row < 0) continue;
     int* table = p.table + (long long)row * p.max_pages;
     int* pages = a.pages ? a.pages + (long long)b * p.max_pages : nullptr;
     int page[kAtOnce];
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      const int c = c0 + k * 32 + lane;
+      const int c = c0 + k * l.lanes + l.lane;
       page[k] = 0;
       if (c < end && (pages || c >= held) && in_bounds(&g_err_kv, c >= 0 && c < p.max_pages))
         page[k] = c >= held ? p.free_pages[count - 1 - (first + c - held)] : table[c];
     }
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      const int c = c0 + k * 32 + lane;
+      const int c = c0 + k * l.lanes + l.lane;
       if (c >= end || !in_bounds(&g_err_kv, c >= 0 && c < p.max_pages)) continue;
       if (c >= held) table[c] = page[k];
       if (pages) pages[c] = page[k];
@@ -299,22 +314,21 @@ __global__ void __launch_bounds__(kMostThreads) gdn_page_release_kernel(GdnPoolA
         in_bounds(&g_err_kv, s.row[b] >= 0 && s.row[b] < p.num_rows))
       p.held[s.row[b]] = s.from[b];
   if (tid == 0) *p.free_count = end;
-  const int lane = threadIdx.x & 31, warps = threads >> 5;
-  const int pieces = (p.max_pages + kColumns - 1) / kColumns;
-  for (long long w = tid >> 5; w < (long long)a.B * pieces; w += warps) {
-    const int b = (int)(w / pieces), c0 = (int)(w - (long long)b * pieces) * kColumns;
+  const Tables l = share_tables(p.max_pages, tid, threads);
+  for (long long w = l.first; w < (long long)a.B * l.pieces; w += l.step) {
+    const int b = (int)(w / l.pieces), c0 = (int)(w - (long long)b * l.pieces) * l.columns;
     const int first = s.pages[b], given = s.pages[b + 1] - first, kept = s.from[b];
     if (given == 0) continue;
     const int* table = p.table + (long long)s.row[b] * p.max_pages + kept;
     int page[kAtOnce];
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      const int c = c0 + k * 32 + lane;
+      const int c = c0 + k * l.lanes + l.lane;
       page[k] = c < given && in_bounds(&g_err_kv, kept + c < p.max_pages) ? table[c] : 0;
     }
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      const int c = c0 + k * 32 + lane, to = end - 1 - (first + c);
+      const int c = c0 + k * l.lanes + l.lane, to = end - 1 - (first + c);
       if (c < given && in_bounds(&g_err_kv, to >= count && to < p.num_pages)) p.free_pages[to] = page[k];
     }
   }
