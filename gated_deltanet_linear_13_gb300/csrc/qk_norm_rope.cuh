@@ -22,6 +22,8 @@
 // Part of kv_cache.cu, whose error word it uses.
 #pragma once
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "kv_cache.cuh"
 #include "sm100_ptx.cuh"
@@ -364,12 +366,12 @@ template <typename T, int L, int kTo>
 cudaError_t launch(const GdnRopeArgs& a, cudaStream_t stream) {
   constexpr int kGroups = kThreads / L;
   const int per = a.Hq + a.H * (kTo == kToTensors ? 1 : 2);
-  // Tokens of a CTA, which share the cost of its start: as many as leave every SM enough CTAs to
-  // even out.  24 + 4 + 4 heads of 256 in bf16, one, two, three and four a CTA: 600 tokens 5.9 / 7.3 /
-  // - / 10.4 us, 1200 12.1 / 11.1 / - / 13.6, 2500 19.8 / 19.9 / 17.7 / 19.4; 16 + 2 of 128 in fp32: 1200
-  // 8.4 / 6.8 / - / 6.8, 2500 14.4 / 14.7 / 12.4 / 12.9, 10000 43.8 / 40.3 / - / 37.3.
-  const int per_sm = a.n / 152;
-  const int tokens = per_sm >= 4 * 5 ? 4 : per_sm >= 3 * 4 ? 3 : per_sm >= 2 * 3 ? 2 : 1;
+  // Tokens of a CTA, which share the cost of its start: as few as let all CTAs run at once (six an
+  // SM).  24 + 4 + 4 heads of 256 in bf16, one, two, three and four a CTA: 600 tokens 5.9 / 7.3 / - / 10.4
+  // us, 1200 12.1 / 11.1 / - / 13.6, 2500 19.8 / 19.9 / 17.7 / 19.4; 4 + 4 + 4: 3000 14.0 / 11.4 / 12.3 /
+  // 9.0; 16 + 2 of 128 in fp32: 1200 8.4 / 6.8 / - / 6.8, 2500 14.4 / 14.7 / 12.4 / 12.9, 10000 43.8 / 40.3 /
+  // - / 37.3.  (Up to eight cost the others: 16384 tokens 89 us, so 97 to 105.)
+  const int tokens = (int)std::min(4ll, (a.n + 152ll * 6 - 1) / (152 * 6));
   if (a.turn == kRaggedHalves) return launch<T, L, kTo, 4, 1, true>(a, tokens, 1, stream);
   // Few vectors: one a lane group, so that all of them are on the way at once.
   if ((long long)a.n * per <= 152ll * 4 * kGroups)
