@@ -372,10 +372,11 @@ cudaError_t launch(const GdnRopeArgs& a, cudaStream_t stream) {
   // 9.0; 16 + 2 of 128 in fp32: 1200 8.4 / 6.8 / - / 6.8, 2500 14.4 / 14.7 / 12.4 / 12.9, 10000 43.8 / 40.3 /
   // - / 37.3.  (Up to eight cost the others: 16384 tokens 89 us, so 97 to 105.)
   const int tokens = (int)std::min(4ll, (a.n + 152ll * 6 - 1) / (152 * 6));
-  if (a.turn == kRaggedHalves) return launch<T, L, kTo, 4, 1, true>(a, tokens, 1, stream);
   // Few vectors: one a lane group, so that all of them are on the way at once.
-  if ((long long)a.n * per <= 152ll * 4 * kGroups)
-    return launch<T, L, kTo, 1, 1, false>(a, 1, (per + kGroups - 1) / kGroups, stream);
+  const bool few = (long long)a.n * per <= 152ll * 4 * kGroups;
+  const int parts = few ? (per + kGroups - 1) / kGroups : 1;
+  if (a.turn == kRaggedHalves) return launch<T, L, kTo, 4, 1, true>(a, few ? 1 : tokens, parts, stream);
+  if (few) return launch<T, L, kTo, 1, 1, false>(a, 1, parts, stream);
   // Heads at a time: two of bf16 (registers; the large case of one 94 us, two 89, four 96), one of
   // fp32 (two spill: 15.4 us where one takes 13.0).
   return launch<T, L, kTo, 4, sizeof(T) == 2 ? 2 : 1, false>(a, tokens, 1, stream);
