@@ -17,7 +17,7 @@
 // are within 2^-16 of each other they are compared in 64 bits, and so is a u near its border.
 //
 // Bound by memory where the batch is large: 64 sequences of 4 drafts over 248320 logits in bf16 66 us
-// (250 MB of rows in 42 us, 5.9 TB/s, then 90 MB), 128 draws of 151936 23 us (105 MB); by instructions
+// (250 MB of rows in 42 us, 5.9 TB/s, then 90 MB), 128 draws of 151936 24 us (117 MB); by instructions
 // and exponentials next to it (a granule of a row 130 instructions a warp, sixteen exponentials a
 // lane).  By latency where it is small: one sequence of 3 drafts 11 us, of which the rows take 3.3,
 // the second kernel's start behind the first 1.8, statistics and decisions 1.3, a slice 1.8, the join
@@ -43,8 +43,8 @@ namespace verify {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 3, kRaceCtasPerSm = 3;
-// of the pass that also draws: 128 rows of 151936 in bf16 26.8 us (three: registers spill, 39.9); 64 of
-// 151936 in fp32 20.6 us with two, 19.2 with three
+// of the pass that also draws: 128 rows of 151936 in bf16 24 us (three: registers spill, 39); 64 of 151936
+// in fp32 18.5 us with two, 17.0 with three
 constexpr int draw_ctas(bool bf16) { return bf16 ? 2 : 3; }
 constexpr int kMaxRows = 2 * kGdnMaxDrafts + 1;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
