@@ -162,6 +162,13 @@ def test_steps_of_a_server(gdn, b, rows, columns, page, most):
     _clean(gdn)
 
 
+@pytest.mark.parametrize("columns", [1, 4, 5, 8, 9, 16, 17, 32, 33, 64, 65, 127, 128, 129, 256, 257])
+def test_tables_of_any_width(gdn, columns):
+    """Block tables around the widths that share a warp, of one request and of many."""
+    for b in (1, 3, 37, 130):
+        test_steps_of_a_server(gdn, b, b + 2, columns, 16, 16 * columns // 3 + 1)
+
+
 def test_what_was_taken_comes_back_as_it_was(gdn):
     pool = Pool(20, 30, 500, 16, seed=3)
     before = {k: x.clone() for k, x in pool.gpu.items()}

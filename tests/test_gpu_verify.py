@@ -203,6 +203,27 @@ def test_strides_and_alignment(gdn, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("sizes", [range(1, 42), (4089, 4096, 4097, 4103, 6145, 8200)])
+def test_every_alignment(gdn, sizes, dtype):
+    """Rows of the target and of the draft that begin at any element, each at its own, around the
+    sizes of a vector and of a slice; most drafts are refused, so that the race runs."""
+    for v in sizes:
+        for off, more in ((0, 0), (1, 0), (0, 1), (3, 6), (5, 2), (7, 7)):
+            c = _case(3, 2, v, dtype, "logits", seed=v)
+            c["scale"], c["u"] = None, 0.5 + c["u"] / 2
+            c["ids"] = c["ids"].clamp(min=0)
+            c["ids"][1] = c["draft"][1].float().argmax(-1)
+            for name, first in (("target", off), ("draft", more)):
+                x = c[name]
+                wide = torch.full((*x.shape[:2], v + 9), math.nan, dtype=dtype, device="cuda")
+                wide[..., first:first + v] = x
+                c[name] = wide[..., first:first + v]
+            out = _call(gdn, c)
+            _check(c, out, close=3)
+    _clean(gdn)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("v", [40, 5000, 100003])
 def test_masks(gdn, v, dtype):
     """Masks of -inf and of the type's lowest value, rows with one logit left or none, NaN and
