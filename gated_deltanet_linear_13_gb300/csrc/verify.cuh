@@ -50,6 +50,9 @@ constexpr int kMaxRows = 2 * kGdnMaxDrafts + 1;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMost = 18446744073709551616.0f;       // 2^64: scales lie within it and its inverse
 constexpr float kClose = 1.0f - 0x1p-16f;
+// A tinier clock rings as this one, so that w / E stays finite: an infinite one is above larger ones, and
+// is a NaN once its reference has moved far.
+constexpr float kLeastClock = 0x1p-126f;
 
 struct Plan {
   int granules;                            // of a row
@@ -200,7 +203,7 @@ __device__ __noinline__ double exact_race(const T* x, const T* y, const float* c
                                           float my, float ratio, float scale, int i) {
   double w = exp(((double)ld_elem(x + i) - (double)mx) * (double)scale);
   if (y) w -= exp(((double)ld_elem(y + i) - (double)my) * (double)scale) * (double)ratio;
-  return w / (double)clocks[i];
+  return w / (double)fmaxf(clocks[i], kLeastClock);
 }
 
 // The race of one row pair, as a warp runs it: the same best in all lanes.
@@ -238,7 +241,7 @@ struct Race {
   template <int N, typename At>
   __device__ __forceinline__ void offer(const float (&w)[N], const float (&e)[N], At&& at_of) {
     const float floor = best * kClose;
-    float over = 0.0f;                     // (a NaN or an infinite clock stays below)
+    float over = 0.0f;                     // (a NaN or an infinite clock stays below, a tiny one above)
     if constexpr (N % 2 == 0) {
       const unsigned long long minus = pair(-floor, -floor);
 #pragma unroll
@@ -256,8 +259,9 @@ struct Race {
     int at_k = 0;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      if (!(e[k] > 0.0f && w[k] > 0.0f && w[k] > floor * e[k] && at_of(k) != never)) continue;
-      const float q = __fdiv_rn(w[k], e[k]);
+      const float clock = fmaxf(e[k], kLeastClock);
+      if (!(e[k] > 0.0f && w[k] > 0.0f && w[k] > floor * clock && at_of(k) != never)) continue;
+      const float q = __fdiv_rn(w[k], clock);
       if (q > r) r = q, at_k = at_of(k);
     }
     if (__any_sync(0xffffffffu, r > 0.0f)) join(r, at_k);
