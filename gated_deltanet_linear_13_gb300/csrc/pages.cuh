@@ -42,6 +42,12 @@ __device__ __forceinline__ Shared carve(int* smem, int B) {
 }
 size_t shared_bytes(int B) { return sizeof(int) * (5 * (size_t)B + 2); }
 
+struct WarpSums {                          // of a scan: the running sums, and the totals in halves
+  unsigned a, b, a_low, a_high, b_low, b_high;
+};
+// Dynamic shared memory that a kernel may have without asking for more: 48 KB with what it declares.
+constexpr size_t kUnasked = 48 * 1024 - kMostWarps * sizeof(WarpSums);
+
 __device__ __forceinline__ int cluster_rank() {
   int r;
   asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
@@ -66,10 +72,7 @@ struct Totals {
   unsigned long long a, b;
 };
 __device__ __forceinline__ Two scan(Two x, Totals* totals) {
-  struct Warp {
-    unsigned a, b, a_low, a_high, b_low, b_high;
-  };
-  __shared__ Warp s_warp[kMostWarps];
+  __shared__ WarpSums s_warp[kMostWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   constexpr unsigned kAll = 0xffffffffu;
   auto inclusive = [&](Two v) {
@@ -82,15 +85,15 @@ __device__ __forceinline__ Two scan(Two x, Totals* totals) {
   };
   const Two sum = inclusive(x);
   // (in halves, whose sums over 8192 requests stay below 2^32)
-  const Warp mine{0, 0, __reduce_add_sync(kAll, x.a & 0xffffu), __reduce_add_sync(kAll, x.a >> 16),
-                  __reduce_add_sync(kAll, x.b & 0xffffu), __reduce_add_sync(kAll, x.b >> 16)};
+  const WarpSums mine{0, 0, __reduce_add_sync(kAll, x.a & 0xffffu), __reduce_add_sync(kAll, x.a >> 16),
+                      __reduce_add_sync(kAll, x.b & 0xffffu), __reduce_add_sync(kAll, x.b >> 16)};
   __syncthreads();                         // (the warps' sums of the scan before are read)
   if (lane == 31) {
     s_warp[warp] = mine;
     s_warp[warp].a = sum.a, s_warp[warp].b = sum.b;
   }
   __syncthreads();
-  const Warp w = lane < warps ? s_warp[lane] : Warp{0, 0, 0, 0, 0, 0};
+  const WarpSums w = lane < warps ? s_warp[lane] : WarpSums{0, 0, 0, 0, 0, 0};
   const Two all = inclusive(Two{w.a, w.b});
   const unsigned a0 = __shfl_sync(kAll, all.a, warp > 0 ? warp - 1 : 0);
   const unsigned b0 = __shfl_sync(kAll, all.b, warp > 0 ? warp - 1 : 0);
@@ -343,7 +346,7 @@ cudaError_t launch(K kernel, const GdnPoolArgs& p, const GdnPlanArgs& a, long lo
   while (ctas < kMaxCtas && words > (long long)ctas * threads * 2) ctas *= 2;
   while (threads < kMostThreads && words > (long long)ctas * threads * 4) threads *= 2;
   const size_t smem = shared_bytes(a.B);
-  if (smem > 48 * 1024) {
+  if (smem > kUnasked) {
     const cudaError_t e = set_smem_once(kernel, (int)shared_bytes(kGdnMaxRequests), done);
     if (e != cudaSuccess) return e;
   }
@@ -373,7 +376,7 @@ cudaError_t gdn_launch_page_plan(const GdnPoolArgs& p, const GdnPlanArgs& a, cud
   if (words <= pages::kOneCluster)
     return pages::launch(pages::gdn_page_plan_kernel<pages::kAll>, p, a, words, &done[0], stream);
   const size_t smem = pages::shared_bytes(a.B);
-  if (smem > 48 * 1024) {
+  if (smem > pages::kUnasked) {
     const int most = (int)pages::shared_bytes(kGdnMaxRequests);
     cudaError_t e = set_smem_once(pages::gdn_page_plan_kernel<pages::kOutputs>, most, &done[1]);
     if (e == cudaSuccess) e = set_smem_once(pages::gdn_page_plan_kernel<pages::kState>, most, &done[2]);
