@@ -854,7 +854,8 @@ __global__ void __launch_bounds__(kThreads, kRaceCtasPerSm) gdn_verify_race_kern
     if (a.logprobs) {
       float lp = 0.0f;
       if (given_id >= 0)
-        lp = ((k < accepted ? s_x[k] : logit) - s_row[k].m) * scale - kLn2 * log2f(s_row[k].z);
+        lp = scaled_difference(k < accepted ? s_x[k] : logit, s_row[k].m, scale) -
+             kLn2 * log2f(s_row[k].z);   // (an accepted draft's logit may be far below)
       a.logprobs[to] = lp;
     }
   }
