@@ -25,6 +25,7 @@
 // Part of logprobs.cu, whose error word it uses.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "common.cuh"
@@ -61,11 +62,12 @@ struct Plan {
   int each, more;                          // granules of a part, and the first `more` have one more
   int pieces;                              // slices of a sequence's race
   int slice;                               // logits of a slice
+  long long room;                          // slices that the workspace holds, of all sequences
   float4* stats;                           // [row + part]: m, z, granule of the largest; where
                                            // the first pass draws: m, z, index (greedy:
                                            // granule), w / E
   float4* best;                            // [B][pieces]: w / E, its index and its logit
-  int* done;                               // [B]
+  int* done;                               // [B] (neither is there without drafts)
 };
 
 // A row's largest logit (m = -inf: none above it), z, and the first granule that holds it.
@@ -884,13 +886,16 @@ Plan plan_of(int B, int T, int V, int bf16, bool draft) {
   pieces = pieces < 1 ? 1 : pieces < pieces_most ? pieces : pieces_most;
   p.slice = ((V + pieces - 1) / pieces + 15) & ~15;
   p.pieces = (V + p.slice - 1) / p.slice;
+  // room for the slices of any smaller batch and vocabulary too (456 / B goes down in steps), so that
+  // what a larger call needs is never less
+  p.room = T ? std::min((long long)std::max(kRaceCtas, B), (long long)B * pieces_most) : 0;
   return p;
 }
 size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t stats_bytes(const Plan& p, int B) {
   return up(sizeof(float4) * ((size_t)p.rows * B + p.parts));
 }
-size_t best_bytes(const Plan& p, int B) { return up(sizeof(float4) * (size_t)p.pieces * B); }
+size_t best_bytes(const Plan& p) { return up(sizeof(float4) * (size_t)p.room); }
 
 template <typename T>
 cudaError_t launch(const GdnVerifyArgs& a, const Plan& p, cudaStream_t stream) {
@@ -911,7 +916,7 @@ cudaError_t launch(const GdnVerifyArgs& a, const Plan& p, cudaStream_t stream) {
 
 size_t gdn_verify_tokens_bytes(int B, int T, int V, int bf16, int draft) {
   const verify::Plan p = verify::plan_of(B, T, V, bf16, draft);
-  return verify::stats_bytes(p, B) + verify::best_bytes(p, B) + verify::up(sizeof(int) * (size_t)B);
+  return verify::stats_bytes(p, B) + verify::best_bytes(p) + (T ? verify::up(sizeof(int) * (size_t)B) : 0);
 }
 
 cudaError_t gdn_launch_verify_tokens(const GdnVerifyArgs& a, cudaStream_t stream) {
@@ -919,6 +924,6 @@ cudaError_t gdn_launch_verify_tokens(const GdnVerifyArgs& a, cudaStream_t stream
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.stats = reinterpret_cast<float4*>(ws);
   p.best = reinterpret_cast<float4*>(ws + verify::stats_bytes(p, a.B));
-  p.done = reinterpret_cast<int*>(ws + verify::stats_bytes(p, a.B) + verify::best_bytes(p, a.B));
+  p.done = reinterpret_cast<int*>(ws + verify::stats_bytes(p, a.B) + verify::best_bytes(p));
   return a.bf16 ? verify::launch<__nv_bfloat16>(a, p, stream) : verify::launch<float>(a, p, stream);
 }

@@ -685,6 +685,8 @@ gdn_status gdn_page_release(const gdn_page_pool* pool, int32_t batch, const int3
  * distribution (a NaN or +inf logit, nothing but -inf) accepts nothing; where it is the next
  * token's, p or q, next is -1 and its logprob 0.
  *   workspace     gdn_verify_tokens_workspace_size() bytes (0 for invalid sizes), 16-byte aligned.
+ *                 The size never falls as batch, drafts or vocabulary grow, nor with draft_logits, so
+ *                 the largest call's serves the smaller ones (of its dtype).
  * T <= 64.  Decisions are those of exact arithmetic but where two sides agree to 2^-18; a weight
  * below 2^-126 of its row's largest probability counts as 0.
  */
