@@ -14,7 +14,9 @@
 // so without drafts the first pass runs it as it goes and the second only joins.
 // A warp keeps the best w / E of its elements so far; an element is looked at closer only if
 // w > best E, nearly, so there is a division where the best changes and none elsewhere.  Where two
-// are within 2^-16 of each other they are compared in 64 bits, and so is a u near its border.
+// lanes' or slices' best are within 2^-16 of each other they are compared in 64 bits, and so is a u near
+// its border.  m, z and a lane's own weights are in 32 bits: p and q are right to 2^-20 or so of
+// themselves, and after a refusal p - q to that of p + q, however small it is.
 //
 // Bound by memory where the batch is large: 64 sequences of 4 drafts over 248320 logits in bf16 66 us
 // (250 MB of rows in 42 us, 5.9 TB/s, then 90 MB), 128 draws of 151936 24 us (117 MB); by instructions

@@ -662,8 +662,8 @@ gdn_status gdn_page_release(const gdn_page_pool* pool, int32_t batch, const int3
  *                w = max(p_a - q_a, 0) where draft a = accepted < m was refused,
  *                w = p_m where all were accepted
  * (the first of exponential clocks with rates w rings at i with probability w_i / sum w).
- * A refused draft without any w_i > 0 (p = q but for rounding) is itself the next token; where all
- * were accepted and no clock of a w_i > 0 rings, next is -1.
+ * A refused draft without any w_i > 0 whose clock rings is itself the next token; where all were
+ * accepted and no clock of a w_i > 0 rings, next is -1.
  *   target_logits [B, T + 1, V] in dtype, rows target_row_stride elements apart (>= V); any
  *                 alignment of the element's own.  Row j is of the token behind draft j - 1.
  *   draft_ids     [B, T] device int32: drafts up to the first negative id; the rest of the row is
@@ -687,8 +687,12 @@ gdn_status gdn_page_release(const gdn_page_pool* pool, int32_t batch, const int3
  *   workspace     gdn_verify_tokens_workspace_size() bytes (0 for invalid sizes), 16-byte aligned.
  *                 The size never falls as batch, drafts or vocabulary grow, nor with draft_logits, so
  *                 the largest call's serves the smaller ones (of its dtype).
- * T <= 64.  Decisions are those of exact arithmetic but where two sides agree to 2^-18; a weight
- * below 2^-126 of its row's largest probability counts as 0.
+ * T <= 64.  Drafts are accepted as in exact arithmetic but where u and p / q agree to 2^-18.  The
+ * weights are made from p and q with an error of 2^-20 of each, and 2^-22 more for every binary order
+ * that it lies below its row's largest; next is that of exact arithmetic but where two w / clock are
+ * as close as that leaves them.  The difference p - q of nearly equal rows keeps that error: where
+ * only rounding tells them apart, next may be any token whose p - q is within it of 0.  A weight below
+ * 2^-126 of its row's largest probability counts as 0.
  */
 size_t gdn_verify_tokens_workspace_size(int32_t batch, int32_t num_drafts, int32_t vocab,
                                         gdn_dtype dtype, int32_t with_draft_logits);

@@ -1,5 +1,6 @@
-"""gdn_verify_tokens where its numbers are far apart: log probabilities of accepted drafts whose
-logits lie further below the row's largest than fp32 reaches."""
+"""gdn_verify_tokens where its numbers are far apart or very close: log probabilities of accepted
+drafts whose logits lie further below the row's largest than fp32 reaches, and the token behind a
+refusal where the draft's probabilities are nearly the target's."""
 import pytest
 import torch
 
@@ -42,3 +43,39 @@ def test_log_probabilities_of_far_drafts(gdn, scale, dtype):
     want = (float(x[0, 0, 1]) - float(x[0, 0, 0])) * scale   # (z is 1)
     assert abs(float(logprobs[0, 0]) - want) <= 2.0 ** -22 * abs(want)
     assert abs(float(logprobs[0, 1])) <= 4e-6
+
+
+@pytest.mark.parametrize("dtype,close", [(torch.float32, 1e-2), (torch.float32, 1e-4),
+                                         (torch.bfloat16, 1e-2), (torch.bfloat16, 1e-4)])
+@pytest.mark.parametrize("v", [3000, 50021])
+def test_draft_probabilities_close_to_the_targets(gdn, v, dtype, close):
+    """A probability is off by 2^-20 of itself (its row's sum, the exponential) and 2^-22 more for every
+    binary order below its row's largest (the exponent's rounding: 2^-24 each of the difference, the
+    scale and their product, times ln 2), whatever p - q leaves of it: the token given is within that
+    of the first."""
+    b = 48
+    g = torch.Generator(device="cuda").manual_seed(v)
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=g, device="cuda")
+
+    x = (3 * randn(b, 2, v)).to(dtype)
+    y = (x[:, :1].float() + close * randn(b, 1, v)).to(dtype)
+    scale = torch.tensor([1.0, 1.25, 0.7], device="cuda").repeat(b // 3)
+    clocks = torch.empty(b, v, device="cuda").exponential_(generator=g)
+    logs = [torch.log_softmax(z[:, 0].double() * scale.double()[:, None], 1) for z in (x, y)]
+    (p, q), below = [z.exp() for z in logs], [(z.amax(1, keepdim=True) - z) / 0.6931471805599453 for z in logs]
+    ids = (q - p).argmax(1, keepdim=True).to(torch.int32)
+    if not bool((p != q).any(1).all()):
+        pytest.skip("rounded to the same rows")
+    ratio = (p / q).gather(1, ids.long())[:, 0]
+    tokens, accepted, _ = _run(gdn, x, clocks=clocks, draft_logits=y, draft_ids=ids, scale=scale,
+                               accept_u=torch.full((b, 1), 1 - 2.0 ** -24, device="cuda"))
+    refused = ratio < 1 - 2.0 ** -17
+    assert int(refused.sum()) >= b // 2 and not bool(accepted[refused].any())
+    race = (p - q) / clocks.double()
+    slack = (2.0 ** -20 + 2.0 ** -22 * torch.maximum(*below)) * (p + q) / clocks.double()
+    got = tokens[:, :1].long()
+    assert bool((got[refused] >= 0).all())
+    good = (race + slack).gather(1, got.clamp(min=0))[:, 0] >= (race - slack).amax(1)
+    assert bool(good[refused].all())
