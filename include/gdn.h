@@ -672,7 +672,8 @@ gdn_status gdn_page_release(const gdn_page_pool* pool, int32_t batch, const int3
  *   draft_logits  [B, T, V] in dtype, rows draft_row_stride apart, or NULL.
  *   accept_u      [B, T] fp32, uniform on [0, 1); NULL when T is 0.
  *   clocks        [B, V] fp32, independent exponential numbers; entries that are not above 0
- *                 (zero, negative, NaN) never ring, those below 2^-126 ring as 2^-126.
+ *                 (zero, negative, NaN) and infinite ones never ring, those below 2^-126 ring as
+ *                 2^-126; a w / clock below 2^-126 may count as 0.
  *   scale         [B] fp32 inverse temperatures, or NULL (= 1).  +inf: greedy: a draft is accepted
  *                 if it is the largest logit (the lowest id of equal ones), next is the largest, no
  *                 random number counts.  Else within [2^-64, 2^64]; any other value (negative,

@@ -1,5 +1,5 @@
 """gdn_verify_tokens with clocks at the ends of their range, against the definition in 64 bits: a
-clock between 0 and 2^-126 rings as one of 2^-126.
+clock between 0 and 2^-126 rings as one of 2^-126; zero, negative, NaN and infinite ones never.
 The weights are chosen so that the first clock is ahead of every other by a tenth or more (the
 kernel's weights are right to 2^-16 and better), so tokens are equal."""
 import math
@@ -120,3 +120,30 @@ def test_tiny_clocks_behind_drafts(gdn, v, dtype, drafts):
             w = (w - q * float(w.sum())).clamp(min=0)
         want = _first(w, e[i])
         assert tokens[i].tolist() == ([want, -1] if refused else [3, want]), i
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("v", [600, 20001])
+@pytest.mark.parametrize("clock", [0.0, -1.0, math.nan, INF])
+def test_clocks_that_never_ring(gdn, clock, v, dtype):
+    """Rows in which nothing rings: without drafts and behind accepted ones no token (and a log
+    probability of 0); a refused draft is the token itself.  One clock among them decides."""
+    g = torch.Generator(device="cuda").manual_seed(v)
+    x = torch.randn(4, 2, v, generator=g, device="cuda").to(dtype)
+    e = torch.full((4, v), clock, device="cuda")
+    e[2:, v // 3] = 3.0
+    tokens, _, logprobs = _run(gdn, x[:, :1].contiguous(), e)
+    assert tokens[:, 0].tolist() == [-1, -1, v // 3, v // 3]
+    assert logprobs[:2, 0].tolist() == [0.0, 0.0] and bool((logprobs[2:] < 0).all())
+    ids = torch.full((4, 1), 5, device="cuda", dtype=torch.int32)
+    u = torch.tensor([[0.0], [1.0], [0.0], [1.0]], device="cuda")
+    y = torch.full((4, 1, v), -20.0, device="cuda", dtype=dtype)
+    y[:, :, 5] = 20.0                                     # p / q is below 1
+    for draft in (None, y):
+        tokens, accepted, logprobs = _run(gdn, x, e, draft_ids=ids, draft_logits=draft, accept_u=u)
+        assert accepted.tolist() == [1, 0, 1, 0]
+        assert tokens.tolist() == [[5, -1], [5, -1], [5, v // 3], [v // 3, -1]]
+        assert float(logprobs[0, 1]) == 0.0 and bool((logprobs[:, 0] < 0).all())
+        want = torch.log_softmax(x[1, 0].double(), 0)[5]
+        # 4e-6 + 2^-22 (|lse| + |x|), lse at most 10.5 and |x| below 6
+        assert abs(float(logprobs[1, 0]) - float(want)) <= 1e-5
