@@ -682,9 +682,12 @@ gdn_status gdn_page_release(const gdn_page_pool* pool, int32_t batch, const int3
  *   accepted      [B] int32.
  *   logprobs      [B, T + 1] fp32 or NULL: log p_j of each token given (at scale 1 for greedy
  *                 sequences), 0 behind them.
- * Only the rows of the drafts and of the token behind them are read.  A row that is no
- * distribution (a NaN or +inf logit, nothing but -inf) accepts nothing; where it is the next
- * token's, p or q, next is -1 and its logprob 0.
+ * Only the rows of the drafts and of the token behind them count, and of greedy sequences the
+ * target's alone (all rows may be read, whatever they hold).  Such a row that is no distribution (a
+ * NaN or +inf logit, nothing but -inf) accepts nothing; where it is the next token's, p or q, next is
+ * -1 and its logprob 0.  How the sums are cut follows the whole call: the last bits of a sequence's
+ * logprobs, and decisions as close as those below, may change with the batch around it; the same
+ * call gives the same bits.
  *   workspace     gdn_verify_tokens_workspace_size() bytes (0 for invalid sizes), 16-byte aligned.
  *                 The size never falls as batch, drafts or vocabulary grow, nor with draft_logits, so
  *                 the largest call's serves the smaller ones (of its dtype).

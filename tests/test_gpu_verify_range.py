@@ -79,3 +79,27 @@ def test_draft_probabilities_close_to_the_targets(gdn, v, dtype, close):
     assert bool((got[refused] >= 0).all())
     good = (race + slack).gather(1, got.clamp(min=0))[:, 0] >= (race - slack).amax(1)
     assert bool(good[refused].all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("v", [70, 9001])
+def test_rows_that_do_not_count(gdn, v, dtype):
+    """NaN in the draft's rows of greedy sequences, behind the last draft and in rows of sequences
+    that are left out change nothing."""
+    b, t = 9, 3
+    g = torch.Generator(device="cuda").manual_seed(v)
+    x = (3 * torch.randn(b, t + 1, v, generator=g, device="cuda")).to(dtype)
+    y = (x[:, :t].float() + 0.5 * torch.randn(b, t, v, generator=g, device="cuda")).to(dtype)
+    ids = x[:, :t].float().argmax(-1).to(torch.int32)
+    ids[3:6, 1] = -1                                     # one draft each
+    kw = dict(clocks=torch.empty(b, v, device="cuda").exponential_(generator=g), draft_ids=ids,
+              accept_u=torch.rand(b, t, generator=g, device="cuda"),
+              scale=torch.tensor([float("inf"), 1.0, -1.0] * 3, device="cuda"))
+    want = _run(gdn, x, draft_logits=y, **kw)
+    spoilt_x, spoilt_y = x.clone(), y.clone()
+    spoilt_y[0::3] = float("nan")
+    spoilt_x[2::3], spoilt_y[2::3] = float("nan"), float("nan")
+    spoilt_x[3:6, 2:], spoilt_y[3:6, 1:] = float("nan"), float("nan")
+    for a, z in zip(want, _run(gdn, spoilt_x, draft_logits=spoilt_y, **kw)):
+        assert torch.equal(a, z)
+    assert bool((want[1][0::3] == torch.tensor([3, 1, 3], device="cuda")).all())
