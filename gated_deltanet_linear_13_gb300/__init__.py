@@ -6,8 +6,9 @@ This module only marshals torch tensors into pointers and sizes: every step of t
 in the CUDA kernels of ``libgdn.so``.  It checks shapes, dtypes, devices and contiguity
 before handing raw pointers to the library (a wrong size would otherwise let a kernel read
 past a buffer).  The usual call of the serving step's operators is checked and marshalled by a
-native part (``csrc/marshal.cpp``), whatever it leaves by the checks here.  If ``libgdn.so`` is
-missing loading it fails: there is no fallback.
+native part (``csrc/marshal.cpp``), whatever it leaves by the checks here, and all of it where that
+part is missing or belongs to another torch.  If ``libgdn.so`` is missing loading it fails: there is
+no fallback.
 """
 from __future__ import annotations
 
@@ -186,17 +187,30 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     return L
 
 
-_native = None
+class _NoNative:
+    """In the place of the binding's native part: leaves every call to the checks in Python."""
+
+    @staticmethod
+    def qk_norm_rope(*args):
+        return None
+
+    page_plan = page_release = verify_tokens = qk_norm_rope
+
+
+_native = _NoNative
 
 
 def _bind_marshal(L: ctypes.CDLL) -> None:
-    """The binding's native part (csrc/marshal.cpp), on the functions of this library."""
+    """The binding's native part (csrc/marshal.cpp), on the functions of this library, if it is
+    there and was built against this torch (whose tensors it reads)."""
     global _native
+    _native = _NoNative
     try:
         from . import _marshal as m
-    except ImportError as e:
-        raise OSError("the binding's native part (_marshal.so) cannot be loaded: build it with "
-                      "`python -m gated_deltanet_linear_13_gb300.build_lib`") from e
+    except ImportError:
+        return
+    if getattr(m, "torch_version", None) != str(torch.__version__):
+        return
     m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
              (L.gdn_qk_norm_rope, L.gdn_page_plan, L.gdn_page_release, L.gdn_verify_tokens)),
            getattr(torch._C, "_cuda_getCurrentRawStream", None))

@@ -71,7 +71,8 @@ def build_marshal(force: bool = False) -> str:
     lib = os.path.join(base, "lib")
     tmp = MARSHAL + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DGDN_TORCH_VERSION="{torch.__version__}"']
     cmd += [x for p in include for x in ("-isystem" if p != INCLUDE else "-I", p)]
     cmd += [MARSHAL_SRC, "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -307,4 +307,9 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__marshal() {
+  PyObject* m = PyModule_Create(&kModule);
+  // (the binding leaves a module of another torch alone)
+  if (m && PyModule_AddStringConstant(m, "torch_version", GDN_TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}
