@@ -111,6 +111,18 @@ void* stream_of(PyObject* o, const at::Device& device) {
   return reinterpret_cast<void*>(x);
 }
 
+// Calls the library with the interpreter's lock given up: a launch waits where the queue is full, and
+// other threads, and what the stream's host functions need of them, go on meanwhile.  (The arguments
+// are made before, under the lock; the caller's frame keeps the tensors.)
+template <typename F, typename... A>
+gdn_status unlocked(F* f, A... args) {
+  struct Unlock {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlock() { PyEval_RestoreThread(state); }
+  } unlock;
+  return f(args...);
+}
+
 // (the body's C++ exceptions end here)
 template <typename F>
 PyObject* guarded(F&& body) {
@@ -177,9 +189,9 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* x, Py_ssize_t count) {
     } else {
       need(!none(x[5]) && none(x[11]) && none(x[13]) && none(x[14]));
     }
-    return p_qk_norm_rope(
-        size32(n), size32(Hq), size32(H), size32(D), dt, q.data_ptr(), token, head, k.data_ptr(),
-        token_stride(k, type, n, H, D, dev), (const float*)dense_or_null(x[6], at::kFloat, {D}, dev),
+    return unlocked(
+        p_qk_norm_rope, size32(n), size32(Hq), size32(H), size32(D), dt, q.data_ptr(), token, head,
+        k.data_ptr(), token_stride(k, type, n, H, D, dev), (const float*)dense_or_null(x[6], at::kFloat, {D}, dev),
         (const float*)dense_or_null(x[7], at::kFloat, {D}, dev), (float)real(x[8]), positions, &rope,
         out.data_ptr(), token_stride(out, type, n, Hq, D, dev),
         dense_or_null(x[5], type, {n, H, D}, dev), cached ? &cache : nullptr, v, v_stride, slots,
@@ -215,15 +227,16 @@ PyObject* page_plan(PyObject*, PyObject* const* x, Py_ssize_t count) {
     int64_t capacity = INT32_MAX;          // (nothing to be written a token)
     for (PyObject* o : {x[3], x[2]})
       if (!none(o)) need(tensor(o).dim() == 1), capacity = tensor(o).size(0);
-    return p_page_plan(&pool, size32(B), (const int32_t*)dense_or_null(x[12], at::kInt, {B}, dev),
-                       (const int32_t*)dense(kv, at::kInt, {B}, dev),
-                       (const int32_t*)dense(x[1], at::kInt, {B}, dev), size32(capacity), small(x[13]),
-                       (int32_t*)dense_or_null(x[2], at::kInt, {capacity}, dev),
-                       (int32_t*)dense_or_null(x[3], at::kInt, {capacity}, dev),
-                       (int32_t*)dense_or_null(x[4], at::kInt, {B + 1}, dev),
-                       (int32_t*)dense_or_null(x[5], at::kInt, {B}, dev),
-                       (int32_t*)dense_or_null(x[6], at::kInt, {B, pool.max_pages}, dev),
-                       stream_of(x[14], dev));
+    return unlocked(p_page_plan, &pool, size32(B),
+                    (const int32_t*)dense_or_null(x[12], at::kInt, {B}, dev),
+                    (const int32_t*)dense(kv, at::kInt, {B}, dev),
+                    (const int32_t*)dense(x[1], at::kInt, {B}, dev), size32(capacity), small(x[13]),
+                    (int32_t*)dense_or_null(x[2], at::kInt, {capacity}, dev),
+                    (int32_t*)dense_or_null(x[3], at::kInt, {capacity}, dev),
+                    (int32_t*)dense_or_null(x[4], at::kInt, {B + 1}, dev),
+                    (int32_t*)dense_or_null(x[5], at::kInt, {B}, dev),
+                    (int32_t*)dense_or_null(x[6], at::kInt, {B, pool.max_pages}, dev),
+                    stream_of(x[14], dev));
   });
 }
 
@@ -237,8 +250,9 @@ PyObject* page_release(PyObject*, PyObject* const* x, Py_ssize_t count) {
     need(keep.dim() == 1);
     const int64_t B = keep.size(0);
     need(!none(x[6]) || B <= pool.num_rows);
-    return p_page_release(&pool, size32(B), (const int32_t*)dense_or_null(x[6], at::kInt, {B}, dev),
-                          (const int32_t*)dense(keep, at::kInt, {B}, dev), stream_of(x[7], dev));
+    return unlocked(p_page_release, &pool, size32(B),
+                    (const int32_t*)dense_or_null(x[6], at::kInt, {B}, dev),
+                    (const int32_t*)dense(keep, at::kInt, {B}, dev), stream_of(x[7], dev));
   });
 }
 
@@ -267,15 +281,14 @@ PyObject* verify_tokens(PyObject*, PyObject* const* x, Py_ssize_t count) {
     } else {
       need(none(x[4]) && none(x[5]) && none(x[6]));
     }
-    return p_verify_tokens(size32(B), size32(T), size32(V), dt, target.data_ptr(),
-                           row_stride(target, type, B, T + 1, V, dev), (const int32_t*)ids, draft,
-                           draft_stride, (const float*)u,
-                           (const float*)dense(x[3], at::kFloat, {B, V}, dev),
-                           (const float*)dense_or_null(x[7], at::kFloat, {B}, dev),
-                           (int32_t*)dense(x[1], at::kInt, {B, T + 1}, dev),
-                           (int32_t*)dense(x[2], at::kInt, {B}, dev),
-                           (float*)dense_or_null(x[8], at::kFloat, {B, T + 1}, dev),
-                           workspace.data_ptr(), workspace.nbytes(), stream_of(x[10], dev));
+    return unlocked(p_verify_tokens, size32(B), size32(T), size32(V), dt, target.data_ptr(),
+                    row_stride(target, type, B, T + 1, V, dev), (const int32_t*)ids, draft,
+                    draft_stride, (const float*)u, (const float*)dense(x[3], at::kFloat, {B, V}, dev),
+                    (const float*)dense_or_null(x[7], at::kFloat, {B}, dev),
+                    (int32_t*)dense(x[1], at::kInt, {B, T + 1}, dev),
+                    (int32_t*)dense(x[2], at::kInt, {B}, dev),
+                    (float*)dense_or_null(x[8], at::kFloat, {B, T + 1}, dev), workspace.data_ptr(),
+                    workspace.nbytes(), stream_of(x[10], dev));
   });
 }
 
