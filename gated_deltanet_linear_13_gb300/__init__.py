@@ -737,18 +737,19 @@ def _kv_cache(k_cache, v_cache, k_exp, v_exp):
     """(C struct, device) of a paged cache [num_pages, H, page_size, D]: bf16, or float8_e4m3fn
     codes with uint8 exponents [num_pages, H, page_size]."""
     dev, shape, dtype = k_cache.device, k_cache.shape, k_cache.dtype
-    if (dtype is torch.float8_e4m3fn and len(shape) == 4 and k_exp is not None and
-            v_exp is not None and v_cache.dtype is dtype and v_cache.shape == shape and
-            k_exp.dtype is torch.uint8 and v_exp.dtype is torch.uint8 and
+    if (dtype is torch.float8_e4m3fn and len(shape) == 4 and v_cache is not None and
+            k_exp is not None and v_exp is not None and v_cache.dtype is dtype and
+            v_cache.shape == shape and k_exp.dtype is torch.uint8 and v_exp.dtype is torch.uint8 and
             k_exp.shape == v_exp.shape == shape[:3] and
             dev == v_cache.device == k_exp.device == v_exp.device and dev.type == "cuda" and
             k_cache.is_contiguous() and v_cache.is_contiguous() and k_exp.is_contiguous() and
             v_exp.is_contiguous()):                  # the usual case at once
         return GdnKvCache(shape[0], shape[2], shape[1], shape[3], GDN_KV_E4M3, k_cache.data_ptr(),
                           v_cache.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr()), dev
-    if (dtype is torch.bfloat16 and len(shape) == 4 and k_exp is None and v_exp is None and
-            v_cache.dtype is dtype and v_cache.shape == shape and dev == v_cache.device and
-            dev.type == "cuda" and k_cache.is_contiguous() and v_cache.is_contiguous()):
+    if (dtype is torch.bfloat16 and len(shape) == 4 and v_cache is not None and k_exp is None and
+            v_exp is None and v_cache.dtype is dtype and v_cache.shape == shape and
+            dev == v_cache.device and dev.type == "cuda" and k_cache.is_contiguous() and
+            v_cache.is_contiguous()):
         return GdnKvCache(shape[0], shape[2], shape[1], shape[3], GDN_KV_BF16, k_cache.data_ptr(),
                           v_cache.data_ptr(), None, None), dev
     if dev.type != "cuda":
