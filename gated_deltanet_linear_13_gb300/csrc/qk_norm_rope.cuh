@@ -4,9 +4,9 @@
 // Per head vector x of D elements: y = x rsqrt(mean x^2 + eps) w, then each pair (a, b) of its
 // first r elements is turned by the angle w_p = position * frequency_p.  The angle is kept as a
 // phase in 2^64ths of a turn: position * step_p modulo 2^64 is one 64-bit product, exact for every
-// position (in 32 bits an angle of 10^6 radians is off by 0.03), and its upper 32 bits give cos and
-// sin to 2^-31 of a turn.  All in fp32, rounded once to what is stored; an 8-bit cache is
-// quantised from the fp32 keys.
+// position (in 32 bits an angle of 10^6 radians is off by 0.03); its upper 32 bits, rounded to a float,
+// give cos and sin to 2^-26 of a turn.  All in fp32, rounded once to what is stored; an 8-bit cache
+// is quantised from the fp32 keys.
 //
 // L lanes a vector, two runs of eight elements each (16 bytes of bf16): in the half layout a lane's
 // runs are the two halves of its pairs, otherwise they are neighbours, so a pair lies in one lane

@@ -19,7 +19,7 @@
 // themselves, and after a refusal p - q to that of p + q, however small it is.
 //
 // Bound by memory where the batch is large: 64 sequences of 4 drafts over 248320 logits in bf16 66 us
-// (250 MB of rows in 42 us, 5.9 TB/s, then 90 MB), 128 draws of 151936 24 us (117 MB); by instructions
+// (240 MB of rows in 42 us, 5.7 TB/s, then 90 MB), 128 draws of 151936 23 us (95 MB); by instructions
 // and exponentials next to it (a granule of a row 130 instructions a warp, sixteen exponentials a
 // lane).  By latency where it is small: one sequence of 3 drafts 11 us, of which the rows take 3.3,
 // the second kernel's start behind the first 1.8, statistics and decisions 1.3, a slice 1.8, the join
