@@ -210,6 +210,19 @@ __device__ __noinline__ double exact_race(const T* x, const T* y, const float* c
   return w / (double)fmaxf(clocks[i], kLeastClock);
 }
 
+// (x - mx) - (y - my), finite and of any size, as if rounded once: where x and y are alike far below
+// (masks of the type's lowest value) it is my - mx that is left (seldom, so out of line).
+__device__ __noinline__ double difference_of(double x, double mx, double y, double my) {
+  auto sum = [](double a, double b, double* lost) {
+    const double s = a + b, t = s - a;
+    *lost += (a - (s - t)) + (b - t);
+    return s;
+  };
+  double lost = 0.0;
+  const double xy = sum(x, -y, &lost), m = sum(my, -mx, &lost), all = sum(xy, m, &lost);
+  return all + lost;
+}
+
 // The race of one row pair, as a warp runs it: the same best in all lanes.
 template <typename T>
 struct Race {
@@ -668,9 +681,10 @@ __global__ void __launch_bounds__(kThreads, kRaceCtasPerSm) gdn_verify_race_kern
         good = u < r;
         // near the border, or where the exponents are rounded by much: in 64 bits
         if (fabsf(u - r) <= r * 0x1p-14f || !(size < 64.0f)) {
-          double far = ((double)xi - (double)px.m) * (double)scale;
-          if (a.draft) far -= ((double)yi - (double)s_row[a.T + 1 + t].m) * (double)scale;
-          good = (double)u < exp(far) / (double)z;
+          double far = (double)xi - (double)px.m;
+          if (a.draft)
+            far = yi == -INFINITY ? (double)INFINITY : difference_of(xi, px.m, yi, s_row[a.T + 1 + t].m);
+          good = (double)u < exp(far * (double)scale) / (double)z;
         }
       }
     }

@@ -103,3 +103,46 @@ def test_rows_that_do_not_count(gdn, v, dtype):
     for a, z in zip(want, _run(gdn, spoilt_x, draft_logits=spoilt_y, **kw)):
         assert torch.equal(a, z)
     assert bool((want[1][0::3] == torch.tensor([3, 1, 3], device="cuda")).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("low", ["lowest", -1e30, -3e4])
+def test_drafts_far_below_in_both_rows(gdn, low, dtype):
+    """A draft at the same far logit in the target's row and the draft's: p / q is what the rows'
+    largest logits (4 above 1, or 1 above 4, beside zeros) and sums leave."""
+    low = torch.finfo(dtype).min if low == "lowest" else low
+    v, us = 300, [0.0, 0.01, 0.04, 0.06, 0.9, 0.999]
+    x = torch.zeros(2 * len(us), 2, v, device="cuda", dtype=dtype)
+    y = torch.zeros(2 * len(us), 1, v, device="cuda", dtype=dtype)
+    x[:len(us), :, 7], y[:len(us), :, 7] = 4.0, 1.0
+    x[len(us):, :, 7], y[len(us):, :, 7] = 1.0, 4.0
+    x[..., 3], y[..., 3] = low, low
+    u = torch.tensor(us + us, device="cuda")[:, None]
+    tokens, accepted, _ = _run(
+        gdn, x, clocks=torch.ones(len(u), v, device="cuda"), draft_logits=y, accept_u=u,
+        draft_ids=torch.full((len(u), 1), 3, device="cuda", dtype=torch.int32))
+    # the same logit in both: p / q = sum e^y / sum e^x, 298 zeros in each
+    one, four = 298 + 2.718281828459045, 298 + 54.598150033144236
+    ratio = torch.tensor([one / four] * len(us) + [four / one] * len(us), dtype=torch.float64)
+    assert accepted.tolist() == (u[:, 0].cpu().double() < ratio).int().tolist()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale", [1.0, 3.0, 2.0 ** -3])
+def test_lowest_values_with_far_maxima(gdn, scale, dtype):
+    """The same where the largest logits alone decide: one logit of hundreds, the rest masked."""
+    low, v = torch.finfo(dtype).min, 40
+    cases = [(300.0, 299.0), (299.0, 300.0), (0.0, 2.0), (2.0, 0.0), (-5.0, 5.0), (640.0, 0.0)]
+    x = torch.full((len(cases), 2, v), low, device="cuda", dtype=dtype)
+    y = torch.full((len(cases), 1, v), low, device="cuda", dtype=dtype)
+    for i, (a, b) in enumerate(cases):
+        x[i, :, 5], y[i, :, 5] = a, b
+    u = torch.full((len(cases), 1), 0.5, device="cuda")
+    _, accepted, _ = _run(
+        gdn, x, clocks=torch.ones(len(cases), v, device="cuda"), draft_logits=y, accept_u=u,
+        draft_ids=torch.full((len(cases), 1), 3, device="cuda", dtype=torch.int32),
+        scale=torch.full((len(cases),), scale, device="cuda"))
+    # p / q = e^(scale (b - a)), a and b as the type holds them (299 is 300 in bf16)
+    held = zip(x[:, 0, 5].tolist(), y[:, 0, 5].tolist())
+    want = [int(0.5 < 2.718281828459045 ** (scale * (b - a))) for a, b in held]
+    assert accepted.tolist() == want
