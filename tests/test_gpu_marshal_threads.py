@@ -1,8 +1,10 @@
 """Other Python threads run while a call of the binding's native part launches (a launch waits where
 the queue is full): the library's functions are replaced by one that sleeps."""
 import ctypes
+import os
 import shutil
 import subprocess
+import sys
 import threading
 import time
 
@@ -10,6 +12,7 @@ import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture
@@ -63,3 +66,40 @@ def test_threads_run_beside_a_launch(gdn):
     finally:
         over.set()
         thread.join()
+
+
+def test_threads_call_at_once():
+    """Two threads with a stream, tensors and a workspace each, calling side by side: the results of
+    the same calls one after the other."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from test_gpu_step_streams import Step
+    import gated_deltanet_linear_13_gb300 as gdn
+    from gated_deltanet_linear_13_gb300 import build_lib
+    build_lib.build()
+    gdn.load_library()
+
+    def run(step, stream, rounds):
+        with torch.cuda.stream(stream):
+            for _ in range(rounds):
+                step.plan()
+                step.rotate()
+                step.verify()
+                step.release()
+
+    wants, steps = ([Step(gdn, seed) for seed in (3, 4)] for _ in range(2))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for step in wants:
+        run(step, torch.cuda.current_stream(), 300)
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=run, args=(s, t, 300)) for s, t in zip(steps, streams)]
+    for thread in threads:
+        thread.start()
+    for thread in threads:
+        thread.join()
+    torch.cuda.synchronize()
+    assert gdn.gdn_get_device_error() == 0
+    for want, step in zip(wants, steps):
+        for a, b in zip(want.state(), step.state()):
+            assert torch.equal(a, b)

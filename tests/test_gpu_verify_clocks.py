@@ -147,3 +147,35 @@ def test_clocks_that_never_ring(gdn, clock, v, dtype):
         want = torch.log_softmax(x[1, 0].double(), 0)[5]
         # 4e-6 + 2^-22 (|lse| + |x|), lse at most 10.5 and |x| below 6
         assert abs(float(logprobs[1, 0]) - float(want)) <= 1e-5
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("v", [1, 9, 513, 4097, 30001])
+@pytest.mark.parametrize("order", ["mixed", "rising", "falling"])
+def test_ties_go_to_the_lower_id(gdn, order, v, dtype):
+    """Whole logits and clocks that are powers of two: w / E of two tokens is the same number or
+    apart by 7% and more (e^2 and 8 are the closest of e^k and a power of two, k = 1 .. 5)."""
+    b, t = 12, 1
+    g = torch.Generator(device="cuda").manual_seed(v)
+    x = torch.randint(-3, 3, (b, t + 1, v), generator=g, device="cuda").to(dtype)
+    if order != "mixed":
+        x = x.sort(-1, descending=order == "falling").values
+    e = 2.0 ** torch.randint(-2, 3, (b, v), generator=g, device="cuda").float()
+    ids = torch.randint(0, v, (b, 1), generator=g, device="cuda", dtype=torch.int32)
+    u = torch.tensor([0.0, 2.0] * (b // 2), device="cuda")[:, None]
+
+    def first(row, i, never=-1):
+        w = torch.exp(x[i, row].double() - x[i, row].double().max())
+        if never >= 0:
+            w[never] = 0.0
+        race = w / e[i].double()
+        return int((race == race.max()).nonzero()[0, 0]) if float(race.max()) > 0 else never
+
+    tokens, _, _ = _run(gdn, x[:, :1].contiguous(), e)
+    assert tokens[:, 0].tolist() == [first(0, i) for i in range(b)]
+    tokens, accepted, _ = _run(gdn, x, e, draft_ids=ids, accept_u=u)
+    assert accepted.tolist() == [1, 0] * (b // 2)
+    for i in range(b):
+        drafted = int(ids[i, 0])
+        want = [drafted, first(1, i)] if i % 2 == 0 else [first(0, i, drafted), -1]
+        assert tokens[i].tolist() == want, i
