@@ -532,7 +532,7 @@ gdn_status gdn_token_logprobs(int32_t rows, int32_t vocab, gdn_dtype dtype, cons
  * cache, the write of keys and values to their slots (as gdn_kv_cache_append would, from the
  * unrounded keys).
  * Definition, per token i and head vector x of D elements, in fp32 and rounded once (elements
- * whose squares pass fp32's range make the vector's norm infinite):
+ * whose squares pass fp32's range make the vector's norm infinite, squares below it count as 0):
  *     y = x / sqrt(mean(x^2) + eps) * weight          (y = x where the weight is NULL)
  *     pair p of the first rotary_dim elements, (a, b) = (y_p, y_{p + rotary_dim/2}) in the half
  *     layout, (y_2p, y_{2p+1}) in the interleaved one:
